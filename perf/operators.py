@@ -142,9 +142,9 @@ def _views(buf, off, sizes):
 
 
 def _control(dev):
-    """The control block's 64 bytes, T0 steps taken: words 0 norm, 1 factor, 2-3 step, 4-5 skipped, 6-7 and 8-9 the
-    bias corrections (fp64), 10 the rate's factor, 11 skip."""
-    c = torch.zeros(16, dtype=torch.int32, device=dev)
+    """The control block, T0 steps taken: words 0 norm, 1 factor, 2-3 step, 4-5 skipped, 6-7 and 8-9 the bias corrections
+    (fp64), 10 the rate's factor, 11 skip; from word 16 on room for partial sums."""
+    c = torch.zeros(16 + 2 * 2048, dtype=torch.int32, device=dev)
     f = c.view(torch.float32)
     f[1] = 1.0
     f[10] = 1.0
