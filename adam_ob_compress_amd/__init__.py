@@ -17,5 +17,8 @@ from ._native import (  # noqa: F401
     ob_lamb_warmup_step, ob_pack, ob_plan_create, ob_plan_read_timing, ob_plan_set_diagnostics,
     ob_plan_set_timing,
     ob_server_reduce, ob_status_str, ob_unpack,
+    OB_CONTROL_BYTES, OB_STATE_BLOCK, Tensors, adamw_hparams, control_create, control_fields, ob_adamw8_step,
+    ob_adamw_hparams, ob_adamw_step, ob_grad_norm, ob_state8_decode, ob_state8_encode, ob_tensors_create,
 )
+from .adamw import AdamW  # noqa: F401
 from .schedule import OneBitAdam, OneBitLamb, step_kind  # noqa: F401

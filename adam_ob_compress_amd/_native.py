@@ -19,6 +19,9 @@ OB_NOALLOC_SCRATCH_BYTES = 64 << 20
 OB_F32, OB_BF16, OB_F16 = 0, 1, 2
 OB_EF_PLAIN, OB_EF_EMA = 0, 1
 OB_ROUND_NEAREST, OB_ROUND_STOCHASTIC = 0, 1
+OB_STATE_BLOCK = 256
+OB_CONTROL_PARTIALS = 2048
+OB_CONTROL_BYTES = 64 + 8 * OB_CONTROL_PARTIALS
 (OB_KERNEL_CHUNK_SUMSQ, OB_KERNEL_COMPRESS, OB_KERNEL_DENSE, OB_KERNEL_SERVER_SUMSQ,
  OB_KERNEL_SERVER_APPLY, OB_KERNEL_UNPACK, OB_KERNEL_TRUST_RATIO, OB_KERNEL_LAMB_APPLY,
  OB_KERNEL_DIAG, OB_KERNEL_SCALE, OB_KERNEL_WORKER_COMPRESS, OB_KERNEL_WORKER_UPDATE) = range(12)
@@ -49,6 +52,19 @@ def hparams(lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, clip=0.0, ef_mode=OB_EF_P
             bias_correction=False, step=0, err_rounding=OB_ROUND_NEAREST, sr_seed=0) -> ob_hparams:
     return ob_hparams(lr, beta1, beta2, eps, clip, ef_mode, ef_beta, 1 if bias_correction else 0, step,
                       err_rounding, 0, sr_seed)
+
+
+class ob_adamw_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float), ("bias_correction", ctypes.c_int32),
+                ("step", ctypes.c_int64), ("rounding", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("sr_seed", ctypes.c_uint64)]
+
+
+def adamw_hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, bias_correction=True, step=1,
+                  rounding=OB_ROUND_NEAREST, sr_seed=0) -> ob_adamw_hparams:
+    return ob_adamw_hparams(lr, beta1, beta2, eps, weight_decay, 1 if bias_correction else 0, step, rounding, 0,
+                            sr_seed)
 
 
 _lib = None
@@ -88,6 +104,17 @@ def lib() -> ctypes.CDLL:
         "ob_plan_set_timing": (I32, [P, I32]),
         "ob_plan_set_diagnostics": (I32, [P, P, P]),
         "ob_plan_read_timing": (I32, [P, I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(I64)]),
+        "ob_tensors_create": (I32, [I64, P, P, P, P, P, ctypes.POINTER(P)]),
+        "ob_tensors_destroy": (I32, [P]),
+        "ob_tensors_count": (I64, [P]),
+        "ob_tensors_num_elements": (I64, [P]),
+        "ob_tensors_state_elems": (I64, [P]),
+        "ob_tensors_state_offset": (I64, [P, I64]),
+        "ob_grad_norm": (I32, [P, P, ctypes.c_float, ctypes.c_float, ctypes.POINTER(ob_adamw_hparams), P, P]),
+        "ob_adamw_step": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P, P]),
+        "ob_adamw8_step": (I32, [P, P, P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P, P]),
+        "ob_state8_encode": (I32, [I64, P, P, P, P, P, P, P]),
+        "ob_state8_decode": (I32, [I64, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -368,3 +395,211 @@ def ob_plan_read_timing(plan: Plan, kernel: int) -> tuple[float, int]:
     _check(lib().ob_plan_read_timing(plan.handle, kernel, ctypes.byref(ms), ctypes.byref(cnt)),
            "ob_plan_read_timing")
     return ms.value, cnt.value
+
+
+# ---- AdamW over lists of tensors ----
+
+class Tensors:
+    """Owner of an ob_tensors handle (destroyed with the object): a list of tensors by size and type."""
+
+    def __init__(self, handle: ctypes.c_void_p, sizes, g_dtypes, p_dtypes, device: torch.device):
+        self.handle = handle
+        self.sizes = tuple(sizes)
+        self.g_dtypes = tuple(g_dtypes)
+        self.p_dtypes = tuple(p_dtypes)
+        self.device = device
+        self._array = ctypes.c_void_p * len(self.sizes)
+        self.state_elems = int(lib().ob_tensors_state_elems(handle))
+
+    def __len__(self) -> int:
+        return len(self.sizes)
+
+    @property
+    def num_elements(self) -> int:
+        return int(lib().ob_tensors_num_elements(self.handle))
+
+    def state_offset(self, t: int) -> int:
+        return int(lib().ob_tensors_state_offset(self.handle, t))
+
+    def destroy(self):
+        if self.handle:
+            _check(lib().ob_tensors_destroy(self.handle), "ob_tensors_destroy")
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+    def _pointers(self, tensors, name, dtypes, others=None):
+        """The list's tensors as an array of device addresses; None (for others: where others has None) -> NULL."""
+        if len(tensors) != len(self.sizes):
+            raise ValueError(f"{name} must have {len(self.sizes)} tensors, got {len(tensors)}")
+        out = self._array()
+        index = self.device.index
+        for j, t in enumerate(tensors):
+            if t is None:
+                if others is not None and others[j] is not None:
+                    raise TypeError(f"{name}[{j}] must be a torch.Tensor")
+                continue
+            if (t.dtype is not dtypes[j] or t.numel() != self.sizes[j] or t.get_device() != index
+                    or not t.is_contiguous()):
+                self._refuse(t, f"{name}[{j}]", dtypes[j], self.sizes[j])
+            out[j] = t.data_ptr()
+        return out
+
+    def _refuse(self, t, name, dtype, numel):
+        _want(t, name, dtype, numel)
+        _dev(t, name)
+        raise ValueError(f"{name} must be on {self.device}, the list's device (got {t.device})")
+
+    def _flat(self, t, name, dtype, numel):
+        """Device address of a flat state buffer on the list's device (None -> NULL)."""
+        if t is None:
+            return None
+        _want(t, name, dtype, numel)
+        if t.get_device() != self.device.index or not t.is_contiguous():
+            self._refuse(t, name, dtype, numel)
+        return t.data_ptr()
+
+
+def _dtype_list(d, count, name):
+    ds = [d] * count if isinstance(d, torch.dtype) else list(d)
+    if len(ds) != count:
+        raise ValueError(f"{name} must have {count} entries, got {len(ds)}")
+    for x in ds:
+        if x not in _ERR_DTYPES:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x}")
+    return ds
+
+
+def _mult_array(x, count, name):
+    if x is None:
+        return None
+    x = [float(y) for y in x]
+    if len(x) != count:
+        raise ValueError(f"{name} must have {count} entries, got {len(x)}")
+    return (ctypes.c_float * count)(*x)
+
+
+def ob_tensors_create(sizes, g_dtype, p_dtype, lr_mults=None, wd_mults=None, device=None) -> Tensors:
+    """List of tensors of the given element counts; g_dtype and p_dtype: one torch dtype, or one per
+    tensor.  device: the list's GPU (the current one by default)."""
+    sizes = [int(s) for s in sizes]
+    T = len(sizes)
+    gd, pd = _dtype_list(g_dtype, T, "g_dtype"), _dtype_list(p_dtype, T, "p_dtype")
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"the list must be on the GPU (got {device}); there is no CPU path")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    codes = [(ctypes.c_int32 * T)(*[_ERR_DTYPES[x] for x in ds]) for ds in (gd, pd)]
+    h = ctypes.c_void_p()
+    with torch.cuda.device(device):
+        _check(lib().ob_tensors_create(T, (ctypes.c_int64 * T)(*sizes), *codes, _mult_array(lr_mults, T, "lr_mults"),
+                                       _mult_array(wd_mults, T, "wd_mults"), ctypes.byref(h)), "ob_tensors_create")
+    return Tensors(h, sizes, gd, pd, device)
+
+
+def control_create(device=None) -> torch.Tensor:
+    """A control block (ob_control and the norm's partial sums) for ob_grad_norm and the steps."""
+    c = torch.zeros(OB_CONTROL_BYTES // 4, dtype=torch.int32, device="cuda" if device is None else device)
+    c[10:11].view(torch.float32).fill_(1.0)
+    return c
+
+
+def control_fields(control: torch.Tensor) -> dict:
+    """The control block's fields as views of it (one element each): norm, grad_scale, step, skipped, bc1, bc2,
+    lr_scale, skip.  Reading a value waits for the GPU; lr_scale may be written."""
+    f, q, d = control.view(torch.float32), control.view(torch.int64), control.view(torch.float64)
+    return {"norm": f[0:1], "grad_scale": f[1:2], "step": q[1:2], "skipped": q[2:3], "bc1": d[3:4], "bc2": d[4:5],
+            "lr_scale": f[10:11], "skip": control[11:12]}
+
+
+def _control_ptr(tensors: Tensors, control):
+    return tensors._flat(control, "control", torch.int32, OB_CONTROL_BYTES // 4)
+
+
+def _list_stream(tensors: Tensors, stream):
+    if stream is None:
+        stream = torch.cuda.current_stream(tensors.device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp: ob_adamw_hparams | None = None,
+                 stream=None):
+    """Global norm of the gradients (a list; None: no gradient) and the factor that clips it to max_norm
+    (<= 0 or infinite: no clipping), into the control block; with hp also the step count and the bias
+    corrections of the step that follows."""
+    if control is None:
+        raise TypeError("control must be a torch.Tensor")
+    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
+    _check(lib().ob_grad_norm(tensors.handle, g, g_mult, max_norm, None if hp is None else ctypes.byref(hp),
+                              _control_ptr(tensors, control), _list_stream(tensors, stream)), "ob_grad_norm")
+
+
+def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None):
+    """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems."""
+    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
+    p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
+    N = tensors.state_elems
+    f = [tensors._flat(t, name, torch.float32, N) for t, name in ((master, "master"), (m, "m"), (v, "v"))]
+    _check(lib().ob_adamw_step(tensors.handle, g, p, *f, ctypes.byref(hp), _control_ptr(tensors, control),
+                               _list_stream(tensors, stream)), "ob_adamw_step")
+
+
+def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, v_scales, hp: ob_adamw_hparams,
+                   master=None, control=None, stream=None):
+    """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256."""
+    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
+    p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
+    N = tensors.state_elems
+    f = [tensors._flat(t, name, dtype, n) for t, name, dtype, n in
+         ((master, "master", torch.float32, N), (m_codes, "m_codes", torch.int8, N),
+          (m_scales, "m_scales", torch.float32, N // OB_STATE_BLOCK), (v_codes, "v_codes", torch.uint8, N),
+          (v_scales, "v_scales", torch.float32, N // OB_STATE_BLOCK))]
+    _check(lib().ob_adamw8_step(tensors.handle, g, p, *f, ctypes.byref(hp), _control_ptr(tensors, control),
+                                _list_stream(tensors, stream)), "ob_adamw8_step")
+
+
+def _state8_args(m, v, m_codes, m_scales, v_codes, v_scales):
+    """(n, device) of a conversion's tensors, checked; either moment may be None throughout."""
+    some = [t for t in (m, v, m_codes, m_scales, v_codes, v_scales) if t is not None]
+    if not some:
+        raise ValueError("neither moment is given")
+    lead = m if m is not None else v
+    if lead is None:
+        raise ValueError("codes and scales come with their fp32 moments")
+    n = lead.numel()
+    blocks = -(-n // OB_STATE_BLOCK)
+    for x, codes, scales, name, dtype in ((m, m_codes, m_scales, "m", torch.int8), (v, v_codes, v_scales, "v", torch.uint8)):
+        if (x is None) != (codes is None) or (x is None) != (scales is None):
+            raise ValueError(f"{name}, {name}_codes and {name}_scales come together")
+        _want(x, name, torch.float32, n)
+        _want(codes, f"{name}_codes", dtype, n)
+        _want(scales, f"{name}_scales", torch.float32, blocks)
+    for t in some:
+        if t.device != lead.device:
+            raise ValueError(f"all tensors must be on {lead.device} (got {t.device})")
+    return n
+
+
+def ob_state8_encode(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
+    """fp32 moments into the 8-bit format, rounded to nearest (m or v with its codes and scales: None)."""
+    n = _state8_args(m, v, m_codes, m_scales, v_codes, v_scales)
+    a = [_dev(t, name) for t, name in ((m, "m"), (v, "v"), (m_codes, "m_codes"), (m_scales, "m_scales"),
+                                       (v_codes, "v_codes"), (v_scales, "v_scales"))]
+    dev = (m if m is not None else v).device
+    with torch.cuda.device(dev):
+        _check(lib().ob_state8_encode(n, *a, _stream(stream)), "ob_state8_encode")
+
+
+def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
+    """The fp32 moments that 8-bit codes and scales stand for (m or v with its codes and scales: None)."""
+    n = _state8_args(m, v, m_codes, m_scales, v_codes, v_scales)
+    a = [_dev(t, name) for t, name in ((m_codes, "m_codes"), (m_scales, "m_scales"), (v_codes, "v_codes"),
+                                       (v_scales, "v_scales"), (m, "m"), (v, "v"))]
+    dev = (m if m is not None else v).device
+    with torch.cuda.device(dev):
+        _check(lib().ob_state8_decode(n, *a, _stream(stream)), "ob_state8_decode")

@@ -18,6 +18,11 @@ UNITS = [
     ("ob_kernels.hip", []),
     ("ob_noalloc.hip", []),
     ("ob_api.cpp", []),
+    ("ob_adamw.hip", ["-DOB_AW_G=0"]),         # steps over lists of tensors, by gradient type: fp32
+    ("ob_adamw.hip", ["-DOB_AW_G=1"]),         # bf16
+    ("ob_adamw.hip", ["-DOB_AW_G=2"]),         # fp16
+    ("ob_state8.hip", []),
+    ("ob_adamw_api.cpp", []),
 ]
 BUILD_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

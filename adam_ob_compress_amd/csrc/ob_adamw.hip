@@ -1,0 +1,405 @@
+// ob_adamw.hip -- AdamW steps over lists of tensors, with states in fp32 (k_adamw) and in 8 bits
+// (k_adamw8); compiled once per gradient type (OB_AW_G: 0 fp32, 1 bf16, 2 fp16).
+//
+// Both are one pass over the data: every array is read once and written once, so HBM bounds them.  A
+// work block takes part of one tensor; a lane takes four consecutive elements of a 256-element state block
+// per wave.  The tensors' addresses are launch arguments; parameters and gradients may start
+// at any element (vector loads of element alignment), states are aligned by their layout.
+#include "ob_state8.h"
+
+#include <type_traits>
+
+#ifndef OB_AW_G
+#error "OB_AW_G selects the gradient type"
+#endif
+
+namespace ob {
+namespace {
+
+// ------------------------------------------------------------------------------------------------
+// loads and stores of four consecutive elements at the alignment of one
+// ------------------------------------------------------------------------------------------------
+
+typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
+
+// type of elements: 0 fp32, 1 bf16, 2 fp16
+template <int D>
+__device__ __forceinline__ float widen16(uint32_t h)
+{
+    return D == 1 ? __uint_as_float(h << 16) : ErrF16::widen(h);
+}
+
+template <int D>
+__device__ __forceinline__ f4 load_any4(const void* __restrict__ p, int64_t i)
+{
+    if (D == 0) return __builtin_nontemporal_load(reinterpret_cast<const f4e*>(static_cast<const float*>(p) + i));
+    const u2e u = __builtin_nontemporal_load(reinterpret_cast<const u2e*>(static_cast<const uint16_t*>(p) + i));
+    f4 r;
+    r.x = widen16<D>(u.x & 0xffffu);
+    r.y = widen16<D>(u.x >> 16);
+    r.z = widen16<D>(u.y & 0xffffu);
+    r.w = widen16<D>(u.y >> 16);
+    return r;
+}
+
+template <int D>
+__device__ __forceinline__ float load_any1(const void* __restrict__ p, int64_t i)
+{
+    return D == 0 ? static_cast<const float*>(p)[i] : widen16<D>(static_cast<const uint16_t*>(p)[i]);
+}
+
+// fp32 x rounded to the type (nearest even, or by the 16 random bits r)
+template <int D, bool SR>
+__device__ __forceinline__ float round_to(float x, uint32_t r)
+{
+    if (D == 1) return SR ? ErrBF16::rounded_sr(x, r) : ErrBF16::rounded(x);
+    if (D == 2) return SR ? ErrF16::rounded_sr(x, r) : ErrF16::rounded(x);
+    return x;
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t bits16(float x)  // x already a value of the type
+{
+    return D == 1 ? __float_as_uint(x) >> 16 : ErrF16::bits(x);
+}
+
+template <int D>
+__device__ __forceinline__ void store_any4(void* __restrict__ p, int64_t i, f4 x)
+{
+    if (D == 0) {
+        __builtin_nontemporal_store(static_cast<f4e>(x), reinterpret_cast<f4e*>(static_cast<float*>(p) + i));
+        return;
+    }
+    u2e u;
+    u.x = bits16<D>(x.x) | (bits16<D>(x.y) << 16);
+    u.y = bits16<D>(x.z) | (bits16<D>(x.w) << 16);
+    __builtin_nontemporal_store(u, reinterpret_cast<u2e*>(static_cast<uint16_t*>(p) + i));
+}
+
+template <int D>
+__device__ __forceinline__ void store_any1(void* __restrict__ p, int64_t i, float x)
+{
+    if (D == 0)
+        static_cast<float*>(p)[i] = x;
+    else
+        static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(bits16<D>(x));
+}
+
+// Parameters by kind: i the element in the tensor, si the state index (of the master copy).
+template <int PK>
+struct Par {
+    static constexpr bool kMaster = PK == PK_MASTER_BF16 || PK == PK_MASTER_F16;
+    static constexpr int D = kMaster ? PK - 2 : PK;    // type behind p
+    static constexpr bool kRound = !kMaster && D != 0; // the parameter itself is held in 16 bits
+
+    static __device__ __forceinline__ f4 load4(const void* p, const float* master, int64_t i, int64_t si)
+    {
+        return kMaster ? ld4<true>(master, si) : load_any4<D>(p, i);
+    }
+    static __device__ __forceinline__ float load1(const void* p, const float* master, int64_t i, int64_t si)
+    {
+        return kMaster ? master[si] : load_any1<D>(p, i);
+    }
+    // x: new parameters in fp32; w: random words of the four elements (kRound with SR)
+    template <bool SR>
+    static __device__ __forceinline__ void store4(void* p, float* master, int64_t i, int64_t si, f4 x, const u4& w)
+    {
+        if (kMaster) st4<true>(master, si, x);
+        if (D != 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = round_to<D, SR && kRound>(x[k], w.x[k] >> 16);
+        }
+        store_any4<D>(p, i, x);
+    }
+    template <bool SR>
+    static __device__ __forceinline__ void store1(void* p, float* master, int64_t i, int64_t si, float x, uint32_t w)
+    {
+        if (kMaster) master[si] = x;
+        store_any1<D>(p, i, round_to<D, SR && kRound>(x, w >> 16));
+    }
+};
+
+// What a block needs besides its item: from the arguments or the control block.
+struct Step {
+    float scale;
+    double lr, wd, bc1, bc2;
+    uint64_t t;
+    bool skip;
+};
+
+__device__ __forceinline__ Step step_of(const AdamWParams& ap, const ListTensor& tn)
+{
+    Step s;
+    s.scale = 1.0f;
+    s.lr = ap.lr * static_cast<double>(tn.lr_mult);
+    s.wd = ap.wd * static_cast<double>(tn.wd_mult);
+    s.bc1 = ap.bc1;
+    s.bc2 = ap.bc2;
+    s.t = ap.step;
+    s.skip = false;
+    if (ap.control) {
+        s.scale = ap.control->grad_scale;
+        s.lr *= static_cast<double>(ap.control->lr_scale);
+        if (ap.bias_correction) {
+            s.bc1 = ap.control->bc1;
+            s.bc2 = ap.control->bc2;
+        }
+        s.t = static_cast<uint64_t>(ap.control->step);
+        s.skip = ap.control->skip != 0;
+    }
+    return s;
+}
+
+constexpr uint64_t kParStream = uint64_t(1) << 63;  // the counter's top bit: words for 16-bit parameters
+
+// ------------------------------------------------------------------------------------------------
+// fp32 states
+// ------------------------------------------------------------------------------------------------
+
+// One element; every line in double from fp32 operands, rounded once (a large update may nearly cancel
+// p), in the order of the dense step, so that without decay and scale the bits are the dense step's.
+__device__ __forceinline__ void adamw_elem(float g, float& mm, float& vv, float& pp, const Step& s, const AdamWParams& ap)
+{
+    const double gd = static_cast<double>(mul(g, s.scale));
+    mm = static_cast<float>(ap.beta1 * static_cast<double>(mm) + ap.one_m_beta1 * gd);
+    vv = static_cast<float>(ap.beta2 * static_cast<double>(vv) + ap.one_m_beta2 * (gd * gd));
+    double mh = static_cast<double>(mm), vh = static_cast<double>(vv);
+    if (ap.bias_correction) {
+        mh = mh / s.bc1;
+        vh = vh / s.bc2;
+    }
+    const double pd = static_cast<double>(pp);
+    const double u = mh / (sqrt(vh) + ap.eps) + s.wd * pd;
+    pp = static_cast<float>(pd - s.lr * u);
+}
+
+template <int G, int PK, bool SR>
+__global__ __launch_bounds__(kListBlock) void k_adamw(ListLaunch L, ListPtrs ptrs, State32 st, AdamWParams ap)
+{
+    using P = Par<PK>;
+    const ListItem it = L.items[blockIdx.x];
+    const void* g = ptrs.g[it.tensor - L.tensor0];
+    if (g == nullptr) return;
+    void* p = ptrs.p[it.tensor - L.tensor0];
+    const ListTensor tn = L.tensors[it.tensor];
+    const Step s = step_of(ap, tn);
+    if (s.skip) return;
+    u4 w{};
+    for (int base = 0; base < it.len; base += kListTile) {
+        const int at = base + 4 * static_cast<int>(threadIdx.x);
+        const int64_t i = it.start + at, si = tn.state_off + i;
+        const int cnt = it.len - at;
+        if (SR && P::kRound) w = philox_block(ap.seed, s.t | kParStream, si);
+        if (cnt >= 4) {
+            const f4 gv = load_any4<G>(g, i);
+            f4 mv = ld4<true>(st.m, si), vv = ld4<true>(st.v, si), pv = P::load4(p, st.master, i, si);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float mm = mv[k], vq = vv[k], pp = pv[k];
+                adamw_elem(gv[k], mm, vq, pp, s, ap);
+                mv[k] = mm;
+                vv[k] = vq;
+                pv[k] = pp;
+            }
+            st4<true>(st.m, si, mv);
+            st4<true>(st.v, si, vv);
+            P::template store4<SR>(p, st.master, i, si, pv, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= cnt) continue;
+                float mm = st.m[si + k], vq = st.v[si + k], pp = P::load1(p, st.master, i + k, si + k);
+                adamw_elem(load_any1<G>(g, i + k), mm, vq, pp, s, ap);
+                st.m[si + k] = mm;
+                st.v[si + k] = vq;
+                P::template store1<SR>(p, st.master, i + k, si + k, pp, w.x[k]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// 8-bit states
+// ------------------------------------------------------------------------------------------------
+
+// Constants of the fp32 lines.
+struct Step8 {
+    float scale, b1, c1, b2, c2, ibc1, ibc2, eps, lr, wd;
+};
+
+__device__ __forceinline__ Step8 step8_of(const Step& s, const AdamWParams& ap)
+{
+    Step8 r;
+    r.scale = s.scale;
+    r.b1 = static_cast<float>(ap.beta1);
+    r.c1 = static_cast<float>(ap.one_m_beta1);
+    r.b2 = static_cast<float>(ap.beta2);
+    r.c2 = static_cast<float>(ap.one_m_beta2);
+    r.ibc1 = ap.bias_correction ? static_cast<float>(1.0 / s.bc1) : 1.0f;
+    r.ibc2 = ap.bias_correction ? static_cast<float>(1.0 / s.bc2) : 1.0f;
+    r.eps = static_cast<float>(ap.eps);
+    r.lr = static_cast<float>(s.lr);
+    r.wd = static_cast<float>(s.wd);
+    return r;
+}
+
+// Moments and parameter of one element; root: about sqrt(v), for the code.
+__device__ __forceinline__ void adamw8_elem(float g, float& mm, float& vv, float& pp, float& root, const Step8& s)
+{
+    g = mul(g, s.scale);
+    mm = __fmaf_rn(s.b1, mm, mul(s.c1, g));
+    vv = __fmaf_rn(s.b2, vv, mul(s.c2, mul(g, g)));
+    root = __builtin_amdgcn_sqrtf(vv);
+    const float den = __builtin_amdgcn_sqrtf(vv * s.ibc2) + s.eps;
+    const float u = fmaf(mm * s.ibc1, __builtin_amdgcn_rcpf(den), s.wd * pp);
+    pp = fmaf(-s.lr, u, pp);
+}
+
+template <int G, int PK, bool SR>
+__global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs ptrs, State8 st, AdamWParams ap)
+{
+    using P = Par<PK>;
+    const ListItem it = L.items[blockIdx.x];
+    const void* g = ptrs.g[it.tensor - L.tensor0];
+    if (g == nullptr) return;
+    void* p = ptrs.p[it.tensor - L.tensor0];
+    const ListTensor tn = L.tensors[it.tensor];
+    const Step sd = step_of(ap, tn);
+    if (sd.skip) return;
+    const Step8 s = step8_of(sd, ap);
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    // one state block per wave and trip; the trip count is the same for all lanes of a wave
+    for (int base = wave * kStateBlock; base < it.len; base += kListTile) {
+        const int at = base + 4 * lane;
+        const int64_t i = it.start + at, si = tn.state_off + i, sb = (tn.state_off + it.start + base) / kStateBlock;
+        const int cnt = it.len - at;
+        float gv[4], mv[4], vv[4], pv[4], root[4];
+        uint32_t mw = kBias4, vw = 0;
+        const float qm0 = st.mq[sb], qv0 = st.vq[sb];
+        if (cnt >= 4) {
+            const f4 g4 = load_any4<G>(g, i), p4 = P::load4(p, st.master, i, si);
+            mw = *reinterpret_cast<const uint32_t*>(st.mc + si) ^ kBias4;
+            vw = *reinterpret_cast<const uint32_t*>(st.vc + si);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                gv[k] = g4[k];
+                pv[k] = p4[k];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                gv[k] = pv[k] = 0.0f;
+                if (k >= cnt) continue;
+                gv[k] = load_any1<G>(g, i + k);
+                pv[k] = P::load1(p, st.master, i + k, si + k);
+                mw = (mw & ~(0xffu << (8 * k))) | ((static_cast<uint32_t>(static_cast<uint8_t>(st.mc[si + k])) ^ 0x80u) << (8 * k));
+                vw |= static_cast<uint32_t>(st.vc[si + k]) << (8 * k);
+            }
+        }
+        uint32_t tm = 0, tv = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            mv[k] = decode_m(byte_of(mw, k), qm0);
+            vv[k] = decode_v(byte_of(vw, k), qv0);
+            adamw8_elem(gv[k], mv[k], vv[k], pv[k], root[k], s);
+            if (k < cnt) {   // behind the tensor's end nothing enters the scales
+                const uint32_t bm = __float_as_uint(mv[k]) & 0x7fffffffu, bv = __float_as_uint(vv[k]) & 0x7fffffffu;
+                tm = tm > bm ? tm : bm;
+                tv = tv > bv ? tv : bv;
+            }
+        }
+        const float qm = block_scale<false>(wave_max(tm)), qv = block_scale<true>(wave_max(tv));
+        const float rm = guess_scale(qm), rv = guess_scale(qv);
+        u4 w{}, wp{};
+        if (SR) w = philox_block(ap.seed, sd.t, si);
+        if (SR && P::kRound) wp = philox_block(ap.seed, sd.t | kParStream, si);
+        mw = vw = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float c = encode<false, SR>(fabsf(mv[k]), 0.0f, qm, rm, w.x[k] & 0xffffu);
+            mw = put_byte(copysignf(c, mv[k]) + 128.0f, k, mw);
+            vw = put_byte(encode<true, SR>(vv[k], root[k], qv, rv, w.x[k] >> 16), k, vw);
+        }
+        mw ^= kBias4;
+        if (lane == 0) {
+            st.mq[sb] = qm;
+            st.vq[sb] = qv;
+        }
+        if (cnt >= 4) {
+            *reinterpret_cast<uint32_t*>(st.mc + si) = mw;
+            *reinterpret_cast<uint32_t*>(st.vc + si) = vw;
+            f4 p4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p4[k] = pv[k];
+            P::template store4<SR>(p, st.master, i, si, p4, wp);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= cnt) continue;
+                st.mc[si + k] = static_cast<int8_t>(byte_of(mw, k));
+                st.vc[si + k] = static_cast<uint8_t>(byte_of(vw, k));
+                P::template store1<SR>(p, st.master, i + k, si + k, pv[k], wp.x[k]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// launches
+// ------------------------------------------------------------------------------------------------
+
+// f(kind as a constant, rounding as a constant) for the run-time values
+template <class F>
+hipError_t by_kind(int pk, int sr, F&& f)
+{
+#define OB_KIND(K)                                                                                              \
+    case K:                                                                                                     \
+        return sr ? f(std::integral_constant<int, K>{}, std::true_type{})                                       \
+                  : f(std::integral_constant<int, K>{}, std::false_type{});
+    switch (pk) {
+        OB_KIND(PK_F32)
+        OB_KIND(PK_BF16)
+        OB_KIND(PK_F16)
+        OB_KIND(PK_MASTER_BF16)
+        OB_KIND(PK_MASTER_F16)
+    }
+#undef OB_KIND
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+template <int G>
+hipError_t launch_adamw(const ListLaunch& L, const ListPtrs& ptrs, int pk, const State32& st, const AdamWParams& ap,
+                        hipStream_t s)
+{
+    // only 16-bit parameters are rounded by chance here
+    const int sr = ap.stochastic && (pk == PK_BF16 || pk == PK_F16);
+    return by_kind(pk, sr, [&](auto k, auto r) {
+        constexpr int PK = decltype(k)::value;
+        constexpr bool SR = decltype(r)::value && Par<PK>::kRound;
+        hipLaunchKernelGGL((k_adamw<G, PK, SR>), dim3(static_cast<unsigned>(L.n_items)), dim3(kListBlock), 0, s, L,
+                           ptrs, st, ap);
+        return hipGetLastError();
+    });
+}
+
+template <int G>
+hipError_t launch_adamw8(const ListLaunch& L, const ListPtrs& ptrs, int pk, const State8& st, const AdamWParams& ap,
+                         hipStream_t s)
+{
+    return by_kind(pk, ap.stochastic, [&](auto k, auto r) {
+        hipLaunchKernelGGL((k_adamw8<G, decltype(k)::value, decltype(r)::value>), dim3(static_cast<unsigned>(L.n_items)),
+                           dim3(kListBlock), 0, s, L, ptrs, st, ap);
+        return hipGetLastError();
+    });
+}
+
+template hipError_t launch_adamw<OB_AW_G>(const ListLaunch&, const ListPtrs&, int, const State32&, const AdamWParams&,
+                                          hipStream_t);
+template hipError_t launch_adamw8<OB_AW_G>(const ListLaunch&, const ListPtrs&, int, const State8&, const AdamWParams&,
+                                           hipStream_t);
+
+}  // namespace ob

@@ -1,0 +1,287 @@
+// ob_adamw_api.cpp -- host side of the calls over lists of tensors (declarations and contracts in
+// ob_adam.h): checks of arguments, the list's work-block tables, and the launches.
+#include "ob_adam.h"
+#include "ob_adamw.h"
+
+#include <cstddef>
+#include <vector>
+
+static_assert(sizeof(ob_control) == 64 && offsetof(ob_control, bc1) == 24 && offsetof(ob_control, skip) == 44,
+              "the control block's layout is part of the ABI");
+
+namespace {
+
+struct Table {
+    std::vector<int64_t> first;      // [T + 1]: blocks of the tensor in place k are [first[k], first[k+1])
+    ob::ListItem* d_items = nullptr;
+};
+
+}  // namespace
+
+struct ob_tensors_s {
+    int device = 0;
+    ob::ListShape shape;
+    Table step, norm;
+    ob::ListTensor* d_tensors = nullptr;        // by place
+};
+
+namespace {
+
+// Elements per work block, of the steps and of the norm.
+constexpr int64_t kStepElems = 4 * ob::kListTile;
+constexpr int64_t kNormElems = 16 * ob::kListTile;
+
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = true;
+    explicit DeviceGuard(int dev)
+    {
+        if (hipGetDevice(&prev) != hipSuccess) {
+            ok = false;
+            return;
+        }
+        if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
+    }
+    ~DeviceGuard()
+    {
+        int cur = -1;
+        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+    }
+};
+
+void free_list(ob_tensors l)
+{
+    if (!l) return;
+    if (l->step.d_items) (void)hipFree(l->step.d_items);
+    if (l->norm.d_items) (void)hipFree(l->norm.d_items);
+    if (l->d_tensors) (void)hipFree(l->d_tensors);
+    delete l;
+}
+
+template <class T>
+hipError_t upload(T** to, const std::vector<T>& from)
+{
+    if (from.empty()) return hipSuccess;
+    const hipError_t e = hipMalloc(to, from.size() * sizeof(T));
+    if (e != hipSuccess) return e;
+    return hipMemcpy(*to, from.data(), from.size() * sizeof(T), hipMemcpyHostToDevice);
+}
+
+ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const int32_t* pd, const float* lr,
+                      const float* wd, ob_tensors* out, ob_tensors& l)
+{
+    if (!out) return OB_ERR_ARG;
+    *out = nullptr;
+    l = new ob_tensors_s;
+    if (ob_status st = ob::build_shape(T, sizes, gd, pd, lr, wd, l->shape)) return st;
+    std::vector<ob::ListItem> step, norm;
+    if (!ob::build_items(l->shape, kStepElems, step, l->step.first) ||
+        !ob::build_items(l->shape, kNormElems, norm, l->norm.first))
+        return OB_ERR_ARG;
+    std::vector<ob::ListTensor> tensors;
+    for (int32_t t : l->shape.order) tensors.push_back({l->shape.state_off[t], lr ? lr[t] : 1.0f, wd ? wd[t] : 1.0f});
+
+    if (hipGetDevice(&l->device) != hipSuccess) return OB_ERR_HIP;
+    hipError_t e = upload(&l->step.d_items, step);
+    if (e == hipSuccess) e = upload(&l->norm.d_items, norm);
+    if (e == hipSuccess) e = upload(&l->d_tensors, tensors);
+    if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
+    *out = l;
+    return OB_OK;
+}
+
+ob::AdamWParams adamw_params(const ob_adamw_hparams* hp, const ob_control* control)
+{
+    ob::AdamWParams ap;
+    ap.lr = hp->lr;
+    ap.beta1 = hp->beta1;
+    ap.one_m_beta1 = 1.0 - static_cast<double>(hp->beta1);
+    ap.beta2 = hp->beta2;
+    ap.one_m_beta2 = 1.0 - static_cast<double>(hp->beta2);
+    ap.eps = hp->eps;
+    ap.wd = hp->weight_decay;
+    ap.bias_correction = hp->bias_correction ? 1 : 0;
+    ap.stochastic = hp->rounding == OB_ROUND_STOCHASTIC;
+    ap.bc1 = ap.bc2 = 1.0;
+    if (ap.bias_correction && !control) {
+        ap.bc1 = 1.0 - std::pow(ap.beta1, static_cast<double>(hp->step));
+        ap.bc2 = 1.0 - std::pow(ap.beta2, static_cast<double>(hp->step));
+    }
+    ap.seed = hp->sr_seed;
+    ap.step = static_cast<uint64_t>(hp->step);
+    ap.control = control;
+    return ap;
+}
+
+// The launches of a step: f(gradient type, parameter kind, launch, addresses) for each.
+template <class F>
+ob_status launch_step(const ob_tensors_s& l, const void* const* g, void* const* p, bool master, F&& f)
+{
+    const ob::ListShape& sh = l.shape;
+    ob::ListPtrs ptrs;
+    return ob::for_runs(sh, ob::kListPtrs, true, [&](int64_t k, int64_t e) {
+        ob::ListLaunch L;
+        L.items = l.step.d_items + l.step.first[k];
+        L.n_items = l.step.first[e] - l.step.first[k];
+        L.tensors = l.d_tensors;
+        L.tensor0 = static_cast<int32_t>(k);
+        if (L.n_items == 0) return OB_OK;
+        for (int64_t j = k; j < e; ++j) {
+            ptrs.g[j - k] = g[sh.order[j]];
+            ptrs.p[j - k] = p[sh.order[j]];
+        }
+        const int gd = sh.g_dtype[sh.order[k]], pd = sh.p_dtype[sh.order[k]];
+        const int pk = pd == OB_F32 ? ob::PK_F32 : pd + (master ? 2 : 0);
+        (void)hipGetLastError();  // clear a stale error so the check sees this launch only
+        return f(gd, pk, L, ptrs) == hipSuccess ? OB_OK : OB_ERR_HIP;
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+ob_status ob_tensors_create(int64_t n_tensors, const int64_t* sizes, const int32_t* g_dtypes, const int32_t* p_dtypes,
+                            const float* lr_mults, const float* wd_mults, ob_tensors* out)
+{
+    ob_tensors l = nullptr;
+    ob_status st;
+    try {
+        st = list_create(n_tensors, sizes, g_dtypes, p_dtypes, lr_mults, wd_mults, out, l);
+    } catch (...) {
+        st = OB_ERR_OOM;  // host allocation failures are the only exceptions here
+    }
+    if (st != OB_OK) free_list(l);
+    return st;
+}
+
+ob_status ob_tensors_destroy(ob_tensors list)
+try {
+    if (!list) return OB_ERR_ARG;
+    DeviceGuard guard(list->device);
+    free_list(list);
+    return OB_OK;
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+int64_t ob_tensors_count(ob_tensors list) { return list ? static_cast<int64_t>(list->shape.size.size()) : -1; }
+int64_t ob_tensors_num_elements(ob_tensors list) { return list ? list->shape.n : -1; }
+int64_t ob_tensors_state_elems(ob_tensors list) { return list ? list->shape.state_elems : -1; }
+int64_t ob_tensors_state_offset(ob_tensors list, int64_t t)
+{
+    return list && t >= 0 && t < static_cast<int64_t>(list->shape.size.size()) ? list->shape.state_off[static_cast<size_t>(t)] : -1;
+}
+
+ob_status ob_grad_norm(ob_tensors list, const void* const* g, float g_mult, float max_norm,
+                       const ob_adamw_hparams* hp, ob_control* control, hipStream_t stream)
+try {
+    if (!list) return OB_ERR_ARG;
+    const ob_tensors_s& l = *list;
+    if (ob_status st = ob::check_norm(l.shape, g, g_mult, max_norm, hp, control)) return st;
+    DeviceGuard guard(l.device);
+    if (!guard.ok) return OB_ERR_HIP;
+
+    // every launch has the same grid, so that the first one writes all partial sums and later ones add
+    int grid = 0;
+    (void)ob::for_runs(l.shape, ob::kNormPtrs, false, [&](int64_t k, int64_t e) {
+        grid = std::max(grid, static_cast<int>(std::min<int64_t>(l.norm.first[e] - l.norm.first[k], OB_CONTROL_PARTIALS)));
+        return OB_OK;
+    });
+    double* partials = reinterpret_cast<double*>(control + 1);
+    bool first = true;
+    ob::NormPtrs ptrs;
+    const ob_status st = ob::for_runs(l.shape, ob::kNormPtrs, false, [&](int64_t k, int64_t e) {
+        ob::ListLaunch L;
+        L.items = l.norm.d_items + l.norm.first[k];
+        L.n_items = l.norm.first[e] - l.norm.first[k];
+        L.tensors = l.d_tensors;
+        L.tensor0 = static_cast<int32_t>(k);
+        if (L.n_items == 0) return OB_OK;
+        for (int64_t j = k; j < e; ++j) ptrs.g[j - k] = g[l.shape.order[j]];
+        (void)hipGetLastError();
+        const hipError_t err = ob::launch_grad_sumsq(L, ptrs, l.shape.g_dtype[l.shape.order[k]], grid, first, partials, stream);
+        first = false;
+        return err == hipSuccess ? OB_OK : OB_ERR_HIP;
+    });
+    if (st != OB_OK) return st;
+    ob::NormParams np;
+    np.g_mult = g_mult;
+    np.max_norm = max_norm;
+    np.clip = max_norm > 0.0f && !std::isinf(max_norm);
+    np.advance = hp != nullptr;
+    np.beta1 = hp ? hp->beta1 : 0.0;
+    np.beta2 = hp ? hp->beta2 : 0.0;
+    (void)hipGetLastError();
+    return ob::launch_grad_control(control, grid, np, stream) == hipSuccess ? OB_OK : OB_ERR_HIP;
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+ob_status ob_adamw_step(ob_tensors list, const void* const* g, void* const* p, float* master, float* m, float* v,
+                        const ob_adamw_hparams* hp, const ob_control* control, hipStream_t stream)
+try {
+    if (!list) return OB_ERR_ARG;
+    if (ob_status st = ob::check_step(list->shape, g, p, master, false, hp, control)) return st;
+    if (list->shape.n == 0) return OB_OK;
+    if (!m || !v) return OB_ERR_ARG;
+    if (!ob::is_aligned(m, 16) || !ob::is_aligned(v, 16)) return OB_ERR_ALIGN;
+    const ob::AdamWParams ap = adamw_params(hp, control);
+    const ob::State32 state{master, m, v};
+    DeviceGuard guard(list->device);
+    if (!guard.ok) return OB_ERR_HIP;
+    return launch_step(*list, g, p, master != nullptr,
+                       [&](int gd, int pk, const ob::ListLaunch& L, const ob::ListPtrs& ptrs) {
+                           return gd == OB_BF16  ? ob::launch_adamw<OB_BF16>(L, ptrs, pk, state, ap, stream)
+                                  : gd == OB_F16 ? ob::launch_adamw<OB_F16>(L, ptrs, pk, state, ap, stream)
+                                                 : ob::launch_adamw<OB_F32>(L, ptrs, pk, state, ap, stream);
+                       });
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, float* master, int8_t* m_codes,
+                         float* m_scales, uint8_t* v_codes, float* v_scales, const ob_adamw_hparams* hp,
+                         const ob_control* control, hipStream_t stream)
+try {
+    if (!list) return OB_ERR_ARG;
+    if (ob_status st = ob::check_step(list->shape, g, p, master, true, hp, control)) return st;
+    if (list->shape.n == 0) return OB_OK;
+    if (!m_codes || !m_scales || !v_codes || !v_scales) return OB_ERR_ARG;
+    if (!ob::is_aligned(m_codes, 4) || !ob::is_aligned(v_codes, 4) || !ob::is_aligned(m_scales, 4) || !ob::is_aligned(v_scales, 4))
+        return OB_ERR_ALIGN;
+    const ob::AdamWParams ap = adamw_params(hp, control);
+    const ob::State8 state{master, m_codes, m_scales, v_codes, v_scales};
+    DeviceGuard guard(list->device);
+    if (!guard.ok) return OB_ERR_HIP;
+    return launch_step(*list, g, p, master != nullptr,
+                       [&](int gd, int pk, const ob::ListLaunch& L, const ob::ListPtrs& ptrs) {
+                           return gd == OB_BF16  ? ob::launch_adamw8<OB_BF16>(L, ptrs, pk, state, ap, stream)
+                                  : gd == OB_F16 ? ob::launch_adamw8<OB_F16>(L, ptrs, pk, state, ap, stream)
+                                                 : ob::launch_adamw8<OB_F32>(L, ptrs, pk, state, ap, stream);
+                       });
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_codes, float* m_scales,
+                           uint8_t* v_codes, float* v_scales, hipStream_t stream)
+{
+    if (ob_status st = ob::check_state8(n, m, v, m_codes, m_scales, v_codes, v_scales)) return st;
+    if (n == 0) return OB_OK;
+    (void)hipGetLastError();
+    return ob::launch_state8_encode(n, m, v, m_codes, m_scales, v_codes, v_scales, stream) == hipSuccess ? OB_OK
+                                                                                                       : OB_ERR_HIP;
+}
+
+ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,
+                           const float* v_scales, float* m, float* v, hipStream_t stream)
+{
+    if (ob_status st = ob::check_state8(n, m, v, m_codes, m_scales, v_codes, v_scales)) return st;
+    if (n == 0) return OB_OK;
+    (void)hipGetLastError();
+    return ob::launch_state8_decode(n, m_codes, m_scales, v_codes, v_scales, m, v, stream) == hipSuccess ? OB_OK
+                                                                                                       : OB_ERR_HIP;
+}
+
+}  // extern "C"

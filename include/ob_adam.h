@@ -294,6 +294,127 @@ ob_status ob_plan_read_timing(ob_plan plan, int32_t kernel, double* total_ms, in
  * switches them off; exactly one NULL is OB_ERR_ARG. */
 ob_status ob_plan_set_diagnostics(ob_plan plan, double* err_sumsq_out, uint64_t* plus_count_out);
 
+/* ---- AdamW over many tensors at once ----
+ * For models whose parameters are separate tensors (or views into buckets) rather than one flat buffer:
+ * the dense Adam step of ob_adam_warmup_step with decoupled weight decay, per-tensor rates, parameters
+ * and gradients of mixed types, clipping by the global gradient norm, and states in fp32 or in 8 bits.
+ *
+ * A list (ob_tensors) describes T tensors by size and type.  Their addresses are given with every call,
+ * as host arrays of T device pointers, so gradients may move from step to step.  Parameter and gradient
+ * pointers need the alignment of their element type only.  g[t] == NULL: tensor t has no gradient and the
+ * call leaves it and its states alone.  Tensors of 0 elements are allowed (their pointers are ignored).
+ * The parameters (and 16-bit copies) of two tensors must not overlap: OB_ERR_ARG.
+ *
+ * States (m, v, the master copy, 8-bit codes) are flat buffers of ob_tensors_state_elems(list) elements:
+ * tensor t's state starts at ob_tensors_state_offset(list, t), the sum of the sizes before it with each
+ * rounded up to a multiple of OB_STATE_BLOCK.  The gaps are neither read into a result nor written.
+ *
+ * Threads and streams: a list is read-only after its creation and holds no workspace, so calls with one
+ * list may overlap if their buffers (parameters, states, control) differ.  No call synchronises,
+ * allocates device memory or records anything but kernels, so all can be captured into a HIP graph; a
+ * captured call keeps its addresses and hparams, while what the control block holds is read on replay. */
+#define OB_STATE_BLOCK 256
+
+typedef struct ob_tensors_s* ob_tensors;
+
+/* sizes: T >= 0 host int64, each >= 0.  g_dtypes, p_dtypes: T ob_dtype values each (OB_F32, OB_BF16 or
+ * OB_F16).  lr_mults, wd_mults: T host factors of the rate and of the weight decay (parameter groups), or
+ * NULL for 1; finite.  At most 2^31 - 1 work blocks of 4096 elements in all (OB_ERR_ARG beyond).  The list belongs to the
+ * device that is current here; it owns its device tables (hipMalloc here, hipFree in ob_tensors_destroy). */
+ob_status ob_tensors_create(int64_t n_tensors, const int64_t* sizes, const int32_t* g_dtypes, const int32_t* p_dtypes,
+                            const float* lr_mults, const float* wd_mults, ob_tensors* out);
+ob_status ob_tensors_destroy(ob_tensors list);
+int64_t ob_tensors_count(ob_tensors list);                    /* -1 for a NULL list */
+int64_t ob_tensors_num_elements(ob_tensors list);             /* sum of the sizes; -1 for a NULL list */
+int64_t ob_tensors_state_elems(ob_tensors list);              /* multiple of OB_STATE_BLOCK; -1 for a NULL list */
+int64_t ob_tensors_state_offset(ob_tensors list, int64_t t);  /* -1 for a NULL list or t outside 0..T-1 */
+
+/* Parameters of the AdamW step.  beta1, beta2 in [0, 1), eps >= 0 (8-bit states: eps a normal number > 0),
+ * weight_decay and lr finite; OB_ERR_ARG otherwise. */
+typedef struct {
+    float lr;
+    float beta1;
+    float beta2;
+    float eps;
+    float weight_decay;      /* decoupled: p -= lr * weight_decay * p */
+    int32_t bias_correction; /* divide m, v by 1 - beta^t */
+    int64_t step;            /* t >= 1 without a control block; ignored with one */
+    int32_t rounding;        /* ob_rounding: of 8-bit states and of 16-bit parameters without a master */
+    int32_t reserved;        /* 0 */
+    uint64_t sr_seed;        /* OB_ROUND_STOCHASTIC: the generator's key, with t */
+} ob_adamw_hparams;
+
+/* The control block: OB_CONTROL_BYTES of device memory owned by the caller, 8-byte aligned, all zero but
+ * lr_scale (1) before its first use.  The fields below are followed by the norm's partial sums. */
+typedef struct {
+    float norm;          /* |g_mult| times the L2 norm of all gradients */
+    float grad_scale;    /* what the step multiplies every gradient with */
+    int64_t step;        /* t: steps taken, the coming one included */
+    int64_t skipped;     /* steps not taken because their norm was not finite */
+    double bc1, bc2;     /* 1 - beta1^t, 1 - beta2^t */
+    float lr_scale;      /* written by the caller: factor of the rate (schedules under a captured graph) */
+    int32_t skip;        /* 1: the norm was not finite, and a step with this block changes nothing */
+    uint32_t reserved[4];
+} ob_control;
+#define OB_CONTROL_PARTIALS 2048
+#define OB_CONTROL_BYTES (64 + 8 * OB_CONTROL_PARTIALS)
+
+/* Global gradient norm and clipping:
+ *   norm = |g_mult| * sqrt(sum over all tensors of g^2), squares and sums in double, in an order that
+ *          depends on the list alone (the same bits on every call);
+ *   grad_scale = g_mult * min(1, max_norm / (norm + 1e-6)) in double, rounded once; max_norm <= 0 or
+ *          infinite: g_mult.  g_mult (finite, not 0) removes a loss scale.
+ * hp != NULL: also the step's bookkeeping.  norm finite: step += 1, bc1 and bc2 from it, skip = 0;
+ * otherwise skipped += 1, skip = 1 (grad_scale then is 0 for an infinite norm with clipping, NaN for a NaN).
+ * hp == NULL: skip is set as above, step, skipped, bc1 and bc2 stay. */
+ob_status ob_grad_norm(ob_tensors list, const void* const* g, float g_mult, float max_norm,
+                       const ob_adamw_hparams* hp, ob_control* control, hipStream_t stream);
+
+/* AdamW step with fp32 states.  With t, bc1, bc2, s = grad_scale and r = lr_scale from `control` (NULL: t =
+ * hp->step, s = r = 1), for tensor j: a = lr * r * lr_mults[j], d = weight_decay * wd_mults[j],
+ *   g' = fl32(widen(g) * s);  m = beta1*m + (1-beta1)*g';  v = beta2*v + (1-beta2)*g'^2;
+ *   p -= a * ( (m/bc1) / (sqrt(v/bc2) + eps) + d*p )     (bc1 = bc2 = 1 without hp->bias_correction)
+ * each line in double, rounded once, as in ob_adam_warmup_step; with d = 0, s = 1 the same bits as there.
+ * p[t]: the parameters, updated in place.  master != NULL (fp32[state_elems]): for tensors of a 16-bit
+ * type the master copy is the parameter, and p[t] gets its rounding to nearest; fp32 tensors do not use
+ * it.  16-bit parameters without a master are widened, updated, rounded to fp32 and then to their type:
+ * to nearest, ties to even, or stochastically by the rule of ob_adam_compress_step's error buffer, with i
+ * the state index and the counter (i >> 2, t + 2^63). */
+ob_status ob_adamw_step(ob_tensors list, const void* const* g, void* const* p, float* master, float* m, float* v,
+                        const ob_adamw_hparams* hp, const ob_control* control, hipStream_t stream);
+
+/* The 8-bit format: blocks of OB_STATE_BLOCK consecutive state elements, one fp32 scale q per block and
+ * moment, fl = rounding to fp32:
+ *   m: code c in -127..127, q = fl(max|m| * fl(1/127^2)), value fl(c*|c| * q);
+ *   v: code k in 0..255, q = fl(fl(sqrt(max v)) * fl(1/255^2)), root r = fl(k^2 * q), value fl(r^2).
+ * (Square-law codes: the step between neighbours is 2/c of an m and 4/k of a v, finest for the largest
+ * values of a block and widening to 1/127^2 and 1/255^4 of it at the smallest.)
+ * Rounding to nearest in the code: |c| is the largest k with k = 0 or |m| >= fl((k-1/2)^2 * q); k the
+ * largest with k = 0 or v >= fl(T^2), T = fl((k-1/2)^2 * q).  Stochastic (steps only): k the largest with
+ * value(k) <= x, then up iff fl(u * fl(value(k+1) - value(k))) < fl(fl(x - value(k)) * 65536), at most the
+ * largest code; u: 16 bits of output word i & 3 of Philox4x32-10 at the counter (i >> 2, t) under the key
+ * sr_seed, the low half for m, the high half for v (i: state index).  A v > 0 gets at least code 1, so that
+ * no denominator collapses.  A block whose largest value is below 2^-96 is held as zeros (q = 0); in a
+ * block with a NaN, an infinity or a negative v, q = NaN and the codes are 0: the block reads as NaN. */
+
+/* AdamW step with states in that format: m_codes int8[state_elems], v_codes uint8[state_elems], m_scales and
+ * v_scales fp32[state_elems / 256]; all zero is the state before the first step.  Arguments as
+ * ob_adamw_step; the moments of the step are
+ *   m = fma(beta1, m, fl(fl(1-beta1) * g')), v = fma(beta2, v, fl(fl(1-beta2) * fl(g'^2))) in fp32,
+ * and the parameters' line is evaluated in fp32 (relative error of the update below 2^-20; values of v
+ * below 2^-126 count as zero in its denominator). */
+ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, float* master, int8_t* m_codes,
+                         float* m_scales, uint8_t* v_codes, float* v_scales, const ob_adamw_hparams* hp,
+                         const ob_control* control, hipStream_t stream);
+
+/* n fp32 moments into the 8-bit format, to nearest (v >= 0), and back; n >= 0, the last block may be short
+ * (ceil(n / 256) scales).  Either moment may be left out: all its pointers NULL.  fp32 pointers 16-byte
+ * aligned, codes 4 bytes, scales 4 bytes. */
+ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_codes, float* m_scales,
+                           uint8_t* v_codes, float* v_scales, hipStream_t stream);
+ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,
+                           const float* v_scales, float* m, float* v, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
