@@ -20,7 +20,6 @@ namespace {
 // loads and stores of four consecutive elements at the alignment of one
 // ------------------------------------------------------------------------------------------------
 
-typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
 
 // type of elements: 0 fp32, 1 bf16, 2 fp16
@@ -185,36 +184,55 @@ __global__ __launch_bounds__(kListBlock) void k_adamw(ListLaunch L, ListPtrs ptr
     const ListTensor tn = L.tensors[it.tensor];
     const Step s = step_of(ap, tn);
     if (s.skip) return;
-    u4 w{};
-    for (int base = 0; base < it.len; base += kListTile) {
-        const int at = base + 4 * static_cast<int>(threadIdx.x);
-        const int64_t i = it.start + at, si = tn.state_off + i;
-        const int cnt = it.len - at;
-        if (SR && P::kRound) w = philox_block(ap.seed, s.t | kParStream, si);
+    const int tid4 = 4 * static_cast<int>(threadIdx.x);
+    f4 gv[kTiles32], mv[kTiles32], vv[kTiles32], pv[kTiles32];
+    auto load = [&](int u) {
+        const int64_t i = it.start + u * kListTile + tid4, si = tn.state_off + i;
+        gv[u] = load_any4<G>(g, i);
+        mv[u] = ld4<true>(st.m, si);
+        vv[u] = ld4<true>(st.v, si);
+        pv[u] = P::load4(p, st.master, i, si);
+    };
+    auto finish = [&](int u) {
+        const int64_t i = it.start + u * kListTile + tid4, si = tn.state_off + i;
+        u4 w{};
+        if (SR) w = philox_block(ap.seed, s.t | kParStream, si);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float mm = mv[u][k], vq = vv[u][k], pp = pv[u][k];
+            adamw_elem(gv[u][k], mm, vq, pp, s, ap);
+            mv[u][k] = mm;
+            vv[u][k] = vq;
+            pv[u][k] = pp;
+        }
+        st4<true>(st.m, si, mv[u]);
+        st4<true>(st.v, si, vv[u]);
+        P::template store4<SR>(p, st.master, i, si, pv[u], w);
+    };
+    if (it.len == kStepElems32) {   // a whole block: all its loads ahead of the arithmetic
+#pragma unroll
+        for (int u = 0; u < kTiles32; ++u) load(u);
+#pragma unroll
+        for (int u = 0; u < kTiles32; ++u) finish(u);
+        return;
+    }
+#pragma unroll
+    for (int u = 0; u < kTiles32; ++u) {   // a tensor's last block
+        const int64_t i = it.start + u * kListTile + tid4, si = tn.state_off + i;
+        const int cnt = it.len - u * kListTile - tid4;
         if (cnt >= 4) {
-            const f4 gv = load_any4<G>(g, i);
-            f4 mv = ld4<true>(st.m, si), vv = ld4<true>(st.v, si), pv = P::load4(p, st.master, i, si);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float mm = mv[k], vq = vv[k], pp = pv[k];
-                adamw_elem(gv[k], mm, vq, pp, s, ap);
-                mv[k] = mm;
-                vv[k] = vq;
-                pv[k] = pp;
-            }
-            st4<true>(st.m, si, mv);
-            st4<true>(st.v, si, vv);
-            P::template store4<SR>(p, st.master, i, si, pv, w);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k >= cnt) continue;
-                float mm = st.m[si + k], vq = st.v[si + k], pp = P::load1(p, st.master, i + k, si + k);
-                adamw_elem(load_any1<G>(g, i + k), mm, vq, pp, s, ap);
-                st.m[si + k] = mm;
-                st.v[si + k] = vq;
-                P::template store1<SR>(p, st.master, i + k, si + k, pp, w.x[k]);
-            }
+            load(u);
+            finish(u);
+            continue;
+        }
+        u4 w{};
+        if (SR) w = philox_block(ap.seed, s.t | kParStream, si);
+        for (int k = 0; k < cnt; ++k) {
+            float mm = st.m[si + k], vq = st.v[si + k], pp = P::load1(p, st.master, i + k, si + k);
+            adamw_elem(load_any1<G>(g, i + k), mm, vq, pp, s, ap);
+            st.m[si + k] = mm;
+            st.v[si + k] = vq;
+            P::template store1<SR>(p, st.master, i + k, si + k, pp, k == 0 ? w.x[0] : k == 1 ? w.x[1] : w.x[2]);
         }
     }
 }
@@ -225,7 +243,7 @@ __global__ __launch_bounds__(kListBlock) void k_adamw(ListLaunch L, ListPtrs ptr
 
 // Constants of the fp32 lines.
 struct Step8 {
-    float scale, b1, c1, b2, c2, ibc1, ibc2, eps, lr, wd;
+    float scale, b1, c1, b2, c2, inv_bc1, inv_root_bc2, eps, lr, wd;
 };
 
 __device__ __forceinline__ Step8 step8_of(const Step& s, const AdamWParams& ap)
@@ -236,30 +254,106 @@ __device__ __forceinline__ Step8 step8_of(const Step& s, const AdamWParams& ap)
     r.c1 = static_cast<float>(ap.one_m_beta1);
     r.b2 = static_cast<float>(ap.beta2);
     r.c2 = static_cast<float>(ap.one_m_beta2);
-    r.ibc1 = ap.bias_correction ? static_cast<float>(1.0 / s.bc1) : 1.0f;
-    r.ibc2 = ap.bias_correction ? static_cast<float>(1.0 / s.bc2) : 1.0f;
+    r.inv_bc1 = ap.control && ap.bias_correction ? ap.control->inv_bc1 : ap.inv_bc1;
+    r.inv_root_bc2 = ap.control && ap.bias_correction ? ap.control->inv_root_bc2 : ap.inv_root_bc2;
     r.eps = static_cast<float>(ap.eps);
     r.lr = static_cast<float>(s.lr);
     r.wd = static_cast<float>(s.wd);
     return r;
 }
 
-// Moments and parameter of one element; root: about sqrt(v), for the code.
+// Moments and parameter of one element; root: about sqrt(v).
 __device__ __forceinline__ void adamw8_elem(float g, float& mm, float& vv, float& pp, float& root, const Step8& s)
 {
     g = mul(g, s.scale);
-    mm = __fmaf_rn(s.b1, mm, mul(s.c1, g));
-    vv = __fmaf_rn(s.b2, vv, mul(s.c2, mul(g, g)));
+    mm = __builtin_fmaf(s.b1, mm, mul(s.c1, g));
+    vv = __builtin_fmaf(s.b2, vv, mul(s.c2, mul(g, g)));
     root = __builtin_amdgcn_sqrtf(vv);
-    const float den = __builtin_amdgcn_sqrtf(vv * s.ibc2) + s.eps;
-    const float u = fmaf(mm * s.ibc1, __builtin_amdgcn_rcpf(den), s.wd * pp);
+    const float den = fmaf(root, s.inv_root_bc2, s.eps);
+    const float u = fmaf(mm * s.inv_bc1, __builtin_amdgcn_rcpf(den), s.wd * pp);
     pp = fmaf(-s.lr, u, pp);
+}
+
+// A wave's span: elements [at, at + kSpanElems) of the tensor, `left` of them there (FULL: all).
+template <int G, int PK, bool SR, bool FULL>
+__device__ __forceinline__ void span8(const void* g, void* p, const State8& st, int64_t state_off, int64_t at, int left,
+                                      const Step8& s, uint64_t seed, uint64_t t)
+{
+    using P = Par<PK>;
+    const int lane4 = 4 * (static_cast<int>(threadIdx.x) & 63);
+    const int64_t sb = (state_off + at) / kStateBlock;
+    const int blocks = (left + kStateBlock - 1) / kStateBlock;
+    float gv[kSpan][4], pv[kSpan][4], mv[kSpan][4], vv[kSpan][4], root[kSpan][4];
+    uint32_t mw[kSpan], vw[kSpan], tm[kSpan], tv[kSpan];
+    const f4 qm = load_scales<FULL>(st.mq, sb, blocks), qv = load_scales<FULL>(st.vq, sb, blocks);
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int64_t i = at + j * kStateBlock + lane4, si = state_off + i;
+        const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
+        mw[j] = load_codes<FULL>(st.mc, si, cnt);
+        vw[j] = load_codes<FULL>(st.vc, si, cnt);
+        f4 g4{}, p4{};
+        if (FULL || cnt >= 4) {
+            g4 = load_any4<G>(g, i);
+            p4 = P::load4(p, st.master, i, si);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= cnt) continue;
+                g4[k] = load_any1<G>(g, i + k);
+                p4[k] = P::load1(p, st.master, i + k, si + k);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            gv[j][k] = g4[k];
+            pv[j][k] = p4[k];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int64_t i = at + j * kStateBlock + lane4, si = state_off + i;
+        const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
+        decode4<false>(mw[j], qm[j], mv[j]);
+        decode4<true>(vw[j], qv[j], vv[j]);
+        tm[j] = tv[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            adamw8_elem(gv[j][k], mv[j][k], vv[j][k], pv[j][k], root[j][k], s);
+            if (FULL || k < cnt) {   // what is behind the tensor's end does not enter the scales
+                tm[j] = max_u(tm[j], __float_as_uint(mv[j][k]) & 0x7fffffffu);
+                tv[j] = max_u(tv[j], __float_as_uint(vv[j][k]));   // v >= 0, or a NaN of either sign
+            }
+        }
+        u4 w{};
+        if (SR && P::kRound) w = philox_block(seed, t | kParStream, si);
+        if (FULL || cnt >= 4) {
+            f4 p4;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p4[k] = pv[j][k];
+            P::template store4<SR>(p, st.master, i, si, p4, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < cnt) P::template store1<SR>(p, st.master, i + k, si + k, pv[j][k], w.x[k]);
+        }
+    }
+    const SpanScales q = span_scales(tm, tv);
+    store_scales<FULL>(st.mq, st.vq, sb, blocks, q);
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int64_t si = state_off + at + j * kStateBlock + lane4;
+        const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
+        u4 w{};
+        if (SR) w = philox_block(seed, t, si);
+        store_codes<FULL>(st.mc, si, cnt, encode4<false, SR>(mv[j], nullptr, q.get(j, false), w));
+        store_codes<FULL>(st.vc, si, cnt, encode4<true, SR>(vv[j], root[j], q.get(j, true), w));
+    }
 }
 
 template <int G, int PK, bool SR>
 __global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs ptrs, State8 st, AdamWParams ap)
 {
-    using P = Par<PK>;
     const ListItem it = L.items[blockIdx.x];
     const void* g = ptrs.g[it.tensor - L.tensor0];
     if (g == nullptr) return;
@@ -268,81 +362,13 @@ __global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs pt
     const Step sd = step_of(ap, tn);
     if (sd.skip) return;
     const Step8 s = step8_of(sd, ap);
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-    const int lane = static_cast<int>(threadIdx.x) & 63;
-    // one state block per wave and trip; the trip count is the same for all lanes of a wave
-    for (int base = wave * kStateBlock; base < it.len; base += kListTile) {
-        const int at = base + 4 * lane;
-        const int64_t i = it.start + at, si = tn.state_off + i, sb = (tn.state_off + it.start + base) / kStateBlock;
-        const int cnt = it.len - at;
-        float gv[4], mv[4], vv[4], pv[4], root[4];
-        uint32_t mw = kBias4, vw = 0;
-        const float qm0 = st.mq[sb], qv0 = st.vq[sb];
-        if (cnt >= 4) {
-            const f4 g4 = load_any4<G>(g, i), p4 = P::load4(p, st.master, i, si);
-            mw = *reinterpret_cast<const uint32_t*>(st.mc + si) ^ kBias4;
-            vw = *reinterpret_cast<const uint32_t*>(st.vc + si);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                gv[k] = g4[k];
-                pv[k] = p4[k];
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                gv[k] = pv[k] = 0.0f;
-                if (k >= cnt) continue;
-                gv[k] = load_any1<G>(g, i + k);
-                pv[k] = P::load1(p, st.master, i + k, si + k);
-                mw = (mw & ~(0xffu << (8 * k))) | ((static_cast<uint32_t>(static_cast<uint8_t>(st.mc[si + k])) ^ 0x80u) << (8 * k));
-                vw |= static_cast<uint32_t>(st.vc[si + k]) << (8 * k);
-            }
-        }
-        uint32_t tm = 0, tv = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            mv[k] = decode_m(byte_of(mw, k), qm0);
-            vv[k] = decode_v(byte_of(vw, k), qv0);
-            adamw8_elem(gv[k], mv[k], vv[k], pv[k], root[k], s);
-            if (k < cnt) {   // behind the tensor's end nothing enters the scales
-                const uint32_t bm = __float_as_uint(mv[k]) & 0x7fffffffu, bv = __float_as_uint(vv[k]) & 0x7fffffffu;
-                tm = tm > bm ? tm : bm;
-                tv = tv > bv ? tv : bv;
-            }
-        }
-        const float qm = block_scale<false>(wave_max(tm)), qv = block_scale<true>(wave_max(tv));
-        const float rm = guess_scale(qm), rv = guess_scale(qv);
-        u4 w{}, wp{};
-        if (SR) w = philox_block(ap.seed, sd.t, si);
-        if (SR && P::kRound) wp = philox_block(ap.seed, sd.t | kParStream, si);
-        mw = vw = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float c = encode<false, SR>(fabsf(mv[k]), 0.0f, qm, rm, w.x[k] & 0xffffu);
-            mw = put_byte(copysignf(c, mv[k]) + 128.0f, k, mw);
-            vw = put_byte(encode<true, SR>(vv[k], root[k], qv, rv, w.x[k] >> 16), k, vw);
-        }
-        mw ^= kBias4;
-        if (lane == 0) {
-            st.mq[sb] = qm;
-            st.vq[sb] = qv;
-        }
-        if (cnt >= 4) {
-            *reinterpret_cast<uint32_t*>(st.mc + si) = mw;
-            *reinterpret_cast<uint32_t*>(st.vc + si) = vw;
-            f4 p4;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p4[k] = pv[k];
-            P::template store4<SR>(p, st.master, i, si, p4, wp);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (k >= cnt) continue;
-                st.mc[si + k] = static_cast<int8_t>(byte_of(mw, k));
-                st.vc[si + k] = static_cast<uint8_t>(byte_of(vw, k));
-                P::template store1<SR>(p, st.master, i + k, si + k, pv[k], wp.x[k]);
-            }
-        }
+    const int first = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * kSpanElems;
+    for (int base = first; base < it.len; base += kListBlock / 64 * kSpanElems) {   // uniform over a wave
+        const int left = it.len - base;
+        if (left >= kSpanElems)
+            span8<G, PK, SR, true>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
+        else
+            span8<G, PK, SR, false>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
     }
 }
 

@@ -21,24 +21,41 @@ constexpr uint32_t kTinyBits = 0x0f800000u;  // 2^-96
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr float kBelow = 1.0f / 8192.0f;
 
-// Largest value over the wave's 64 lanes, in every lane (a scalar register): maxima over pairs, quads,
-// half rows and rows by DPP, then rows joined by row broadcasts into lane 63.  All lanes active.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
+
+// A wave takes spans of kSpan state blocks, four elements of each block per lane.  Their 2 kSpan largest
+// magnitudes (of m and of v) are reduced together: each exchange of half-waves or rows leaves half as many
+// registers, so eight values over 64 lanes cost 20 operations.
+constexpr int kSpan = 4;
+constexpr int kSpanElems = kSpan * kStateBlock;
+
+__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// a over lanes 0..31 (pairs with the upper half) next to b over lanes 32..63
+__device__ __forceinline__ uint32_t fold32(uint32_t a, uint32_t b)
 {
-#define OB_DPP_MAX(ctrl, rows)                                                                             \
-    {                                                                                                      \
-        const uint32_t y = static_cast<uint32_t>(                                                          \
-            __builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), ctrl, rows, 0xF, false)); \
-        x = x > y ? x : y;                                                                                 \
-    }
-    OB_DPP_MAX(0xB1, 0xF)    // quad_perm [1,0,3,2]
-    OB_DPP_MAX(0x4E, 0xF)    // quad_perm [2,3,0,1]
-    OB_DPP_MAX(0x141, 0xF)   // row_half_mirror
-    OB_DPP_MAX(0x140, 0xF)   // row_mirror
-    OB_DPP_MAX(0x142, 0xA)   // row_bcast:15 into rows 1 and 3
-    OB_DPP_MAX(0x143, 0xC)   // row_bcast:31 into rows 2 and 3
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return max_u(r[0], r[1]);
+}
+
+// rows (16 lanes) of a: 0, 2 and of b: 1, 3, each with its neighbouring row folded in
+__device__ __forceinline__ uint32_t fold16(uint32_t a, uint32_t b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    return max_u(r[0], r[1]);
+}
+
+// the largest of each row of 16 lanes, in all of them
+__device__ __forceinline__ uint32_t row_max(uint32_t x)
+{
+#define OB_DPP_MAX(ctrl) \
+    x = max_u(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl, 0xF, 0xF, true)));
+    OB_DPP_MAX(0xB1)    // quad_perm [1,0,3,2]
+    OB_DPP_MAX(0x4E)    // quad_perm [2,3,0,1]
+    OB_DPP_MAX(0x141)   // row_half_mirror
+    OB_DPP_MAX(0x140)   // row_mirror
 #undef OB_DPP_MAX
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
+    return x;
 }
 
 // Single operations, never fused with a neighbour: the format's rules round each of them.
@@ -54,18 +71,42 @@ __device__ __forceinline__ float sub(float a, float b)
     return a - b;
 }
 
-// The format's scale from the bits of the block's largest magnitude.  (top as unsigned bits: NaN above
-// infinity above every number, so neither is lost in the maximum.)
-template <bool V>
-__device__ __forceinline__ float block_scale(uint32_t top)
+// The root of t in [2^-96, 2^128), correctly rounded: the hardware's root is within one unit, and the residuals
+// with its neighbours say which of the three is nearest.
+__device__ __forceinline__ float exact_root(float t)
+{
+    const float s = __builtin_amdgcn_sqrtf(t);
+    const float down = __uint_as_float(__float_as_uint(s) - 1u), up = __uint_as_float(__float_as_uint(s) + 1u);
+    float r = fmaf(-down, s, t) <= 0.0f ? down : s;
+    return fmaf(-up, s, t) > 0.0f ? up : r;
+}
+
+// The scales of a span's blocks.  tm, tv: per block the lane's largest magnitude as unsigned bits (NaN above
+// infinity above every number, so neither is lost in a maximum).  Two registers hold the eight scales, each in
+// a row of 16 lanes: rows 0, 1 of a the m of blocks 0, 1, rows 2, 3 their v; b blocks 2, 3.
+struct SpanScales {
+    float a, b;
+    __device__ __forceinline__ float get(int j, bool v) const   // uniform
+    {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(j < 2 ? a : b), (v ? 32 : 0) + 16 * (j & 1)));
+    }
+};
+
+__device__ __forceinline__ float block_scale(uint32_t top, bool v)
 {
     const float t = __uint_as_float(top);
-    const float q = V ? mul(sqrtf(t), kQuantV) : mul(t, kQuantM);
+    const float q = v ? mul(exact_root(t), kQuantV) : mul(t, kQuantM);
     return top >= kInfBits ? __uint_as_float(0x7fc00000u) : top < kTinyBits ? 0.0f : q;
 }
 
-// 1/q for the first guess of a code (0 where the block has no codes)
-__device__ __forceinline__ float guess_scale(float q) { return q > 0.0f ? __builtin_amdgcn_rcpf(q) : 0.0f; }
+__device__ __forceinline__ SpanScales span_scales(const uint32_t tm[kSpan], const uint32_t tv[kSpan])
+{
+    const bool v = (threadIdx.x & 32) != 0;
+    SpanScales s;
+    s.a = block_scale(row_max(fold16(fold32(tm[0], tv[0]), fold32(tm[1], tv[1]))), v);
+    s.b = block_scale(row_max(fold16(fold32(tm[2], tv[2]), fold32(tm[3], tv[3]))), v);
+    return s;
+}
 
 // value of code k >= 0 (also of the half-way borders k - 1/2)
 template <bool V>
@@ -75,48 +116,107 @@ __device__ __forceinline__ float code_value(float k, float q)
     return V ? mul(r, r) : r;
 }
 
-// |code| of x >= 0 as a float; rq: guess_scale(q); bits: 16 random bits (SR).  root_x: about sqrt(x) (V).
+// |code| of x >= 0 as a float, for a block with q > 0 (the caller replaces the codes of other blocks by
+// zeros).  rq: about 1/q; root: about sqrt(x) (V only); bits: 16 random bits (SR).
 template <bool V, bool SR>
-__device__ __forceinline__ float encode(float x, float root_x, float q, float rq, uint32_t bits)
+__device__ __forceinline__ float encode(float x, float root, float q, float rq, uint32_t bits)
 {
     constexpr float most = V ? 255.0f : 127.0f;
-    const float y = __builtin_amdgcn_sqrtf(V ? root_x * rq : x * rq);
+    const float y = __builtin_amdgcn_sqrtf((V ? root : x) * rq);
     float k;
     if (!SR) {
-        k = floorf(y + (0.5f - kBelow));
-        k += x >= code_value<V>(k + 0.5f, q) ? 1.0f : 0.0f;
+        const float z = y + (0.5f - kBelow), h = floorf(z) + 0.5f;   // h: the next border
+        bool up = x >= code_value<V>(h, q);
+        if (V) up = up || (z < 1.0f && x > 0.0f);
+        k = h + (up ? 0.5f : -0.5f);
     } else {
         k = fmaxf(floorf(y - kBelow), 0.0f);
-        float low = code_value<V>(k, q), high = code_value<V>(k + 1.0f, q);
-        if (x >= high) {
-            k += 1.0f;
-            low = high;
-            high = code_value<V>(k + 1.0f, q);
-        }
+        k += x >= code_value<V>(k + 1.0f, q) ? 1.0f : 0.0f;
+        const float low = code_value<V>(k, q), high = code_value<V>(k + 1.0f, q);
         const float u = static_cast<float>(bits);
         k += mul(u, sub(high, low)) < mul(sub(x, low), 65536.0f) ? 1.0f : 0.0f;
         k = fminf(k, most);
+        if (V) k = x > 0.0f ? fmaxf(k, 1.0f) : k;
     }
-    if (V) k = x > 0.0f ? fmaxf(k, 1.0f) : 0.0f;
-    return q > 0.0f ? k : 0.0f;
+    return k;
 }
 
-__device__ __forceinline__ float decode_m(uint32_t biased_byte, float q)
+// The codes of a lane's four elements of one block, as stored (int8 codes of m, uint8 of v).
+template <bool V, bool SR>
+__device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4], float q, const u4& w)
 {
-    const float c = static_cast<float>(biased_byte) - 128.0f;
-    return mul(c * fabsf(c), q);
+    const float rq = __builtin_amdgcn_rcpf(q);
+    uint32_t r = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (V) {
+            r = __builtin_amdgcn_cvt_pk_u8_f32(encode<true, SR>(x[k], root[k], q, rq, w.x[k] >> 16), k, r);
+        } else {
+            const float c = encode<false, SR>(fabsf(x[k]), 0.0f, q, rq, w.x[k] & 0xffffu);
+            r = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(c, x[k]) + 128.0f, k, r);
+        }
+    }
+    return q > 0.0f ? (V ? r : r ^ 0x80808080u) : 0u;
 }
 
-__device__ __forceinline__ float decode_v(uint32_t byte, float q) { return code_value<true>(static_cast<float>(byte), q); }
-
-// m codes are int8; the bytes are handled with 128 added (one exclusive-or per four of them)
-constexpr uint32_t kBias4 = 0x80808080u;
-
-__device__ __forceinline__ uint32_t byte_of(uint32_t w, int j) { return (w >> (8 * j)) & 0xffu; }
-
-__device__ __forceinline__ uint32_t put_byte(float k, int j, uint32_t w)
+// The values of four stored codes.
+template <bool V>
+__device__ __forceinline__ void decode4(uint32_t w, float q, float x[4])
 {
-    return __builtin_amdgcn_cvt_pk_u8_f32(k, j, w);
+    if (!V) w ^= 0x80808080u;   // int8 codes plus 128
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float c = static_cast<float>((w >> (8 * k)) & 0xffu);
+        x[k] = V ? code_value<true>(c, q) : mul((c - 128.0f) * fabsf(c - 128.0f), q);
+    }
+}
+
+// A lane's four codes, `cnt` of them in the tensor (4 or more: all).
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const void* codes, int64_t i, int cnt)
+{
+    const uint8_t* c = static_cast<const uint8_t*>(codes) + i;
+    if (FULL || cnt >= 4) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(c));
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < cnt) w |= static_cast<uint32_t>(c[k]) << (8 * k);
+    return w;
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store_codes(void* codes, int64_t i, int cnt, uint32_t w)
+{
+    uint8_t* c = static_cast<uint8_t*>(codes) + i;
+    if (FULL || cnt >= 4) {
+        __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(c));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < cnt) c[k] = static_cast<uint8_t>(w >> (8 * k));
+}
+
+// Scales of a span's blocks, the first `blocks` of them there; sb: the first block.
+template <bool FULL>
+__device__ __forceinline__ f4 load_scales(const float* q, int64_t sb, int blocks)
+{
+    if (FULL) return *reinterpret_cast<const f4e*>(q + sb);
+    f4 r{};
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j)
+        if (j < blocks) r[j] = q[sb + j];
+    return r;
+}
+
+template <bool FULL>
+__device__ __forceinline__ void store_scales(float* mq, float* vq, int64_t sb, int blocks, const SpanScales& s)
+{
+    const int lane = static_cast<int>(threadIdx.x) & 63, j = (lane >> 4) & 1;
+    if ((lane & 15) != 0) return;
+    float* q = (lane < 32 ? mq : vq) + sb + j;
+    if (FULL || j < blocks) q[0] = s.a;
+    if (FULL || j + 2 < blocks) q[2] = s.b;
 }
 
 }  // namespace

@@ -10,7 +10,6 @@ namespace {
 // over the gradients, then one block over the partial sums
 // ------------------------------------------------------------------------------------------------
 
-typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
 
 template <int G>
@@ -94,119 +93,124 @@ __global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, in
         return;
     }
     const int64_t t = ctl->step + 1;
+    const double bc1 = 1.0 - pow(np.beta1, static_cast<double>(t)), bc2 = 1.0 - pow(np.beta2, static_cast<double>(t));
     ctl->step = t;
-    ctl->bc1 = 1.0 - pow(np.beta1, static_cast<double>(t));
-    ctl->bc2 = 1.0 - pow(np.beta2, static_cast<double>(t));
+    ctl->bc1 = bc1;
+    ctl->bc2 = bc2;
+    ctl->inv_bc1 = static_cast<float>(1.0 / bc1);
+    ctl->inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
 }
 
 // ------------------------------------------------------------------------------------------------
 // the 8-bit format: one state block per wave and trip
 // ------------------------------------------------------------------------------------------------
 
-template <bool V>
-__device__ __forceinline__ void encode_block(int64_t at, int64_t cnt, int lane, const float* __restrict__ x,
-                                             uint8_t* __restrict__ codes, float* __restrict__ scales)
+// The lane's four elements of x that are in the array; zeros behind it.
+template <bool FULL>
+__device__ __forceinline__ void load4(const float* __restrict__ x, int64_t i, int64_t left, float e[4])
 {
-    float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int64_t i = at + 4 * lane;
-    const int64_t left = cnt - 4 * lane;
-    if (left >= 4) {
+    if (FULL || left >= 4) {
         const f4 r = ld4<true>(x, i);
 #pragma unroll
         for (int k = 0; k < 4; ++k) e[k] = r[k];
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < left) e[k] = x[i + k];
+        return;
     }
-    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t b = __float_as_uint(e[k]);
-        if (V && b > 0x80000000u) b = kInfBits + 1;   // a negative v counts as NaN (-0 does not)
-        b &= 0x7fffffffu;
-        top = top > b ? top : b;
-    }
-    const float q = block_scale<V>(wave_max(top));
-    const float rq = guess_scale(q);
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (V) {
-            w = put_byte(encode<true, false>(e[k], __builtin_amdgcn_sqrtf(e[k]), q, rq, 0), k, w);
-        } else {
-            const float c = encode<false, false>(fabsf(e[k]), 0.0f, q, rq, 0);
-            w = put_byte(copysignf(c, e[k]) + 128.0f, k, w);
-        }
-    }
-    if (!V) w ^= kBias4;
-    if (lane == 0) scales[at / kStateBlock] = q;
-    if (left >= 4) {
-        *reinterpret_cast<uint32_t*>(codes + i) = w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < left) codes[i + k] = static_cast<uint8_t>(byte_of(w, k));
-    }
+    for (int k = 0; k < 4; ++k) e[k] = k < left ? x[i + k] : 0.0f;
 }
 
-template <bool V>
-__device__ __forceinline__ void decode_block(int64_t at, int64_t cnt, int lane, const uint8_t* __restrict__ codes,
-                                             const float* __restrict__ scales, float* __restrict__ x)
+template <bool FULL>
+__device__ __forceinline__ void encode_span(int64_t n, int64_t at, const float* m, const float* v, uint8_t* mc, float* mq,
+                                            uint8_t* vc, float* vq)
 {
-    const int64_t i = at + 4 * lane;
-    const int64_t left = cnt - 4 * lane;
-    const float q = scales[at / kStateBlock];
-    if (left >= 4) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + i) ^ (V ? 0u : kBias4);
-        f4 r;
+    const int lane4 = 4 * (static_cast<int>(threadIdx.x) & 63);
+    const int left = FULL ? kSpanElems : static_cast<int>(n - at), blocks = (left + kStateBlock - 1) / kStateBlock;
+    float me[kSpan][4] = {}, ve[kSpan][4] = {}, root[kSpan][4];
+    uint32_t tm[kSpan] = {}, tv[kSpan] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = V ? decode_v(byte_of(w, k), q) : decode_m(byte_of(w, k), q);
-        st4<true>(x, i, r);
-    } else {
+    for (int j = 0; j < kSpan; ++j) {
+        const int o = j * kStateBlock + lane4;
+        if (m) load4<FULL>(m, at + o, left - o, me[j]);
+        if (v) load4<FULL>(v, at + o, left - o, ve[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (k >= left) continue;
-            const uint32_t b = codes[i + k];
-            x[i + k] = V ? decode_v(b, q) : decode_m(b ^ 0x80u, q);
+            tm[j] = max_u(tm[j], __float_as_uint(me[j][k]) & 0x7fffffffu);
+            ve[j][k] += 0.0f;                              // -0 becomes +0, so that
+            tv[j] = max_u(tv[j], __float_as_uint(ve[j][k]));   // a set sign is a negative v or a NaN
+            root[j][k] = __builtin_amdgcn_sqrtf(ve[j][k]);
+        }
+    }
+    const SpanScales q = span_scales(tm, tv);
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    if (lane < 32 ? m != nullptr : v != nullptr) store_scales<FULL>(mq, vq, at / kStateBlock, blocks, q);
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int o = j * kStateBlock + lane4;
+        if (m) store_codes<FULL>(mc, at + o, left - o, encode4<false, false>(me[j], nullptr, q.get(j, false), u4{}));
+        if (v) store_codes<FULL>(vc, at + o, left - o, encode4<true, false>(ve[j], root[j], q.get(j, true), u4{}));
+    }
+}
+
+template <bool FULL, bool V>
+__device__ __forceinline__ void decode_span(int64_t n, int64_t at, const uint8_t* codes, const float* scales, float* x)
+{
+    const int lane4 = 4 * (static_cast<int>(threadIdx.x) & 63);
+    const int left = FULL ? kSpanElems : static_cast<int>(n - at), blocks = (left + kStateBlock - 1) / kStateBlock;
+    const f4 q = load_scales<FULL>(scales, at / kStateBlock, blocks);
+    uint32_t w[kSpan];
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) w[j] = load_codes<FULL>(codes, at + j * kStateBlock + lane4, left - j * kStateBlock - lane4);
+#pragma unroll
+    for (int j = 0; j < kSpan; ++j) {
+        const int o = j * kStateBlock + lane4;
+        float e[4];
+        decode4<V>(w[j], q[j], e);
+        if (FULL || left - o >= 4) {
+            const f4 r = {e[0], e[1], e[2], e[3]};
+            st4<true>(x, at + o, r);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < left - o) x[at + o + k] = e[k];
         }
     }
 }
 
-// A block of the launch takes kSpan state blocks per wave, of m and of v.
-constexpr int kSpan = 4;
+constexpr int64_t kState8Elems = int64_t(kListBlock / 64) * kSpanElems;   // per block of the launch
+
+__device__ __forceinline__ int64_t span_start()
+{
+    return static_cast<int64_t>(blockIdx.x) * kState8Elems +
+           __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * kSpanElems;
+}
 
 __global__ __launch_bounds__(kListBlock) void k_state8_encode(int64_t n, const float* m, const float* v, uint8_t* mc,
                                                               float* mq, uint8_t* vc, float* vq)
 {
-    const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kListBlock / 64) + wave) * kSpan * kStateBlock;
-    for (int j = 0; j < kSpan; ++j) {
-        const int64_t at = first + j * kStateBlock, cnt = n - at;
-        if (cnt <= 0) return;
-        if (m) encode_block<false>(at, cnt, lane, m, mc, mq);
-        if (v) encode_block<true>(at, cnt, lane, v, vc, vq);
-    }
+    const int64_t at = span_start();
+    if (n - at >= kSpanElems)
+        encode_span<true>(n, at, m, v, mc, mq, vc, vq);
+    else if (n > at)
+        encode_span<false>(n, at, m, v, mc, mq, vc, vq);
 }
 
 __global__ __launch_bounds__(kListBlock) void k_state8_decode(int64_t n, const uint8_t* mc, const float* mq,
                                                               const uint8_t* vc, const float* vq, float* m, float* v)
 {
-    const int wave = static_cast<int>(threadIdx.x) >> 6, lane = static_cast<int>(threadIdx.x) & 63;
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kListBlock / 64) + wave) * kSpan * kStateBlock;
-    for (int j = 0; j < kSpan; ++j) {
-        const int64_t at = first + j * kStateBlock, cnt = n - at;
-        if (cnt <= 0) return;
-        if (m) decode_block<false>(at, cnt, lane, mc, mq, m);
-        if (v) decode_block<true>(at, cnt, lane, vc, vq, v);
+    const int64_t at = span_start();
+    if (n - at >= kSpanElems) {
+        if (m) decode_span<true, false>(n, at, mc, mq, m);
+        if (v) decode_span<true, true>(n, at, vc, vq, v);
+    } else if (n > at) {
+        if (m) decode_span<false, false>(n, at, mc, mq, m);
+        if (v) decode_span<false, true>(n, at, vc, vq, v);
     }
 }
 
-unsigned state8_grid(int64_t n)
-{
-    constexpr int64_t per = int64_t(kListBlock / 64) * kSpan * kStateBlock;
-    return static_cast<unsigned>((n + per - 1) / per);
-}
+unsigned state8_grid(int64_t n) { return static_cast<unsigned>((n + kState8Elems - 1) / kState8Elems); }
 
 }  // namespace
 

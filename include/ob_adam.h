@@ -319,7 +319,7 @@ typedef struct ob_tensors_s* ob_tensors;
 
 /* sizes: T >= 0 host int64, each >= 0.  g_dtypes, p_dtypes: T ob_dtype values each (OB_F32, OB_BF16 or
  * OB_F16).  lr_mults, wd_mults: T host factors of the rate and of the weight decay (parameter groups), or
- * NULL for 1; finite.  At most 2^31 - 1 work blocks of 4096 elements in all (OB_ERR_ARG beyond).  The list belongs to the
+ * NULL for 1; finite.  At most 2^31 - 1 work blocks of 2048 elements in all (OB_ERR_ARG beyond).  The list belongs to the
  * device that is current here; it owns its device tables (hipMalloc here, hipFree in ob_tensors_destroy). */
 ob_status ob_tensors_create(int64_t n_tensors, const int64_t* sizes, const int32_t* g_dtypes, const int32_t* p_dtypes,
                             const float* lr_mults, const float* wd_mults, ob_tensors* out);
@@ -354,7 +354,9 @@ typedef struct {
     double bc1, bc2;     /* 1 - beta1^t, 1 - beta2^t */
     float lr_scale;      /* written by the caller: factor of the rate (schedules under a captured graph) */
     int32_t skip;        /* 1: the norm was not finite, and a step with this block changes nothing */
-    uint32_t reserved[4];
+    float inv_bc1;       /* 1 / bc1 */
+    float inv_root_bc2;  /* 1 / sqrt(bc2) */
+    uint32_t reserved[2];
 } ob_control;
 #define OB_CONTROL_PARTIALS 2048
 #define OB_CONTROL_BYTES (64 + 8 * OB_CONTROL_PARTIALS)
