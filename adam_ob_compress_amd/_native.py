@@ -124,6 +124,20 @@ def lib() -> ctypes.CDLL:
     return L
 
 
+_torch_module = None
+
+
+def _obtorch():
+    """Load the _obtorch module (raises if it has not been built)."""
+    global _torch_module
+    if _torch_module is None:
+        if not os.path.exists(os.path.join(_PKG, "_obtorch.so")):
+            raise RuntimeError(f"{_PKG}/_obtorch.so is missing: build it with __graft_entry__.build()")
+        from . import _obtorch as module
+        _torch_module = module
+    return _torch_module
+
+
 def ob_status_str(status: int) -> str:
     return lib().ob_status_str(status).decode()
 
@@ -408,8 +422,12 @@ class Tensors:
         self.g_dtypes = tuple(g_dtypes)
         self.p_dtypes = tuple(p_dtypes)
         self.device = device
-        self._array = ctypes.c_void_p * len(self.sizes)
         self.state_elems = int(lib().ob_tensors_state_elems(handle))
+        T = len(self.sizes)
+        self._array = ctypes.c_void_p * T
+        self._numels = (ctypes.c_int64 * T)(*self.sizes)
+        self._codes = {ds: (ctypes.c_int8 * T)(*[_obtorch().scalar_type(d) for d in ds])
+                       for ds in (self.g_dtypes, self.p_dtypes)}
 
     def __len__(self) -> int:
         return len(self.sizes)
@@ -434,32 +452,36 @@ class Tensors:
 
     def _pointers(self, tensors, name, dtypes, others=None):
         """The list's tensors as an array of device addresses; None (for others: where others has None) -> NULL."""
+        if not isinstance(tensors, (list, tuple)):
+            tensors = list(tensors)
         if len(tensors) != len(self.sizes):
             raise ValueError(f"{name} must have {len(self.sizes)} tensors, got {len(tensors)}")
         out = self._array()
-        index = self.device.index
-        for j, t in enumerate(tensors):
-            if t is None:
-                if others is not None and others[j] is not None:
-                    raise TypeError(f"{name}[{j}] must be a torch.Tensor")
-                continue
-            if (t.dtype is not dtypes[j] or t.numel() != self.sizes[j] or t.get_device() != index
-                    or not t.is_contiguous()):
-                self._refuse(t, f"{name}[{j}]", dtypes[j], self.sizes[j])
-            out[j] = t.data_ptr()
+        j = _obtorch().pointers(tensors, others, ctypes.addressof(self._numels), ctypes.addressof(self._codes[dtypes]),
+                                self.device.index, ctypes.addressof(out))
+        if j >= 0:
+            if tensors[j] is None:
+                raise TypeError(f"{name}[{j}] must be a torch.Tensor")
+            self._refuse(tensors[j], f"{name}[{j}]", dtypes[j], self.sizes[j])
         return out
 
     def _refuse(self, t, name, dtype, numel):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.layout is not torch.strided:
+            raise ValueError(f"{name} must be a dense tensor, got {t.layout}")
         _want(t, name, dtype, numel)
         _dev(t, name)
+        if t.is_neg():
+            raise ValueError(f"{name} must not be a negated view")
         raise ValueError(f"{name} must be on {self.device}, the list's device (got {t.device})")
 
     def _flat(self, t, name, dtype, numel):
         """Device address of a flat state buffer on the list's device (None -> NULL)."""
         if t is None:
             return None
-        _want(t, name, dtype, numel)
-        if t.get_device() != self.device.index or not t.is_contiguous():
+        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != numel
+                or t.get_device() != self.device.index or not t.is_contiguous()):
             self._refuse(t, name, dtype, numel)
         return t.data_ptr()
 
@@ -523,7 +545,7 @@ def _control_ptr(tensors: Tensors, control):
 
 def _list_stream(tensors: Tensors, stream):
     if stream is None:
-        stream = torch.cuda.current_stream(tensors.device)
+        return torch._C._cuda_getCurrentRawStream(tensors.device.index)  # what current_stream() wraps, at 1/25 of its time
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -563,43 +585,47 @@ def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, 
                                 _list_stream(tensors, stream)), "ob_adamw8_step")
 
 
-def _state8_args(m, v, m_codes, m_scales, v_codes, v_scales):
-    """(n, device) of a conversion's tensors, checked; either moment may be None throughout."""
-    some = [t for t in (m, v, m_codes, m_scales, v_codes, v_scales) if t is not None]
-    if not some:
-        raise ValueError("neither moment is given")
+def _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales):
+    """(n, device index, addresses in this order) of a conversion's tensors, checked; either moment may be None
+    throughout."""
     lead = m if m is not None else v
     if lead is None:
-        raise ValueError("codes and scales come with their fp32 moments")
+        raise ValueError("neither moment is given")
     n = lead.numel()
     blocks = -(-n // OB_STATE_BLOCK)
-    for x, codes, scales, name, dtype in ((m, m_codes, m_scales, "m", torch.int8), (v, v_codes, v_scales, "v", torch.uint8)):
-        if (x is None) != (codes is None) or (x is None) != (scales is None):
-            raise ValueError(f"{name}, {name}_codes and {name}_scales come together")
-        _want(x, name, torch.float32, n)
-        _want(codes, f"{name}_codes", dtype, n)
-        _want(scales, f"{name}_scales", torch.float32, blocks)
-    for t in some:
-        if t.device != lead.device:
-            raise ValueError(f"all tensors must be on {lead.device} (got {t.device})")
-    return n
+    args = ((m, "m", torch.float32, n, m), (v, "v", torch.float32, n, v), (m_codes, "m_codes", torch.int8, n, m),
+            (m_scales, "m_scales", torch.float32, blocks, m), (v_codes, "v_codes", torch.uint8, n, v),
+            (v_scales, "v_scales", torch.float32, blocks, v))
+    for t, name, dtype, want, x in args:
+        if (t is None) != (x is None):
+            raise ValueError(f"{name[0]}, {name[0]}_codes and {name[0]}_scales come together")
+        if t is not None and (t.dtype is not dtype or t.numel() != want):
+            _want(t, name, dtype, want)
+    index = lead.get_device()
+    out = []
+    for t, name, _, _, _ in args:
+        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
+            _dev(t, name)
+            raise ValueError(f"{name} must be on {lead.device} (got {t.device})")
+        out.append(None if t is None else t.data_ptr())
+    return n, index, out
+
+
+def _on_device(index, stream, call):
+    """call(raw stream) with the device current, as a call without a handle of its own needs it."""
+    if index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    with torch.cuda.device(index):
+        return call(_stream(stream))
 
 
 def ob_state8_encode(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
     """fp32 moments into the 8-bit format, rounded to nearest (m or v with its codes and scales: None)."""
-    n = _state8_args(m, v, m_codes, m_scales, v_codes, v_scales)
-    a = [_dev(t, name) for t, name in ((m, "m"), (v, "v"), (m_codes, "m_codes"), (m_scales, "m_scales"),
-                                       (v_codes, "v_codes"), (v_scales, "v_scales"))]
-    dev = (m if m is not None else v).device
-    with torch.cuda.device(dev):
-        _check(lib().ob_state8_encode(n, *a, _stream(stream)), "ob_state8_encode")
+    n, index, a = _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales)
+    _check(_on_device(index, stream, lambda s: lib().ob_state8_encode(n, *a, s)), "ob_state8_encode")
 
 
 def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
     """The fp32 moments that 8-bit codes and scales stand for (m or v with its codes and scales: None)."""
-    n = _state8_args(m, v, m_codes, m_scales, v_codes, v_scales)
-    a = [_dev(t, name) for t, name in ((m_codes, "m_codes"), (m_scales, "m_scales"), (v_codes, "v_codes"),
-                                       (v_scales, "v_scales"), (m, "m"), (v, "v"))]
-    dev = (m if m is not None else v).device
-    with torch.cuda.device(dev):
-        _check(lib().ob_state8_decode(n, *a, _stream(stream)), "ob_state8_decode")
+    n, index, (pm, pv, *codes) = _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales)
+    _check(_on_device(index, stream, lambda s: lib().ob_state8_decode(n, *codes, pm, pv, s)), "ob_state8_decode")

@@ -75,5 +75,26 @@ def build_probe(verbose: bool = False) -> str:
     return PROBE_LIB
 
 
+TORCH_SRC = os.path.join(CSRC, "ob_torch.cpp")
+TORCH_LIB = os.path.join(PKG, "_obtorch.so")
+
+
+def build_torch(verbose: bool = False) -> str:
+    """Compile the Python module that reads device addresses out of lists of torch tensors."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{root}/include",
+           f"-I{root}/include/torch/csrc/api/include", "-I" + sysconfig.get_paths()["include"], "-o", TORCH_LIB + ".tmp",
+           TORCH_SRC, f"-L{root}/lib", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
+    return TORCH_LIB
+
+
 if __name__ == "__main__":
     build(verbose=True, extra=sys.argv[1:])

@@ -72,14 +72,17 @@ template <int G>
 hipError_t launch_adamw8(const ListLaunch& L, const ListPtrs& ptrs, int pk, const State8& st, const AdamWParams& ap,
                          hipStream_t s);
 
-// Sums of squares of the launch's gradients by blocks into partials[0..grid); first: written, else added.
-hipError_t launch_grad_sumsq(const ListLaunch& L, const NormPtrs& ptrs, int g_dtype, int grid, int first,
-                             double* partials, hipStream_t s);
 struct NormParams {
-    double g_mult, max_norm;     // max_norm <= 0: no clipping
-    double beta1, beta2;
-    int clip, advance;
+    double g_mult, max_norm, beta1, beta2;
+    int clip, advance;   // clip to max_norm; count the step
+    int first;           // the call's first launch: partial sums are written, else added to
+    int ticket;          // this launch finishes the norm
 };
+// Sums of squares of the launch's gradients into the control block's partial sums [0, grid).  Items below
+// nt_items are read nontemporally.
+hipError_t launch_grad_sumsq(const ListLaunch& L, const NormPtrs& ptrs, int g_dtype, int grid, int64_t nt_items,
+                             ob_control* ctl, const NormParams& np, hipStream_t s);
+// The control block from them, after the last launch of a call.
 hipError_t launch_grad_control(ob_control* ctl, int grid, const NormParams& np, hipStream_t s);
 
 hipError_t launch_state8_encode(int64_t n, const float* m, const float* v, int8_t* mc, float* mq, uint8_t* vc,

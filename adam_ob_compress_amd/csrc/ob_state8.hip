@@ -10,7 +10,7 @@ namespace {
 // over the gradients, then one block over the partial sums
 // ------------------------------------------------------------------------------------------------
 
-typedef uint32_t u2e __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u4e __attribute__((ext_vector_type(4), aligned(2)));
 
 template <int G>
 __device__ __forceinline__ float load_grad1(const void* g, int64_t i)
@@ -20,64 +20,39 @@ __device__ __forceinline__ float load_grad1(const void* g, int64_t i)
     return G == 1 ? __uint_as_float(h << 16) : ErrF16::widen(h);
 }
 
-template <int G>
-__device__ __forceinline__ f4 load_grad4(const void* g, int64_t i)
-{
-    if (G == 0) return *reinterpret_cast<const f4e*>(static_cast<const float*>(g) + i);
-    const u2e u = *reinterpret_cast<const u2e*>(static_cast<const uint16_t*>(g) + i);
-    f4 r;
-    if (G == 1) {
-        r.x = __uint_as_float(u.x << 16);
-        r.y = __uint_as_float(u.x & 0xffff0000u);
-        r.z = __uint_as_float(u.y << 16);
-        r.w = __uint_as_float(u.y & 0xffff0000u);
-    } else {
-        r.x = ErrF16::widen(u.x & 0xffffu);
-        r.y = ErrF16::widen(u.x >> 16);
-        r.z = ErrF16::widen(u.y & 0xffffu);
-        r.w = ErrF16::widen(u.y >> 16);
-    }
-    return r;
-}
+__device__ __forceinline__ void add_square(float x, double& s) { s = fma(static_cast<double>(x), static_cast<double>(x), s); }
 
+// Sum of the squares in 16 bytes of gradients into two sums (the second shortens the chain of additions).
 template <int G>
-__global__ __launch_bounds__(kListBlock) void k_grad_sumsq(ListLaunch L, NormPtrs ptrs, int first,
-                                                           double* __restrict__ partials)
+__device__ __forceinline__ void add_squares(u4e u, double s[2])
 {
-    __shared__ double lds[kListBlock / 64];
-    double s = 0.0;
-    for (int64_t b = blockIdx.x; b < L.n_items; b += gridDim.x) {
-        const ListItem it = L.items[b];
-        const void* g = ptrs.g[it.tensor - L.tensor0];
-        if (g == nullptr) continue;
-        for (int base = 0; base < it.len; base += kListTile) {
-            const int at = base + 4 * static_cast<int>(threadIdx.x);
-            const int cnt = it.len - at;
-            if (cnt >= 4) {
-                const f4 x = load_grad4<G>(g, it.start + at);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s = fma(static_cast<double>(x[k]), static_cast<double>(x[k]), s);
-            } else {
-                for (int k = 0; k < cnt; ++k) {
-                    const double x = static_cast<double>(load_grad1<G>(g, it.start + at + k));
-                    s = fma(x, x, s);
-                }
-            }
+    for (int k = 0; k < 4; ++k) {
+        if (G == 0) {
+            add_square(__uint_as_float(u[k]), s[k & 1]);
+        } else {
+            add_square(G == 1 ? __uint_as_float(u[k] << 16) : ErrF16::widen(u[k] & 0xffffu), s[0]);
+            add_square(G == 1 ? __uint_as_float(u[k] & 0xffff0000u) : ErrF16::widen(u[k] >> 16), s[1]);
         }
     }
-    s = block_sum(s, lds);
-    if (threadIdx.x == 0) partials[blockIdx.x] = first ? s : partials[blockIdx.x] + s;
 }
 
-__global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, int grid, NormParams np)
+// What the norm's last block writes into the control block: s is the sum of all squares.  Threads 0 and 1
+// take one bias correction each; both are lanes of one wave.
+__device__ __forceinline__ void write_control(ob_control* ctl, double s, const NormParams& np)
 {
-    __shared__ double lds[kListBlock / 64];
-    const double* partials = reinterpret_cast<const double*>(ctl + 1);
-    double s = 0.0;
-    for (int b = threadIdx.x; b < grid; b += kListBlock) s += partials[b];
-    s = block_sum(s, lds);
-    if (threadIdx.x != 0) return;
+    if (threadIdx.x > 1) return;
     const double norm = fabs(np.g_mult) * sqrt(s);
+    const bool ok = (__float_as_uint(static_cast<float>(norm)) & 0x7fffffffu) < kInfBits;
+    const int64_t t = ctl->step + 1;
+    const double bc = np.advance ? 1.0 - pow(threadIdx.x == 0 ? np.beta1 : np.beta2, static_cast<double>(t)) : 1.0;
+    if (threadIdx.x == 1) {
+        if (np.advance && ok) {
+            ctl->bc2 = bc;
+            ctl->inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc));
+        }
+        return;
+    }
     double f = 1.0;
     if (np.clip) {
         f = np.max_norm / (norm + 1e-6);
@@ -85,20 +60,91 @@ __global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, in
     }
     ctl->norm = static_cast<float>(norm);
     ctl->grad_scale = static_cast<float>(np.g_mult * f);
-    const bool ok = (__float_as_uint(static_cast<float>(norm)) & 0x7fffffffu) < kInfBits;
     ctl->skip = ok ? 0 : 1;
     if (!np.advance) return;
-    if (!ok) {
+    if (ok) {
+        ctl->step = t;
+        ctl->bc1 = bc;
+        ctl->inv_bc1 = static_cast<float>(1.0 / bc);
+    } else {
         ctl->skipped += 1;
-        return;
     }
-    const int64_t t = ctl->step + 1;
-    const double bc1 = 1.0 - pow(np.beta1, static_cast<double>(t)), bc2 = 1.0 - pow(np.beta2, static_cast<double>(t));
-    ctl->step = t;
-    ctl->bc1 = bc1;
-    ctl->bc2 = bc2;
-    ctl->inv_bc1 = static_cast<float>(1.0 / bc1);
-    ctl->inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc2));
+}
+
+template <int G, bool NT>
+__device__ __forceinline__ void item_squares(const void* grad, const ListItem& it, double s[2])
+{
+    constexpr int V = G == 0 ? 4 : 8, U = 8, kTrip = V * kListBlock * U;
+    const char* g = static_cast<const char*>(grad) + it.start * (16 / V);
+    const int tid = static_cast<int>(threadIdx.x);
+    int base = 0;
+    for (; base + kTrip <= it.len; base += kTrip) {
+        u4e x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const u4e* at = reinterpret_cast<const u4e*>(g + int64_t(base) * (16 / V)) + u * kListBlock + tid;
+            x[u] = NT ? __builtin_nontemporal_load(at) : *at;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add_squares<G>(x[u], s);
+    }
+    for (; base < it.len; base += V * kListBlock) {   // a tensor's last item
+        const int at = base + V * tid, cnt = it.len - at;
+        if (cnt >= V) {
+            add_squares<G>(*reinterpret_cast<const u4e*>(g + int64_t(at) * (16 / V)), s);
+        } else {
+            for (int k = 0; k < cnt; ++k) add_square(load_grad1<G>(g, at + k), s[0]);
+        }
+    }
+}
+
+// The control block from the partial sums [0, grid), added in an order that the grid alone fixes.
+__device__ __forceinline__ void finish_norm(ob_control* ctl, unsigned grid, double* lds, const NormParams& np)
+{
+    const double* partials = reinterpret_cast<const double*>(ctl + 1);
+    double a = 0.0;
+    for (unsigned b = threadIdx.x; b < grid; b += kListBlock)
+        a += __hip_atomic_load(partials + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    write_control(ctl, block_sum(a, lds), np);
+}
+
+// A block takes every gridDim-th item, a lane 16 bytes of every 4 KB of it, eight of them in flight.  With np.ticket
+// the block that finishes last (by a ticket in the control block, which it sets back to zero) also finishes
+// the norm.
+template <int G>
+__global__ __launch_bounds__(kListBlock) void k_grad_sumsq(ListLaunch L, NormPtrs ptrs, int64_t nt_items, ob_control* ctl,
+                                                           NormParams np)
+{
+    __shared__ double lds[kListBlock / 64];
+    __shared__ bool last;
+    double* partials = reinterpret_cast<double*>(ctl + 1);
+    double s[2] = {0.0, 0.0};
+    for (int64_t b = blockIdx.x; b < L.n_items; b += gridDim.x) {
+        const ListItem it = L.items[b];
+        const void* g = ptrs.g[it.tensor - L.tensor0];
+        if (g == nullptr) continue;
+        if (b < nt_items)
+            item_squares<G, true>(g, it, s);
+        else
+            item_squares<G, false>(g, it, s);
+    }
+    const double t = block_sum(s[0] + s[1], lds);
+    if (threadIdx.x == 0) {
+        double* mine = partials + blockIdx.x;
+        __hip_atomic_store(mine, np.first ? t : *mine + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = np.ticket && __hip_atomic_fetch_add(&ctl->ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                                gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    if (threadIdx.x == 0) ctl->ticket = 0;
+    finish_norm(ctl, gridDim.x, lds, np);
+}
+
+__global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, unsigned grid, NormParams np)
+{
+    __shared__ double lds[kListBlock / 64];
+    finish_norm(ctl, grid, lds, np);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -214,20 +260,17 @@ unsigned state8_grid(int64_t n) { return static_cast<unsigned>((n + kState8Elems
 
 }  // namespace
 
-hipError_t launch_grad_sumsq(const ListLaunch& L, const NormPtrs& ptrs, int g_dtype, int grid, int first,
-                             double* partials, hipStream_t s)
+hipError_t launch_grad_sumsq(const ListLaunch& L, const NormPtrs& ptrs, int g_dtype, int grid, int64_t nt_items,
+                             ob_control* ctl, const NormParams& np, hipStream_t s)
 {
-    switch (g_dtype) {
-    case OB_BF16: hipLaunchKernelGGL(k_grad_sumsq<1>, dim3(grid), dim3(kListBlock), 0, s, L, ptrs, first, partials); break;
-    case OB_F16: hipLaunchKernelGGL(k_grad_sumsq<2>, dim3(grid), dim3(kListBlock), 0, s, L, ptrs, first, partials); break;
-    default: hipLaunchKernelGGL(k_grad_sumsq<0>, dim3(grid), dim3(kListBlock), 0, s, L, ptrs, first, partials);
-    }
+    const auto k = g_dtype == OB_BF16 ? k_grad_sumsq<1> : g_dtype == OB_F16 ? k_grad_sumsq<2> : k_grad_sumsq<0>;
+    hipLaunchKernelGGL(k, dim3(grid), dim3(kListBlock), 0, s, L, ptrs, nt_items, ctl, np);
     return hipGetLastError();
 }
 
 hipError_t launch_grad_control(ob_control* ctl, int grid, const NormParams& np, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_grad_control, dim3(1), dim3(kListBlock), 0, s, ctl, grid, np);
+    hipLaunchKernelGGL(k_grad_control, dim3(1), dim3(kListBlock), 0, s, ctl, static_cast<unsigned>(grid), np);
     return hipGetLastError();
 }
 

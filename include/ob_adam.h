@@ -356,7 +356,8 @@ typedef struct {
     int32_t skip;        /* 1: the norm was not finite, and a step with this block changes nothing */
     float inv_bc1;       /* 1 / bc1 */
     float inv_root_bc2;  /* 1 / sqrt(bc2) */
-    uint32_t reserved[2];
+    uint32_t ticket;     /* the norm's own: 0 between calls */
+    uint32_t reserved;
 } ob_control;
 #define OB_CONTROL_PARTIALS 2048
 #define OB_CONTROL_BYTES (64 + 8 * OB_CONTROL_PARTIALS)
