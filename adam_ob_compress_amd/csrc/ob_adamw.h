@@ -27,11 +27,6 @@ struct NormPtrs {
     const void* g[kNormPtrs];
 };
 
-// Tiles per work block of the step with fp32 states, and elements per block of either step.
-constexpr int kTiles32 = 2;
-constexpr int kStepElems32 = kTiles32 * kListTile;
-constexpr int kStepElems8 = 4 * kListTile;
-
 // How a tensor's parameters are held.
 enum { PK_F32 = 0, PK_BF16 = 1, PK_F16 = 2, PK_MASTER_BF16 = 3, PK_MASTER_F16 = 4, kParKinds = 5 };
 
@@ -44,7 +39,7 @@ struct ListLaunch {
 
 struct AdamWParams {
     double lr, beta1, one_m_beta1, beta2, one_m_beta2, eps, wd, bc1, bc2;
-    float inv_bc1, inv_root_bc2; // 1 / bc1, 1 / sqrt(bc2)
+    float root_factor;           // bc1 / sqrt(bc2)
     int bias_correction;
     int stochastic;
     uint64_t seed, step;

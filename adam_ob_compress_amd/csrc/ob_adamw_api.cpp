@@ -21,13 +21,14 @@ struct Table {
 struct ob_tensors_s {
     int device = 0;
     ob::ListShape shape;
-    Table step32, step8, norm;
+    Table step, norm;
     ob::ListTensor* d_tensors = nullptr;        // by place
 };
 
 namespace {
 
-// Elements per work block of the norm.
+// Elements per item of the steps and of the norm.
+constexpr int64_t kStepElems = ob::kStepTiles * ob::kListTile;
 constexpr int64_t kNormElems = 16 * ob::kListTile;
 // Gradient bytes at a call's end that the norm reads with ordinary loads, which leave them in the last-level
 // cache for the step that follows; what comes before is read nontemporally, which is faster.  Norm and step
@@ -60,8 +61,7 @@ struct DeviceGuard {
 void free_list(ob_tensors l)
 {
     if (!l) return;
-    if (l->step32.d_items) (void)hipFree(l->step32.d_items);
-    if (l->step8.d_items) (void)hipFree(l->step8.d_items);
+    if (l->step.d_items) (void)hipFree(l->step.d_items);
     if (l->norm.d_items) (void)hipFree(l->norm.d_items);
     if (l->d_tensors) (void)hipFree(l->d_tensors);
     delete l;
@@ -83,17 +83,15 @@ ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const 
     *out = nullptr;
     l = new ob_tensors_s;
     if (ob_status st = ob::build_shape(T, sizes, gd, pd, lr, wd, l->shape)) return st;
-    std::vector<ob::ListItem> step32, step8, norm;
-    if (!ob::build_items(l->shape, ob::kStepElems32, step32, l->step32.first) ||
-        !ob::build_items(l->shape, ob::kStepElems8, step8, l->step8.first) ||
+    std::vector<ob::ListItem> step, norm;
+    if (!ob::build_items(l->shape, kStepElems, step, l->step.first) ||
         !ob::build_items(l->shape, kNormElems, norm, l->norm.first))
         return OB_ERR_ARG;
     std::vector<ob::ListTensor> tensors;
     for (int32_t t : l->shape.order) tensors.push_back({l->shape.state_off[t], lr ? lr[t] : 1.0f, wd ? wd[t] : 1.0f});
 
     if (hipGetDevice(&l->device) != hipSuccess) return OB_ERR_HIP;
-    hipError_t e = upload(&l->step32.d_items, step32);
-    if (e == hipSuccess) e = upload(&l->step8.d_items, step8);
+    hipError_t e = upload(&l->step.d_items, step);
     if (e == hipSuccess) e = upload(&l->norm.d_items, norm);
     if (e == hipSuccess) e = upload(&l->d_tensors, tensors);
     if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
@@ -118,8 +116,7 @@ ob::AdamWParams adamw_params(const ob_adamw_hparams* hp, const ob_control* contr
         ap.bc1 = 1.0 - std::pow(ap.beta1, static_cast<double>(hp->step));
         ap.bc2 = 1.0 - std::pow(ap.beta2, static_cast<double>(hp->step));
     }
-    ap.inv_bc1 = static_cast<float>(1.0 / ap.bc1);
-    ap.inv_root_bc2 = static_cast<float>(1.0 / std::sqrt(ap.bc2));
+    ap.root_factor = static_cast<float>(ap.bc1 / std::sqrt(ap.bc2));
     ap.seed = hp->sr_seed;
     ap.step = static_cast<uint64_t>(hp->step);
     ap.control = control;
@@ -128,14 +125,14 @@ ob::AdamWParams adamw_params(const ob_adamw_hparams* hp, const ob_control* contr
 
 // The launches of a step: f(gradient type, parameter kind, launch, addresses) for each.
 template <class F>
-ob_status launch_step(const ob_tensors_s& l, const Table& t, const void* const* g, void* const* p, bool master, F&& f)
+ob_status launch_step(const ob_tensors_s& l, const void* const* g, void* const* p, bool master, F&& f)
 {
     const ob::ListShape& sh = l.shape;
     ob::ListPtrs ptrs;
     return ob::for_runs(sh, ob::kListPtrs, true, [&](int64_t k, int64_t e) {
         ob::ListLaunch L;
-        L.items = t.d_items + t.first[k];
-        L.n_items = t.first[e] - t.first[k];
+        L.items = l.step.d_items + l.step.first[k];
+        L.n_items = l.step.first[e] - l.step.first[k];
         L.tensors = l.d_tensors;
         L.tensor0 = static_cast<int32_t>(k);
         if (L.n_items == 0) return OB_OK;
@@ -251,7 +248,7 @@ try {
     const ob::State32 state{master, m, v};
     DeviceGuard guard(list->device);
     if (!guard.ok) return OB_ERR_HIP;
-    return launch_step(*list, list->step32, g, p, master != nullptr,
+    return launch_step(*list, g, p, master != nullptr,
                        [&](int gd, int pk, const ob::ListLaunch& L, const ob::ListPtrs& ptrs) {
                            return gd == OB_BF16  ? ob::launch_adamw<OB_BF16>(L, ptrs, pk, state, ap, stream)
                                   : gd == OB_F16 ? ob::launch_adamw<OB_F16>(L, ptrs, pk, state, ap, stream)
@@ -275,7 +272,7 @@ try {
     const ob::State8 state{master, m_codes, m_scales, v_codes, v_scales};
     DeviceGuard guard(list->device);
     if (!guard.ok) return OB_ERR_HIP;
-    return launch_step(*list, list->step8, g, p, master != nullptr,
+    return launch_step(*list, g, p, master != nullptr,
                        [&](int gd, int pk, const ob::ListLaunch& L, const ob::ListPtrs& ptrs) {
                            return gd == OB_BF16  ? ob::launch_adamw8<OB_BF16>(L, ptrs, pk, state, ap, stream)
                                   : gd == OB_F16 ? ob::launch_adamw8<OB_F16>(L, ptrs, pk, state, ap, stream)

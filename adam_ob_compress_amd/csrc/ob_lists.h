@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 #include <numeric>
 #include <vector>
@@ -19,6 +18,7 @@ namespace ob {
 // consecutive elements (four per lane), a block's tile four of them.
 constexpr int kListBlock = 256;
 constexpr int kListTile = 1024;
+constexpr int kStepTiles = 4;   // tiles per item of the steps
 constexpr int kStateBlock = OB_STATE_BLOCK;
 
 // One work block: elements [start, start + len) of the tensor in place `tensor` of the list's order.
@@ -69,13 +69,14 @@ inline ob_status build_shape(int64_t T, const int64_t* sizes, const int32_t* gd,
 }
 
 // The work blocks of `elems` elements (a multiple of kListTile), in the list's order; first[k]: index of
-// the first block of the tensor in place k, first[T] the count.  False if the blocks would pass 2^31 - 1.
+// the first block of the tensor in place k, first[T] the count.  False if the tiles of the blocks, a launch's
+// most work groups, would pass 2^31 - 1.
 inline bool build_items(const ListShape& l, int64_t elems, std::vector<ListItem>& items, std::vector<int64_t>& first)
 {
     int64_t total = 0;
     for (int64_t n : l.size) {
         total += n / elems + (n % elems != 0);
-        if (total > INT32_MAX) return false;
+        if (total > INT32_MAX / (elems / kListTile)) return false;
     }
     items.reserve(static_cast<size_t>(total));
     for (size_t k = 0; k < l.order.size(); ++k) {
@@ -112,7 +113,7 @@ inline ob_status check_hparams(const ob_adamw_hparams* hp, bool eight, bool has_
     if (!hp) return OB_ERR_ARG;
     if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f)) return OB_ERR_ARG;
     if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay)) return OB_ERR_ARG;
-    if (!std::isfinite(hp->eps) || hp->eps < 0.0f || (eight && hp->eps < FLT_MIN)) return OB_ERR_ARG;
+    if (!std::isfinite(hp->eps) || hp->eps < 0.0f || (eight && hp->eps < 1e-30f)) return OB_ERR_ARG;
     if (hp->rounding != OB_ROUND_NEAREST && hp->rounding != OB_ROUND_STOCHASTIC) return OB_ERR_ARG;
     if (!has_control && hp->bias_correction && hp->step < 1) return OB_ERR_ARG;
     return OB_OK;

@@ -1,12 +1,12 @@
 // ob_state8.h -- device side of the 8-bit state format (the rules are in ob_adam.h) and of gradients
 // at any alignment.
 //
-// The codes are square-law: an m is c|c| q, a v is (k^2 q)^2.  Decoding costs two to three products; the
-// root that encoding needs is one v_sqrt_f32 per value.  That root is good to a few ulp, so it gives the
-// code or the one below it (its argument is lowered by 2^-13, far above its error and far below the
-// distance of two borders), and one comparison with the next border, which is an fp32 number by the format's rule,
-// settles which.  All values here are fp32 in single IEEE operations, so the codes are the same
-// wherever they are computed.
+// The codes are square-law: an m is c|c| q, a v is (k^2 q)^2, and the borders between codes are fp32 numbers by the
+// format's rule, so the codes are the same wherever they are computed.  What bounds the 8-bit step is the
+// vector ALU (1e9 bf16 parameters: about 60 operations each, at 33e12 a second), so a code is first taken from
+// the hardware's roots, rounded, together with its distance from the next border.  Only where a block has
+// an element closer to a border than the roots' error could reach (a few blocks in a hundred) are its codes
+// settled by comparing with the borders themselves.
 #pragma once
 
 #include "ob_adamw.h"
@@ -20,6 +20,12 @@ constexpr float kQuantV = 1.0f / 65025.0f;   // 1 / 255^2
 constexpr uint32_t kTinyBits = 0x0f800000u;  // 2^-96
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr float kBelow = 1.0f / 8192.0f;
+// How close to a border the first guess of a code is not trusted, in codes.  The guess y is off by y times the
+// relative error of its parts (1/q and root 1 ulp each, product half an ulp, under a root that halves them; for v
+// one root more; the borders' own roundings): at most 3.8e-5 for m (y <= 127) and 8e-5 for v (y <= 255).
+constexpr float kNearM = 1.0f / 16384.0f, kNearV = 1.0f / 8192.0f;
+// The same for chance, in units of the 16 random bits: below 1.6 for m and 4.2 for v.
+constexpr float kNearChanceM = 4.0f, kNearChanceV = 8.0f;
 
 typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -116,19 +122,41 @@ __device__ __forceinline__ float code_value(float k, float q)
     return V ? mul(r, r) : r;
 }
 
-// |code| of x >= 0 as a float, for a block with q > 0 (the caller replaces the codes of other blocks by
-// zeros).  rq: about 1/q; root: about sqrt(x) (V only); bits: 16 random bits (SR).
+// Philox4x32-10 (ob_device.h) at the counter (blk, t) with blk = base + lane: base is uniform and a multiple of the
+// lanes that add to it, so the counter's high word and all that depends on it alone stay in scalar registers.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
+
+__device__ __forceinline__ u4 philox_lanes(uint64_t seed, uint64_t t, int64_t base, uint32_t lane)
+{
+    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    uint32_t c0 = static_cast<uint32_t>(base) + lane, c1 = static_cast<uint32_t>(static_cast<uint64_t>(base) >> 32);
+    uint32_t c2 = static_cast<uint32_t>(t), c3 = static_cast<uint32_t>(t >> 32);
+#pragma unroll
+    for (int round = 0; round < 10; ++round) {
+        const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0, p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+        const uint32_t h0 = static_cast<uint32_t>(p0 >> 32), h1 = static_cast<uint32_t>(p1 >> 32);
+        // the first two rounds' scalar parts by plain xors
+        c0 = round < 1 ? h1 ^ c1 ^ k0 : xor3(h1, c1, k0);
+        c2 = round < 1 ? h0 ^ (c3 ^ k1) : xor3(h0, c3, k1);
+        c1 = static_cast<uint32_t>(p1);
+        c3 = static_cast<uint32_t>(p0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u4{{c0, c1, c2, c3}};
+}
+
+// |code| of x >= 0 as a float, by the rule, for a block with q > 0.  rq: about 1/q; root: about sqrt(x) (V
+// only); bits: 16 random bits (SR).
 template <bool V, bool SR>
-__device__ __forceinline__ float encode(float x, float root, float q, float rq, uint32_t bits)
+__device__ __forceinline__ float code_by_rule(float x, float root, float q, float rq, uint32_t bits)
 {
     constexpr float most = V ? 255.0f : 127.0f;
     const float y = __builtin_amdgcn_sqrtf((V ? root : x) * rq);
     float k;
     if (!SR) {
-        const float z = y + (0.5f - kBelow), h = floorf(z) + 0.5f;   // h: the next border
-        bool up = x >= code_value<V>(h, q);
-        if (V) up = up || (z < 1.0f && x > 0.0f);
-        k = h + (up ? 0.5f : -0.5f);
+        const float h = floorf(y + (0.5f - kBelow)) + 0.5f;   // the next border
+        k = h + (x >= code_value<V>(h, q) ? 0.5f : -0.5f);
     } else {
         k = fmaxf(floorf(y - kBelow), 0.0f);
         k += x >= code_value<V>(k + 1.0f, q) ? 1.0f : 0.0f;
@@ -136,9 +164,8 @@ __device__ __forceinline__ float encode(float x, float root, float q, float rq, 
         const float u = static_cast<float>(bits);
         k += mul(u, sub(high, low)) < mul(sub(x, low), 65536.0f) ? 1.0f : 0.0f;
         k = fminf(k, most);
-        if (V) k = x > 0.0f ? fmaxf(k, 1.0f) : k;
     }
-    return k;
+    return V && x > 0.0f ? fmaxf(k, 1.0f) : k;
 }
 
 // The codes of a lane's four elements of one block, as stored (int8 codes of m, uint8 of v).
@@ -147,14 +174,47 @@ __device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4
 {
     const float rq = __builtin_amdgcn_rcpf(q);
     uint32_t r = 0;
+    auto put = [&](float code, int k) {
+        r = __builtin_amdgcn_cvt_pk_u8_f32(V ? code : copysignf(code, x[k]) + 128.0f, k, r);   // rounds to nearest
+    };
+    auto bits = [&](int k) { return V ? w.x[k] >> 16 : w.x[k] & 0xffffu; };
+    bool near = false;
+    if (!SR) {
+        float d = 1.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (V) {
-            r = __builtin_amdgcn_cvt_pk_u8_f32(encode<true, SR>(x[k], root[k], q, rq, w.x[k] >> 16), k, r);
-        } else {
-            const float c = encode<false, SR>(fabsf(x[k]), 0.0f, q, rq, w.x[k] & 0xffffu);
-            r = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(c, x[k]) + 128.0f, k, r);
+        for (int k = 0; k < 4; ++k) {
+            const float y = __builtin_amdgcn_sqrtf((V ? root[k] : fabsf(x[k])) * rq);
+            d = fminf(d, fabsf(__builtin_amdgcn_fractf(y) - 0.5f));
+            put(V ? fmaxf(y, x[k] > 0.0f ? 1.0f : 0.0f) : y, k);
         }
+        near = d < (V ? kNearV : kNearM);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // x in units of q (V: its root), its code k + f, the value between the codes' as a share of the gap: up
+            // where the random bits are below that share.  num and gap are x - value(k) and value(k+1) - value(k)
+            // over q (V: q^2).
+            const float t = (V ? root[k] : fabsf(x[k])) * rq;
+            const float c = floorf(__builtin_amdgcn_sqrtf(t)), odd = fmaf(2.0f, c, 1.0f);
+            float num, gap;
+            if (V) {
+                const float c2 = c * c;
+                num = (t - c2) * (t + c2);
+                gap = odd * fmaf(2.0f, c2, odd);
+            } else {
+                num = fmaf(-c, c, t);
+                gap = odd;
+            }
+            const float e = fmaf(num, 65536.0f, -static_cast<float>(bits(k)) * gap);
+            near = near || fabsf(e) < (V ? kNearChanceV : kNearChanceM) * gap;
+            const float up = c + (e > 0.0f ? 1.0f : 0.0f);
+            put(V ? fmaxf(up, x[k] > 0.0f ? 1.0f : 0.0f) : up, k);
+        }
+    }
+    if (__builtin_amdgcn_ballot_w64(near) != 0) {
+        r = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put(code_by_rule<V, SR>(fabsf(x[k]), V ? root[k] : 0.0f, q, rq, bits(k)), k);
     }
     return q > 0.0f ? (V ? r : r ^ 0x80808080u) : 0u;
 }
@@ -163,11 +223,11 @@ __device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4
 template <bool V>
 __device__ __forceinline__ void decode4(uint32_t w, float q, float x[4])
 {
-    if (!V) w ^= 0x80808080u;   // int8 codes plus 128
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float c = static_cast<float>((w >> (8 * k)) & 0xffu);
-        x[k] = V ? code_value<true>(c, q) : mul((c - 128.0f) * fabsf(c - 128.0f), q);
+        const uint32_t b = w >> (8 * k);
+        const float c = V ? static_cast<float>(b & 0xffu) : static_cast<float>(static_cast<int8_t>(b));
+        x[k] = V ? code_value<true>(c, q) : mul(c * fabsf(c), q);
     }
 }
 

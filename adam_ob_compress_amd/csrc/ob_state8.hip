@@ -46,11 +46,9 @@ __device__ __forceinline__ void write_control(ob_control* ctl, double s, const N
     const bool ok = (__float_as_uint(static_cast<float>(norm)) & 0x7fffffffu) < kInfBits;
     const int64_t t = ctl->step + 1;
     const double bc = np.advance ? 1.0 - pow(threadIdx.x == 0 ? np.beta1 : np.beta2, static_cast<double>(t)) : 1.0;
+    const double bc2 = __shfl(bc, 1, 64);
     if (threadIdx.x == 1) {
-        if (np.advance && ok) {
-            ctl->bc2 = bc;
-            ctl->inv_root_bc2 = static_cast<float>(1.0 / sqrt(bc));
-        }
+        if (np.advance && ok) ctl->bc2 = bc;
         return;
     }
     double f = 1.0;
@@ -65,7 +63,7 @@ __device__ __forceinline__ void write_control(ob_control* ctl, double s, const N
     if (ok) {
         ctl->step = t;
         ctl->bc1 = bc;
-        ctl->inv_bc1 = static_cast<float>(1.0 / bc);
+        ctl->root_factor = static_cast<float>(bc / sqrt(bc2));
     } else {
         ctl->skipped += 1;
     }

@@ -319,7 +319,7 @@ typedef struct ob_tensors_s* ob_tensors;
 
 /* sizes: T >= 0 host int64, each >= 0.  g_dtypes, p_dtypes: T ob_dtype values each (OB_F32, OB_BF16 or
  * OB_F16).  lr_mults, wd_mults: T host factors of the rate and of the weight decay (parameter groups), or
- * NULL for 1; finite.  At most 2^31 - 1 work blocks of 2048 elements in all (OB_ERR_ARG beyond).  The list belongs to the
+ * NULL for 1; finite.  At most 2^31 - 1 tiles of 1024 elements in all (OB_ERR_ARG beyond).  The list belongs to the
  * device that is current here; it owns its device tables (hipMalloc here, hipFree in ob_tensors_destroy). */
 ob_status ob_tensors_create(int64_t n_tensors, const int64_t* sizes, const int32_t* g_dtypes, const int32_t* p_dtypes,
                             const float* lr_mults, const float* wd_mults, ob_tensors* out);
@@ -329,7 +329,7 @@ int64_t ob_tensors_num_elements(ob_tensors list);             /* sum of the size
 int64_t ob_tensors_state_elems(ob_tensors list);              /* multiple of OB_STATE_BLOCK; -1 for a NULL list */
 int64_t ob_tensors_state_offset(ob_tensors list, int64_t t);  /* -1 for a NULL list or t outside 0..T-1 */
 
-/* Parameters of the AdamW step.  beta1, beta2 in [0, 1), eps >= 0 (8-bit states: eps a normal number > 0),
+/* Parameters of the AdamW step.  beta1, beta2 in [0, 1), eps >= 0 (8-bit states: eps >= 1e-30),
  * weight_decay and lr finite; OB_ERR_ARG otherwise. */
 typedef struct {
     float lr;
@@ -354,10 +354,9 @@ typedef struct {
     double bc1, bc2;     /* 1 - beta1^t, 1 - beta2^t */
     float lr_scale;      /* written by the caller: factor of the rate (schedules under a captured graph) */
     int32_t skip;        /* 1: the norm was not finite, and a step with this block changes nothing */
-    float inv_bc1;       /* 1 / bc1 */
-    float inv_root_bc2;  /* 1 / sqrt(bc2) */
+    float root_factor;   /* bc1 / sqrt(bc2) */
     uint32_t ticket;     /* the norm's own: 0 between calls */
-    uint32_t reserved;
+    uint32_t reserved[2];
 } ob_control;
 #define OB_CONTROL_PARTIALS 2048
 #define OB_CONTROL_BYTES (64 + 8 * OB_CONTROL_PARTIALS)

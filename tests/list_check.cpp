@@ -108,9 +108,9 @@ static int check_refusals()
         int64_t huge[2] = {ob::kListMost, 1};
         CHECK(ob::build_shape(2, huge, f32, f32, nullptr, nullptr, l) == OB_ERR_ARG);
     }
-    {   // 2^43 elements: 2^31 blocks of 4096
+    {   // 2^41 elements: 2^31 tiles
         ob::ListShape l;
-        int64_t huge[1] = {int64_t(1) << 43};
+        int64_t huge[1] = {int64_t(1) << 41};
         std::vector<ob::ListItem> items;
         std::vector<int64_t> first;
         CHECK(ob::build_shape(1, huge, f32, f32, nullptr, nullptr, l) == OB_OK);

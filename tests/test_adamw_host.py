@@ -59,14 +59,14 @@ def test_null_handles_are_refused():
 
 
 def test_a_list_that_does_not_fit_the_host_is_a_status():
-    """2^41 elements (2^30 work blocks, 16 GB of table) under a 4 GiB limit: OB_ERR_OOM, not an abort."""
+    """2^40 elements (2^28 items, 4 GB of table) under a 4 GiB limit: OB_ERR_OOM, not an abort."""
     import sys
     code = f"""
 import ctypes, resource
 resource.setrlimit(resource.RLIMIT_AS, (4 << 30, 4 << 30))
 L = ctypes.CDLL({ob.LIB_PATH!r})
 h = ctypes.c_void_p(1)
-n, d = (ctypes.c_int64 * 1)(1 << 41), (ctypes.c_int32 * 1)(0)
+n, d = (ctypes.c_int64 * 1)(1 << 40), (ctypes.c_int32 * 1)(0)
 print(L.ob_tensors_create(ctypes.c_int64(1), n, d, d, None, None, ctypes.byref(h)), h.value)
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
