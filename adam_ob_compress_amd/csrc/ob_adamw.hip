@@ -48,41 +48,51 @@ __device__ __forceinline__ float load_any1(const void* __restrict__ p, int64_t i
     return D == 0 ? static_cast<const float*>(p)[i] : widen16<D>(static_cast<const uint16_t*>(p)[i]);
 }
 
-// fp32 x rounded to the type (nearest even, or by the 16 random bits r)
+// The 16-bit pattern of fp32 x rounded to the type: to nearest even, or (SR) up in magnitude where the 16 random
+// bits r are below what is cut off.
 template <int D, bool SR>
-__device__ __forceinline__ float round_to(float x, uint32_t r)
+__device__ __forceinline__ uint32_t round16(float x, uint32_t r)
 {
-    if (D == 1) return SR ? ErrBF16::rounded_sr(x, r) : ErrBF16::rounded(x);
-    if (D == 2) return SR ? ErrF16::rounded_sr(x, r) : ErrF16::rounded(x);
-    return x;
+    if (D == 1 && SR) {
+        // the cut-off bits plus 65535 - r carry exactly then; infinities have none, a NaN is kept a NaN
+        const uint32_t u = __float_as_uint(x);
+        return (x != x ? u | 0x00400000u : u + (r ^ 0xffffu)) >> 16;
+    }
+    if (D == 1) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+    return ErrF16::bits(SR ? ErrF16::rounded_sr(x, r) : ErrF16::rounded(x));
 }
 
-template <int D>
-__device__ __forceinline__ uint32_t bits16(float x)  // x already a value of the type
+// Two values as elements of the type, in one word.
+template <int D, bool SR>
+__device__ __forceinline__ uint32_t round16x2(float x, float y, uint32_t r, uint32_t s)
 {
-    return D == 1 ? __float_as_uint(x) >> 16 : ErrF16::bits(x);
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    if (D == 1 && !SR) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{x, y}, b2));
+    return round16<D, SR>(x, r) | (round16<D, SR>(y, s) << 16);
 }
 
-template <int D>
-__device__ __forceinline__ void store_any4(void* __restrict__ p, int64_t i, f4 x)
+// Four values as elements of the type; w: their random words (SR).
+template <int D, bool SR>
+__device__ __forceinline__ void store_any4(void* __restrict__ p, int64_t i, f4 x, const u4& w)
 {
     if (D == 0) {
         __builtin_nontemporal_store(static_cast<f4e>(x), reinterpret_cast<f4e*>(static_cast<float*>(p) + i));
         return;
     }
     u2e u;
-    u.x = bits16<D>(x.x) | (bits16<D>(x.y) << 16);
-    u.y = bits16<D>(x.z) | (bits16<D>(x.w) << 16);
+    u.x = round16x2<D, SR>(x.x, x.y, w.x[0] >> 16, w.x[1] >> 16);
+    u.y = round16x2<D, SR>(x.z, x.w, w.x[2] >> 16, w.x[3] >> 16);
     __builtin_nontemporal_store(u, reinterpret_cast<u2e*>(static_cast<uint16_t*>(p) + i));
 }
 
-template <int D>
-__device__ __forceinline__ void store_any1(void* __restrict__ p, int64_t i, float x)
+template <int D, bool SR>
+__device__ __forceinline__ void store_any1(void* __restrict__ p, int64_t i, float x, uint32_t w)
 {
     if (D == 0)
         static_cast<float*>(p)[i] = x;
     else
-        static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(bits16<D>(x));
+        static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(round16<D, SR>(x, w >> 16));
 }
 
 // Parameters by kind: i the element in the tensor, si the state index (of the master copy).
@@ -105,17 +115,13 @@ struct Par {
     static __device__ __forceinline__ void store4(void* p, float* master, int64_t i, int64_t si, f4 x, const u4& w)
     {
         if (kMaster) st4<true>(master, si, x);
-        if (D != 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = round_to<D, SR && kRound>(x[k], w.x[k] >> 16);
-        }
-        store_any4<D>(p, i, x);
+        store_any4<D, SR && kRound>(p, i, x, w);
     }
     template <bool SR>
     static __device__ __forceinline__ void store1(void* p, float* master, int64_t i, int64_t si, float x, uint32_t w)
     {
         if (kMaster) master[si] = x;
-        store_any1<D>(p, i, round_to<D, SR && kRound>(x, w >> 16));
+        store_any1<D, SR && kRound>(p, i, x, w);
     }
 };
 

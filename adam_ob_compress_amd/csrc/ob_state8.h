@@ -207,7 +207,7 @@ __device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4
             }
             const float e = fmaf(num, 65536.0f, -static_cast<float>(bits(k)) * gap);
             near = near || fabsf(e) < (V ? kNearChanceV : kNearChanceM) * gap;
-            const float up = c + (e > 0.0f ? 1.0f : 0.0f);
+            const float up = c + fminf(fmaxf(e * 0x1p100f, 0.0f), 1.0f);   // one above where e > 0
             put(V ? fmaxf(up, x[k] > 0.0f ? 1.0f : 0.0f) : up, k);
         }
     }
