@@ -40,6 +40,15 @@ constexpr int64_t kKeepBytes = int64_t(256) << 20;
 // block's ticket makes its memory visible to the others.
 constexpr int kTicketGrid = 128;
 
+// Elements of one launch of a conversion (4096 per work group).
+constexpr int64_t kState8Part = ob::kMostGroups * 4096;
+
+template <class T>
+T* at(T* p, int64_t i)
+{
+    return p ? p + i : nullptr;
+}
+
 struct DeviceGuard {
     int prev = -1;
     bool ok = true;
@@ -130,20 +139,17 @@ ob_status launch_step(const ob_tensors_s& l, const void* const* g, void* const* 
     const ob::ListShape& sh = l.shape;
     ob::ListPtrs ptrs;
     return ob::for_runs(sh, ob::kListPtrs, true, [&](int64_t k, int64_t e) {
-        ob::ListLaunch L;
-        L.items = l.step.d_items + l.step.first[k];
-        L.n_items = l.step.first[e] - l.step.first[k];
-        L.tensors = l.d_tensors;
-        L.tensor0 = static_cast<int32_t>(k);
-        if (L.n_items == 0) return OB_OK;
         for (int64_t j = k; j < e; ++j) {
             ptrs.g[j - k] = g[sh.order[j]];
             ptrs.p[j - k] = p[sh.order[j]];
         }
         const int gd = sh.g_dtype[sh.order[k]], pd = sh.p_dtype[sh.order[k]];
         const int pk = pd == OB_F32 ? ob::PK_F32 : pd + (master ? 2 : 0);
-        (void)hipGetLastError();  // clear a stale error so the check sees this launch only
-        return f(gd, pk, L, ptrs) == hipSuccess ? OB_OK : OB_ERR_HIP;
+        return ob::for_parts(l.step.first[e] - l.step.first[k], ob::kMostGroups / ob::kStepTiles, [&](int64_t i, int64_t n) {
+            const ob::ListLaunch L{l.step.d_items + l.step.first[k] + i, l.d_tensors, n, static_cast<int32_t>(k)};
+            (void)hipGetLastError();  // clear a stale error so the check sees this launch only
+            return f(gd, pk, L, ptrs) == hipSuccess ? OB_OK : OB_ERR_HIP;
+        });
     });
 }
 
@@ -212,11 +218,8 @@ try {
     np.first = 1;
     ob::NormPtrs ptrs;
     const ob_status st = ob::for_runs(l.shape, ob::kNormPtrs, false, [&](int64_t k, int64_t e) {
-        ob::ListLaunch L;
-        L.items = l.norm.d_items + l.norm.first[k];
-        L.n_items = l.norm.first[e] - l.norm.first[k];
-        L.tensors = l.d_tensors;
-        L.tensor0 = static_cast<int32_t>(k);
+        const ob::ListLaunch L{l.norm.d_items + l.norm.first[k], l.d_tensors, l.norm.first[e] - l.norm.first[k],
+                               static_cast<int32_t>(k)};
         if (L.n_items == 0) return OB_OK;
         const int gd = l.shape.g_dtype[l.shape.order[k]];
         for (int64_t j = k; j < e; ++j) ptrs.g[j - k] = g[l.shape.order[j]];
@@ -286,20 +289,26 @@ ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_
                            uint8_t* v_codes, float* v_scales, hipStream_t stream)
 {
     if (ob_status st = ob::check_state8(n, m, v, m_codes, m_scales, v_codes, v_scales)) return st;
-    if (n == 0) return OB_OK;
-    (void)hipGetLastError();
-    return ob::launch_state8_encode(n, m, v, m_codes, m_scales, v_codes, v_scales, stream) == hipSuccess ? OB_OK
-                                                                                                       : OB_ERR_HIP;
+    return ob::for_parts(n, kState8Part, [&](int64_t i, int64_t count) {
+        (void)hipGetLastError();
+        return ob::launch_state8_encode(count, at(m, i), at(v, i), at(m_codes, i), at(m_scales, i / OB_STATE_BLOCK),
+                                        at(v_codes, i), at(v_scales, i / OB_STATE_BLOCK), stream) == hipSuccess
+                   ? OB_OK
+                   : OB_ERR_HIP;
+    });
 }
 
 ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,
                            const float* v_scales, float* m, float* v, hipStream_t stream)
 {
     if (ob_status st = ob::check_state8(n, m, v, m_codes, m_scales, v_codes, v_scales)) return st;
-    if (n == 0) return OB_OK;
-    (void)hipGetLastError();
-    return ob::launch_state8_decode(n, m_codes, m_scales, v_codes, v_scales, m, v, stream) == hipSuccess ? OB_OK
-                                                                                                       : OB_ERR_HIP;
+    return ob::for_parts(n, kState8Part, [&](int64_t i, int64_t count) {
+        (void)hipGetLastError();
+        return ob::launch_state8_decode(count, at(m_codes, i), at(m_scales, i / OB_STATE_BLOCK), at(v_codes, i),
+                                        at(v_scales, i / OB_STATE_BLOCK), at(m, i), at(v, i), stream) == hipSuccess
+                   ? OB_OK
+                   : OB_ERR_HIP;
+    });
 }
 
 }  // extern "C"

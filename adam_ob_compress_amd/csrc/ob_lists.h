@@ -69,14 +69,13 @@ inline ob_status build_shape(int64_t T, const int64_t* sizes, const int32_t* gd,
 }
 
 // The work blocks of `elems` elements (a multiple of kListTile), in the list's order; first[k]: index of
-// the first block of the tensor in place k, first[T] the count.  False if the tiles of the blocks, a launch's
-// most work groups, would pass 2^31 - 1.
+// the first block of the tensor in place k, first[T] the count.  False if the blocks would pass 2^31 - 1.
 inline bool build_items(const ListShape& l, int64_t elems, std::vector<ListItem>& items, std::vector<int64_t>& first)
 {
     int64_t total = 0;
     for (int64_t n : l.size) {
         total += n / elems + (n % elems != 0);
-        if (total > INT32_MAX / (elems / kListTile)) return false;
+        if (total > INT32_MAX) return false;
     }
     items.reserve(static_cast<size_t>(total));
     for (size_t k = 0; k < l.order.size(); ++k) {
@@ -105,6 +104,18 @@ ob_status for_runs(const ListShape& l, int64_t most, bool parameters, F&& f)
         if (ob_status st = f(k, e)) return st;
         k = e;
     }
+    return OB_OK;
+}
+
+// A launch has at most 2^32 - 1 threads, so what needs more work groups of kListBlock is launched in parts:
+// f(begin, count) over 0..n in parts of at most `most`, until f returns other than OB_OK.
+constexpr int64_t kMostGroups = (int64_t(1) << 32) / kListBlock - 1;
+
+template <class F>
+ob_status for_parts(int64_t n, int64_t most, F&& f)
+{
+    for (int64_t i = 0; i < n; i += most)
+        if (ob_status st = f(i, std::min(most, n - i))) return st;
     return OB_OK;
 }
 
@@ -176,13 +187,10 @@ inline ob_status check_norm(const ListShape& l, const void* const* g, float g_mu
     return check_pointers(l, g, nullptr);
 }
 
-// Most state elements of one conversion: its launch has at most 2^31 - 1 work blocks of 4096.
-constexpr int64_t kMaxState8 = int64_t(INT32_MAX) * 4096;
-
 inline ob_status check_state8(int64_t n, const float* m, const float* v, const void* mc, const float* mq,
                               const void* vc, const float* vq)
 {
-    if (n < 0 || n > kMaxState8) return OB_ERR_ARG;
+    if (n < 0 || n > kListMost) return OB_ERR_ARG;
     if (n == 0) return OB_OK;
     const bool any_m = m || mc || mq, any_v = v || vc || vq;
     if ((any_m && !(m && mc && mq)) || (any_v && !(v && vc && vq)) || (!any_m && !any_v)) return OB_ERR_ARG;

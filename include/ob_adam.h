@@ -312,14 +312,15 @@ ob_status ob_plan_set_diagnostics(ob_plan plan, double* err_sumsq_out, uint64_t*
  * Threads and streams: a list is read-only after its creation and holds no workspace, so calls with one
  * list may overlap if their buffers (parameters, states, control) differ.  No call synchronises,
  * allocates device memory or records anything but kernels, so all can be captured into a HIP graph; a
- * captured call keeps its addresses and hparams, while what the control block holds is read on replay. */
+ * captured call keeps its addresses, hparams and list (which must outlive the graph), while what the control
+ * block holds is read on replay. */
 #define OB_STATE_BLOCK 256
 
 typedef struct ob_tensors_s* ob_tensors;
 
 /* sizes: T >= 0 host int64, each >= 0.  g_dtypes, p_dtypes: T ob_dtype values each (OB_F32, OB_BF16 or
  * OB_F16).  lr_mults, wd_mults: T host factors of the rate and of the weight decay (parameter groups), or
- * NULL for 1; finite.  At most 2^31 - 1 tiles of 1024 elements in all (OB_ERR_ARG beyond).  The list belongs to the
+ * NULL for 1; finite.  At most 2^31 - 1 work blocks of 4096 elements in all (OB_ERR_ARG beyond).  The list belongs to the
  * device that is current here; it owns its device tables (hipMalloc here, hipFree in ob_tensors_destroy). */
 ob_status ob_tensors_create(int64_t n_tensors, const int64_t* sizes, const int32_t* g_dtypes, const int32_t* p_dtypes,
                             const float* lr_mults, const float* wd_mults, ob_tensors* out);

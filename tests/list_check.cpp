@@ -73,6 +73,17 @@ static int check_list(std::mt19937_64& rng, int T)
             CHECK(next == T && last < T);
         }
     }
+    for (int64_t n : {int64_t(0), int64_t(1), int64_t(7), int64_t(8), int64_t(100)}) {
+        int64_t next = 0;
+        CHECK(ob::for_parts(n, 8, [&](int64_t i, int64_t c) {
+                  if (i != next || c < 1 || c > 8) return OB_ERR_ARG;
+                  next = i + c;
+                  return OB_OK;
+              }) == OB_OK);
+        CHECK(next == n);
+        CHECK(n == 0 || ob::for_parts(n, 8, [&](int64_t, int64_t) { return OB_ERR_HIP; }) == OB_ERR_HIP);
+    }
+    CHECK(ob::kMostGroups * ob::kListBlock < (int64_t(1) << 32));
     return 0;
 }
 
@@ -108,9 +119,9 @@ static int check_refusals()
         int64_t huge[2] = {ob::kListMost, 1};
         CHECK(ob::build_shape(2, huge, f32, f32, nullptr, nullptr, l) == OB_ERR_ARG);
     }
-    {   // 2^41 elements: 2^31 tiles
+    {   // 2^43 elements: 2^31 blocks of 4096
         ob::ListShape l;
-        int64_t huge[1] = {int64_t(1) << 41};
+        int64_t huge[1] = {int64_t(1) << 43};
         std::vector<ob::ListItem> items;
         std::vector<int64_t> first;
         CHECK(ob::build_shape(1, huge, f32, f32, nullptr, nullptr, l) == OB_OK);
@@ -178,7 +189,7 @@ static int check_refusals()
 
     const float* f = static_cast<const float*>(at(0x1000));
     CHECK(ob::check_state8(-1, f, f, f, f, f, f) == OB_ERR_ARG);
-    CHECK(ob::check_state8(ob::kMaxState8 + 1, f, f, f, f, f, f) == OB_ERR_ARG);
+    CHECK(ob::check_state8(ob::kListMost + 1, f, f, f, f, f, f) == OB_ERR_ARG);
     CHECK(ob::check_state8(0, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr) == OB_OK);
     CHECK(ob::check_state8(9, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr) == OB_ERR_ARG);
     CHECK(ob::check_state8(9, f, nullptr, f, f, nullptr, nullptr) == OB_OK);

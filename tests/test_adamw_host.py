@@ -59,7 +59,7 @@ def test_null_handles_are_refused():
 
 
 def test_a_list_that_does_not_fit_the_host_is_a_status():
-    """2^40 elements (2^28 items, 4 GB of table) under a 4 GiB limit: OB_ERR_OOM, not an abort."""
+    """2^40 elements (2^28 work blocks, 4 GB of table) under a 4 GiB limit: OB_ERR_OOM, not an abort."""
     import sys
     code = f"""
 import ctypes, resource
