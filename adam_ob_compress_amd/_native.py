@@ -413,6 +413,11 @@ def ob_plan_read_timing(plan: Plan, kernel: int) -> tuple[float, int]:
 
 # ---- AdamW over lists of tensors ----
 
+# types of flat buffers by torch's scalar type codes: float32, int8, uint8, int32
+_KIND_DTYPES = {6: torch.float32, 1: torch.int8, 0: torch.uint8, 3: torch.int32}
+_F32, _I8, _U8, _I32 = b"\x06", b"\x01", b"\x00", b"\x03"
+
+
 class Tensors:
     """Owner of an ob_tensors handle (destroyed with the object): a list of tensors by size and type."""
 
@@ -423,6 +428,8 @@ class Tensors:
         self.p_dtypes = tuple(p_dtypes)
         self.device = device
         self.state_elems = int(lib().ob_tensors_state_elems(handle))
+        N, B, C = self.state_elems, self.state_elems // OB_STATE_BLOCK, OB_CONTROL_BYTES // 4
+        self._numels32, self._numels8, self._numels_control = (N, N, N, C), (N, N, B, N, B, C), (C,)
         T = len(self.sizes)
         self._array = ctypes.c_void_p * T
         self._numels = (ctypes.c_int64 * T)(*self.sizes)
@@ -476,14 +483,12 @@ class Tensors:
             raise ValueError(f"{name} must not be a negated view")
         raise ValueError(f"{name} must be on {self.device}, the list's device (got {t.device})")
 
-    def _flat(self, t, name, dtype, numel):
-        """Device address of a flat state buffer on the list's device (None -> NULL)."""
-        if t is None:
-            return None
-        if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != numel
-                or t.get_device() != self.device.index or not t.is_contiguous()):
-            self._refuse(t, name, dtype, numel)
-        return t.data_ptr()
+    def _flat(self, tensors, names, kinds, numels):
+        """Device addresses of flat buffers on the list's device (None -> NULL); kinds: their types' codes."""
+        out = _obtorch().addresses(tensors, numels, kinds, self.device.index)
+        if isinstance(out, int):
+            self._refuse(tensors[out], names[out], _KIND_DTYPES[kinds[out]], numels[out])
+        return out
 
 
 def _dtype_list(d, count, name):
@@ -539,10 +544,6 @@ def control_fields(control: torch.Tensor) -> dict:
             "lr_scale": f[10:11], "skip": control[11:12]}
 
 
-def _control_ptr(tensors: Tensors, control):
-    return tensors._flat(control, "control", torch.int32, OB_CONTROL_BYTES // 4)
-
-
 def _list_stream(tensors: Tensors, stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(tensors.device.index)  # what current_stream() wraps, at 1/25 of its time
@@ -557,18 +558,18 @@ def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp:
     if control is None:
         raise TypeError("control must be a torch.Tensor")
     g = tensors._pointers(grads, "grads", tensors.g_dtypes)
-    _check(lib().ob_grad_norm(tensors.handle, g, g_mult, max_norm, None if hp is None else ctypes.byref(hp),
-                              _control_ptr(tensors, control), _list_stream(tensors, stream)), "ob_grad_norm")
+    c, = tensors._flat((control,), ("control",), _I32, tensors._numels_control)
+    _check(lib().ob_grad_norm(tensors.handle, g, g_mult, max_norm, None if hp is None else ctypes.byref(hp), c,
+                              _list_stream(tensors, stream)), "ob_grad_norm")
 
 
 def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None):
     """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems."""
     g = tensors._pointers(grads, "grads", tensors.g_dtypes)
     p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
-    N = tensors.state_elems
-    f = [tensors._flat(t, name, torch.float32, N) for t, name in ((master, "master"), (m, "m"), (v, "v"))]
-    _check(lib().ob_adamw_step(tensors.handle, g, p, *f, ctypes.byref(hp), _control_ptr(tensors, control),
-                               _list_stream(tensors, stream)), "ob_adamw_step")
+    f = tensors._flat((master, m, v, control), ("master", "m", "v", "control"), _F32 * 3 + _I32, tensors._numels32)
+    _check(lib().ob_adamw_step(tensors.handle, g, p, *f[:3], ctypes.byref(hp), f[3], _list_stream(tensors, stream)),
+           "ob_adamw_step")
 
 
 def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, v_scales, hp: ob_adamw_hparams,
@@ -576,38 +577,37 @@ def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, 
     """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256."""
     g = tensors._pointers(grads, "grads", tensors.g_dtypes)
     p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
-    N = tensors.state_elems
-    f = [tensors._flat(t, name, dtype, n) for t, name, dtype, n in
-         ((master, "master", torch.float32, N), (m_codes, "m_codes", torch.int8, N),
-          (m_scales, "m_scales", torch.float32, N // OB_STATE_BLOCK), (v_codes, "v_codes", torch.uint8, N),
-          (v_scales, "v_scales", torch.float32, N // OB_STATE_BLOCK))]
-    _check(lib().ob_adamw8_step(tensors.handle, g, p, *f, ctypes.byref(hp), _control_ptr(tensors, control),
-                                _list_stream(tensors, stream)), "ob_adamw8_step")
+    f = tensors._flat((master, m_codes, m_scales, v_codes, v_scales, control),
+                      ("master", "m_codes", "m_scales", "v_codes", "v_scales", "control"),
+                      _F32 + _I8 + _F32 + _U8 + _F32 + _I32, tensors._numels8)
+    _check(lib().ob_adamw8_step(tensors.handle, g, p, *f[:5], ctypes.byref(hp), f[5], _list_stream(tensors, stream)),
+           "ob_adamw8_step")
 
 
-def _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales):
-    """(n, device index, addresses in this order) of a conversion's tensors, checked; either moment may be None
-    throughout."""
+_STATE8_NAMES = ("m", "v", "m_codes", "m_scales", "v_codes", "v_scales")
+
+
+def _state8_pointers(*tensors):
+    """(n, device index, addresses) of a conversion's tensors in the order of _STATE8_NAMES, checked; either moment may
+    be None throughout."""
+    m, v = tensors[:2]
     lead = m if m is not None else v
     if lead is None:
         raise ValueError("neither moment is given")
+    for name, x, codes, scales in (("m", m, *tensors[2:4]), ("v", v, *tensors[4:])):
+        if (x is None) != (codes is None) or (x is None) != (scales is None):
+            raise ValueError(f"{name}, {name}_codes and {name}_scales come together")
     n = lead.numel()
     blocks = -(-n // OB_STATE_BLOCK)
-    args = ((m, "m", torch.float32, n, m), (v, "v", torch.float32, n, v), (m_codes, "m_codes", torch.int8, n, m),
-            (m_scales, "m_scales", torch.float32, blocks, m), (v_codes, "v_codes", torch.uint8, n, v),
-            (v_scales, "v_scales", torch.float32, blocks, v))
-    for t, name, dtype, want, x in args:
-        if (t is None) != (x is None):
-            raise ValueError(f"{name[0]}, {name[0]}_codes and {name[0]}_scales come together")
-        if t is not None and (t.dtype is not dtype or t.numel() != want):
-            _want(t, name, dtype, want)
     index = lead.get_device()
-    out = []
-    for t, name, _, _, _ in args:
-        if t is not None and (t.get_device() != index or index < 0 or not t.is_contiguous()):
+    numels, kinds = (n, n, n, blocks, n, blocks), _F32 * 2 + _I8 + _F32 + _U8 + _F32
+    out = _obtorch().addresses(tensors, numels, kinds, index)
+    if isinstance(out, int):
+        for t, name, kind, numel in zip(tensors, _STATE8_NAMES, kinds, numels):
+            _want(t, name, _KIND_DTYPES[kind], numel)
+        for t, name in zip(tensors, _STATE8_NAMES):
             _dev(t, name)
-            raise ValueError(f"{name} must be on {lead.device} (got {t.device})")
-        out.append(None if t is None else t.data_ptr())
+        raise ValueError(f"{_STATE8_NAMES[out]} must be on {lead.device} (got {tensors[out].device})")
     return n, index, out
 
 

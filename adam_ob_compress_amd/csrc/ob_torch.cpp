@@ -10,6 +10,18 @@
 
 namespace {
 
+// Whether item is a dense GPU tensor of this kind; *address then its memory's.
+bool address_of(PyObject* item, int8_t dtype, int64_t numel, long device, void** address)
+{
+    if (!THPVariable_Check(item)) return false;
+    const at::Tensor& t = THPVariable_Unpack(item);
+    if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.is_neg() ||
+        static_cast<int8_t>(t.scalar_type()) != dtype || t.numel() != numel || !t.is_contiguous())
+        return false;
+    *address = numel > 0 ? t.data_ptr() : nullptr;
+    return true;
+}
+
 // pointers(tensors, others, numels, dtypes, device, out): tensors, a list or tuple of tensors or Nones; others,
 // another one (or None): where it has a tensor, so must tensors; numels (int64), dtypes (int8, c10
 // scalar types) and out (void*): addresses of arrays of len(tensors) entries; device: index of the GPU.  Writes the
@@ -38,19 +50,55 @@ PyObject* pointers(PyObject*, PyObject* const* args, Py_ssize_t n)
                 out[j] = nullptr;
                 continue;
             }
-            if (!THPVariable_Check(items[j])) break;
-            const at::Tensor& t = THPVariable_Unpack(items[j]);
-            if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.is_neg() ||
-                static_cast<int8_t>(t.scalar_type()) != dtypes[j] || t.numel() != numels[j] || !t.is_contiguous())
-                break;
-            out[j] = t.numel() > 0 ? t.data_ptr() : nullptr;
+            if (!address_of(items[j], dtypes[j], numels[j], device, &out[j])) break;
         }
     } catch (...) {   // a tensor without memory of its own (fake or functional ones)
     }
     return PyLong_FromSsize_t(j < T ? j : -1);
 }
 
-// scalar_type(dtype): the code that pointers() compares with
+// addresses(tensors, numels, dtypes, device): the same for a tuple of buffers of different kinds, with numels a tuple
+// of ints and dtypes a bytes object.  A tuple of addresses (None for None), or the place of the first that is
+// not as it should be.
+PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    if (n != 4 || !PyTuple_Check(args[0]) || !PyTuple_Check(args[1]) || !PyBytes_Check(args[2]) ||
+        PyTuple_GET_SIZE(args[1]) != PyTuple_GET_SIZE(args[0]) || PyBytes_GET_SIZE(args[2]) != PyTuple_GET_SIZE(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "expected tensors, element counts and types of one length");
+        return nullptr;
+    }
+    const long device = PyLong_AsLong(args[3]);
+    if (PyErr_Occurred()) return nullptr;
+    const Py_ssize_t T = PyTuple_GET_SIZE(args[0]);
+    PyObject* out = PyTuple_New(T);
+    if (!out) return nullptr;
+    for (Py_ssize_t j = 0; j < T; ++j) {
+        PyObject* item = PyTuple_GET_ITEM(args[0], j);
+        PyObject* value = nullptr;
+        if (item == Py_None) {
+            Py_INCREF(Py_None);
+            value = Py_None;
+        } else {
+            const int64_t numel = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], j));
+            void* p = nullptr;
+            bool ok = false;
+            try {
+                ok = !PyErr_Occurred() &&
+                     address_of(item, static_cast<int8_t>(PyBytes_AS_STRING(args[2])[j]), numel, device, &p);
+            } catch (...) {
+            }
+            if (ok) value = PyLong_FromVoidPtr(p);
+            if (!value) {
+                Py_DECREF(out);
+                return PyErr_Occurred() ? nullptr : PyLong_FromSsize_t(j);
+            }
+        }
+        PyTuple_SET_ITEM(out, j, value);
+    }
+    return out;
+}
+
+// scalar_type(dtype): the code that the others compare with
 PyObject* scalar_type(PyObject*, PyObject* dtype)
 {
     if (!THPDtype_Check(dtype)) {
@@ -62,6 +110,7 @@ PyObject* scalar_type(PyObject*, PyObject* dtype)
 
 PyMethodDef methods[] = {
     {"pointers", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pointers)), METH_FASTCALL, nullptr},
+    {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(addresses)), METH_FASTCALL, nullptr},
     {"scalar_type", scalar_type, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
