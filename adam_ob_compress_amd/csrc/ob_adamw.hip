@@ -261,8 +261,8 @@ __device__ __forceinline__ void adamw8_elem(float g, float& mm, float& vv, float
     pp = fmaf(-s.lr, u, pp);
 }
 
-// A wave's span: elements [at, at + kSpanElems) of the tensor, `left` of them there (FULL: all).
-template <int G, int PK, bool SR, bool FULL>
+// A wave's span of S state blocks: elements from `at` on of the tensor, `left` of them there (FULL: all).
+template <int G, int PK, bool SR, int S, bool FULL>
 __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, int64_t state_off, int64_t at, int left,
                                       const Step8& s, uint64_t seed, uint64_t t)
 {
@@ -270,11 +270,11 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
     const int lane4 = 4 * (static_cast<int>(threadIdx.x) & 63);
     const int64_t sb = (state_off + at) / kStateBlock;
     const int blocks = (left + kStateBlock - 1) / kStateBlock;
-    float gv[kSpan][4], pv[kSpan][4], mv[kSpan][4], vv[kSpan][4], root[kSpan][4];
-    uint32_t mw[kSpan], vw[kSpan], tm[kSpan], tv[kSpan];
-    const f4 qm = load_scales<FULL>(st.mq, sb, blocks), qv = load_scales<FULL>(st.vq, sb, blocks);
+    float gv[S][4], pv[S][4], mv[S][4], vv[S][4], root[S][4];
+    uint32_t mw[S], vw[S], tm[S], tv[S];
+    const f4 qm = load_scales<S, FULL>(st.mq, sb, blocks), qv = load_scales<S, FULL>(st.vq, sb, blocks);
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) {
+    for (int j = 0; j < S; ++j) {
         const int64_t i = at + j * kStateBlock + lane4, si = state_off + i;
         const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
         mw[j] = load_codes<FULL>(st.mc, si, cnt);
@@ -298,7 +298,7 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
         }
     }
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) {
+    for (int j = 0; j < S; ++j) {
         const int64_t i = at + j * kStateBlock + lane4, si = state_off + i;
         const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
         decode4<false>(mw[j], qm[j], mv[j]);
@@ -325,10 +325,10 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
                 if (k < cnt) P::template store1<SR>(p, st.master, i + k, si + k, pv[j][k], w.x[k]);
         }
     }
-    const SpanScales q = span_scales(tm, tv);
-    store_scales<FULL>(st.mq, st.vq, sb, blocks, q);
+    const SpanScales q = span_scales<S>(tm, tv);
+    store_scales<S, FULL>(st.mq, st.vq, sb, blocks, q);
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) {
+    for (int j = 0; j < S; ++j) {
         const int64_t si = state_off + at + j * kStateBlock + lane4;
         const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
         u4 w{};
@@ -338,30 +338,37 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
     }
 }
 
-template <int G, int PK, bool SR>
+// S state blocks per wave.  A long list takes four, which pays for the scales once; a short one, which leaves most
+// of the card idle, takes one, so that more waves share the work.
+template <int G, int PK, bool SR, int S>
 __global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs ptrs, State8 st, AdamWParams ap)
 {
-    const ListItem it = L.items[blockIdx.x];
+    constexpr int kParts = kSpan / S;   // work groups per item
+    const ListItem it = L.items[blockIdx.x / kParts];
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int base = (static_cast<int>(blockIdx.x % kParts) * (kListBlock / 64) + wave) * S * kStateBlock;
     const void* g = ptrs.g[it.tensor - L.tensor0];
-    if (g == nullptr) return;
+    const int left = it.len - base;   // uniform over a wave
+    if (g == nullptr || left <= 0) return;
     void* p = ptrs.p[it.tensor - L.tensor0];
     const ListTensor tn = L.tensors[it.tensor];
     const Step sd = step_of(ap, tn);
     if (sd.skip) return;
     const Step8 s = step8_of(sd, ap);
-    const int first = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * kSpanElems;
-    for (int base = first; base < it.len; base += kListBlock / 64 * kSpanElems) {   // uniform over a wave
-        const int left = it.len - base;
-        if (left >= kSpanElems)
-            span8<G, PK, SR, true>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
-        else
-            span8<G, PK, SR, false>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
-    }
+    if (left >= S * kStateBlock)
+        span8<G, PK, SR, S, true>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
+    else
+        span8<G, PK, SR, S, false>(g, p, st, tn.state_off, it.start + base, left, s, ap.seed, sd.t);
 }
 
 // ------------------------------------------------------------------------------------------------
 // launches
 // ------------------------------------------------------------------------------------------------
+
+// Items (of up to 4096 elements) up to which a launch takes one state block per wave, against four.  fp32 parameters,
+// to nearest: 26 items 3.8 us and 6.8, 313 5.2 and 8.0, 2021 20.8 and 21.7, 1.09e8 elements 265 and 250; bf16
+// by chance: 26 4.2 and 8.4, 2021 25.5 and 25.6, 3973 46.5 and 43.5.
+constexpr int64_t kShortItems = 2048;
 
 // f(kind as a constant, rounding as a constant) for the run-time values
 template <class F>
@@ -404,8 +411,14 @@ hipError_t launch_adamw8(const ListLaunch& L, const ListPtrs& ptrs, int pk, cons
                          hipStream_t s)
 {
     return by_kind(pk, ap.stochastic, [&](auto k, auto r) {
-        hipLaunchKernelGGL((k_adamw8<G, decltype(k)::value, decltype(r)::value>), dim3(static_cast<unsigned>(L.n_items)),
-                           dim3(kListBlock), 0, s, L, ptrs, st, ap);
+        constexpr int PK = decltype(k)::value;
+        constexpr bool SR = decltype(r)::value;
+        if (L.n_items <= kShortItems)
+            hipLaunchKernelGGL((k_adamw8<G, PK, SR, 1>), dim3(static_cast<unsigned>(L.n_items * kSpan)), dim3(kListBlock),
+                               0, s, L, ptrs, st, ap);
+        else
+            hipLaunchKernelGGL((k_adamw8<G, PK, SR, kSpan>), dim3(static_cast<unsigned>(L.n_items)), dim3(kListBlock), 0,
+                               s, L, ptrs, st, ap);
         return hipGetLastError();
     });
 }

@@ -29,9 +29,9 @@ constexpr float kNearChanceM = 4.0f, kNearChanceV = 8.0f;
 
 typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 
-// A wave takes spans of kSpan state blocks, four elements of each block per lane.  Their 2 kSpan largest
-// magnitudes (of m and of v) are reduced together: each exchange of half-waves or rows leaves half as many
-// registers, so eight values over 64 lanes cost 20 operations.
+// A wave takes spans of S = kSpan state blocks (the step on short lists: of one), four elements of each block per
+// lane.  A span's 2 S largest magnitudes (of m and of v) are reduced together: each exchange of half-waves
+// or rows leaves half as many registers, so eight values over 64 lanes cost 20 operations.
 constexpr int kSpan = 4;
 constexpr int kSpanElems = kSpan * kStateBlock;
 
@@ -89,7 +89,8 @@ __device__ __forceinline__ float exact_root(float t)
 
 // The scales of a span's blocks.  tm, tv: per block the lane's largest magnitude as unsigned bits (NaN above
 // infinity above every number, so neither is lost in a maximum).  Two registers hold the eight scales, each in
-// a row of 16 lanes: rows 0, 1 of a the m of blocks 0, 1, rows 2, 3 their v; b blocks 2, 3.
+// a row of 16 lanes: rows 0, 1 of a the m of blocks 0, 1, rows 2, 3 their v; b blocks 2, 3.  (One block: its m in
+// rows 0, 1 of a, its v in rows 2, 3.)
 struct SpanScales {
     float a, b;
     __device__ __forceinline__ float get(int j, bool v) const   // uniform
@@ -105,12 +106,15 @@ __device__ __forceinline__ float block_scale(uint32_t top, bool v)
     return top >= kInfBits ? __uint_as_float(0x7fc00000u) : top < kTinyBits ? 0.0f : q;
 }
 
-__device__ __forceinline__ SpanScales span_scales(const uint32_t tm[kSpan], const uint32_t tv[kSpan])
+template <int S>
+__device__ __forceinline__ SpanScales span_scales(const uint32_t tm[S], const uint32_t tv[S])
 {
+    static_assert(S == 1 || S == 4, "spans of one or four blocks");
     const bool v = (threadIdx.x & 32) != 0;
-    SpanScales s;
-    s.a = block_scale(row_max(fold16(fold32(tm[0], tv[0]), fold32(tm[1], tv[1]))), v);
-    s.b = block_scale(row_max(fold16(fold32(tm[2], tv[2]), fold32(tm[3], tv[3]))), v);
+    const uint32_t first = fold32(tm[0], tv[0]);
+    SpanScales s{};
+    s.a = block_scale(row_max(fold16(first, S == 1 ? first : fold32(tm[S / 4], tv[S / 4]))), v);
+    if (S == 4) s.b = block_scale(row_max(fold16(fold32(tm[S / 2], tv[S / 2]), fold32(tm[S - 1], tv[S - 1]))), v);
     return s;
 }
 
@@ -258,25 +262,25 @@ __device__ __forceinline__ void store_codes(void* codes, int64_t i, int cnt, uin
 }
 
 // Scales of a span's blocks, the first `blocks` of them there; sb: the first block.
-template <bool FULL>
+template <int S, bool FULL>
 __device__ __forceinline__ f4 load_scales(const float* q, int64_t sb, int blocks)
 {
-    if (FULL) return *reinterpret_cast<const f4e*>(q + sb);
+    if (FULL && S == 4) return *reinterpret_cast<const f4e*>(q + sb);
     f4 r{};
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j)
-        if (j < blocks) r[j] = q[sb + j];
+    for (int j = 0; j < S; ++j)
+        if (FULL || j < blocks) r[j] = q[sb + j];
     return r;
 }
 
-template <bool FULL>
+template <int S, bool FULL>
 __device__ __forceinline__ void store_scales(float* mq, float* vq, int64_t sb, int blocks, const SpanScales& s)
 {
     const int lane = static_cast<int>(threadIdx.x) & 63, j = (lane >> 4) & 1;
-    if ((lane & 15) != 0) return;
+    if ((lane & (S == 1 ? 31 : 15)) != 0) return;
     float* q = (lane < 32 ? mq : vq) + sb + j;
     if (FULL || j < blocks) q[0] = s.a;
-    if (FULL || j + 2 < blocks) q[2] = s.b;
+    if (S == 4 && (FULL || j + 2 < blocks)) q[2] = s.b;
 }
 
 }  // namespace

@@ -199,7 +199,7 @@ __device__ __forceinline__ void decode_span(int64_t n, int64_t at, const uint8_t
 {
     const int lane4 = 4 * (static_cast<int>(threadIdx.x) & 63);
     const int left = FULL ? kSpanElems : static_cast<int>(n - at), blocks = (left + kStateBlock - 1) / kStateBlock;
-    const f4 q = load_scales<FULL>(scales, at / kStateBlock, blocks);
+    const f4 q = load_scales<kSpan, FULL>(scales, at / kStateBlock, blocks);
     uint32_t w[kSpan];
 #pragma unroll
     for (int j = 0; j < kSpan; ++j) w[j] = load_codes<FULL>(codes, at + j * kStateBlock + lane4, left - j * kStateBlock - lane4);

@@ -135,6 +135,18 @@ class Lists:
                     keep[o:o + n] = True
             assert np.all(self.master.cpu().numpy()[keep] == 7.0), "the master's unused part written"
 
+    def parts(self):
+        """(tensor, state offset, elements, slice in the tensor) of what is compared: all of a tensor, or, as state blocks
+        do not depend on each other, the first, last and some other blocks of a long one."""
+        for j, (o, n) in enumerate(zip(self.off, self.sizes)):
+            if 0 < n <= 1 << 20:
+                yield j, o, n, slice(0, n)
+            elif n:
+                starts = [0, n // 256 * 256 - 8192] + [int(x) * 256 for x in self.rng.integers(32, n // 256 - 64, 12)]
+                for a in starts:
+                    b = min(n, a + (9000 if a == starts[1] else 2048))
+                    yield j, o + a, b - a, slice(a, b)
+
     def check(self, before, hp, *, t, scale=1.0, lr_scale=1.0, bc=None, none=()):
         """The step from `before` against the reference."""
         after = self.snapshot()
@@ -142,18 +154,16 @@ class Lists:
         b1, b2 = (1.0, 1.0) if not hp.bias_correction else bc or (ref.bc(hp.beta1, t), ref.bc(hp.beta2, t))
         sr = hp.rounding == ob.OB_ROUND_STOCHASTIC
         words = ref.philox_words(hp.sr_seed, t, self.N) if sr else None
-        for j, (o, n) in enumerate(zip(self.off, self.sizes)):
-            if n == 0:
-                continue
+        for j, o, n, part in self.parts():
             s, what = slice(o, o + n), f"tensor {j} ({n}, g {self.g[j]}, p {self.p[j]})"
             if j in none:
-                assert np.array_equal(after["p"][j], before["p"][j]), what
+                assert np.array_equal(after["p"][j][part], before["p"][j][part]), what
                 for k in ("m", "v") + (("master",) if self.master is not None else ()):
                     assert np.array_equal(after[k][s], before[k][s]), (what, k)
                 continue
-            g = f64(self.grads[j])
+            g = f64(self.grads[j][part])
             use_master = self.master is not None and self.p[j] != "f32"
-            p0 = before["master"][s] if use_master else before["p"][j]
+            p0 = before["master"][s] if use_master else before["p"][j][part]
             lr, wd = float(hp.lr) * lr_scale * float(np.float32(self.lr_mults[j])), float(hp.weight_decay) * float(np.float32(self.wd_mults[j]))
             kw = dict(lr=lr, beta1=hp.beta1, beta2=hp.beta2, eps=hp.eps, wd=wd, bc1=b1, bc2=b2, scale=scale)
             if self.bits == 32:
@@ -172,19 +182,19 @@ class Lists:
                 slack = np.abs(lr) * (2.0 ** -20 * np.abs(u) + 2.0 ** -22 * np.abs(wd * p0))
             tol = EPS32 / 2 * np.abs(p) + slack * (1 + 1e-6) + 2.0 ** -149
             if use_master or self.p[j] == "f32":
-                close(after["master"][s] if use_master else after["p"][j], p, tol, (what, "p"))
+                close(after["master"][s] if use_master else after["p"][j][part], p, tol, (what, "p"))
             if self.p[j] == "f32":
                 continue
             if use_master:   # the copy is the rounding of the master that is there
                 want = torch.from_numpy(after["master"][s]).float().to(DT[self.p[j]]).double().numpy()
-                assert np.array_equal(after["p"][j], want), what
+                assert np.array_equal(after["p"][j][part], want), what
             else:
                 lo, hi = (p - tol).astype(np.float32), (p + tol).astype(np.float32)
                 if sr:   # up where the random bits are below the fraction: monotone in the value
                     pw = [from16(oracle.to_format_sr(x, self.p[j], hp.sr_seed, t | ref.PAR_STREAM, o), self.p[j]) for x in (lo, hi)]
                 else:
                     pw = [torch.from_numpy(x).to(DT[self.p[j]]).double().numpy() for x in (lo, hi)]
-                assert np.all((after["p"][j] >= np.minimum(*pw)) & (after["p"][j] <= np.maximum(*pw))), what
+                assert np.all((after["p"][j][part] >= np.minimum(*pw)) & (after["p"][j][part] <= np.maximum(*pw))), what
         return after
 
 
@@ -220,6 +230,19 @@ def test_step(bits, g, p, master, stochastic):
         torch.cuda.synchronize()
         L.check(before, hp, t=t)
         L.draw_grads()
+
+
+@pytest.mark.parametrize("g,p,master", [("bf16", "f32", False), ("bf16", "bf16", False), ("f32", "f16", False),
+                                        ("f16", "bf16", True)])
+@pytest.mark.parametrize("stochastic", [False, True])
+def test_long_tensors(g, p, master, stochastic):
+    """More than 2048 work blocks in a launch, where a wave takes four state blocks: whole and ragged spans."""
+    L = Lists([9_000_000, 300, 8_500_003, 1025], g, p, seed=15, master=master, bits=8)
+    hp = hparams(step=9, rounding=int(stochastic), sr_seed=3)
+    before = L.snapshot()
+    L.step(hp)
+    torch.cuda.synchronize()
+    L.check(before, hp, t=9)
 
 
 @pytest.mark.parametrize("bits", [32, 8])
