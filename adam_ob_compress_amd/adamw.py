@@ -28,6 +28,9 @@ class AdamW:
     into a HIP graph; with ``max_norm`` the step count then lives in ``self.control``, where a replay
     advances it, and ``set_lr_scale`` changes the rate between replays.  Without ``max_norm`` the count is a host
     value, which a captured step would repeat: capturing then raises.
+
+    ``self.hp`` holds the step's parameters; what is changed there (``hp.lr``) holds from the next step on.  The groups'
+    rates and decays keep their ratios to it.
     """
 
     def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None,
@@ -95,8 +98,7 @@ class AdamW:
     @torch.no_grad()
     def step(self, grads=None, loss_scale: float = 1.0, stream=None):
         """One step; loss_scale: what the gradients were multiplied with (other than 1 needs max_norm)."""
-        if grads is None:
-            grads = [p.grad for p in self.params]
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
         if self.control is not None:
             nat.ob_grad_norm(self.list, grads, self.control, 1.0 / loss_scale, self.max_norm, self.hp, stream)
         else:
@@ -133,6 +135,10 @@ class AdamW:
         if (self.master is None) != ("master" not in d):
             raise ValueError("the state has a master copy and this optimizer none, or the other way round")
         dev = self.list.device
+        for k in self._STATES:
+            want = self.list.state_elems // (nat.OB_STATE_BLOCK if k.endswith("_scales") else 1)
+            if k in d and d[k].numel() != want:
+                raise ValueError(f"{k} must have {want} elements, got {d[k].numel()}")
         d = {k: x.to(dev) if isinstance(x, torch.Tensor) else x for k, x in d.items()}
         if d["state_bits"] == self.state_bits:
             for k in self._STATES[:2] if self.state_bits == 32 else self._STATES[2:6]:

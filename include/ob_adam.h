@@ -369,15 +369,18 @@ typedef struct {
  *          infinite: g_mult.  g_mult (finite, not 0) removes a loss scale.
  * hp != NULL: also the step's bookkeeping.  norm finite: step += 1, bc1 and bc2 from it, skip = 0;
  * otherwise skipped += 1, skip = 1 (grad_scale then is 0 for an infinite norm with clipping, NaN for a NaN).
- * hp == NULL: skip is set as above, step, skipped, bc1 and bc2 stay. */
+ * hp == NULL: skip is set as above, step, skipped, bc1 and bc2 stay (a step that corrects the bias or rounds
+ * by chance needs them: give hp). */
 ob_status ob_grad_norm(ob_tensors list, const void* const* g, float g_mult, float max_norm,
                        const ob_adamw_hparams* hp, ob_control* control, hipStream_t stream);
 
-/* AdamW step with fp32 states.  With t, bc1, bc2, s = grad_scale and r = lr_scale from `control` (NULL: t =
- * hp->step, s = r = 1), for tensor j: a = lr * r * lr_mults[j], d = weight_decay * wd_mults[j],
+/* AdamW step with fp32 states.  With t, bc1, bc2, s = grad_scale and r = lr_scale from `control`, as the last
+ * ob_grad_norm left it (NULL: t = hp->step, s = r = 1), for tensor j: a = lr * r * lr_mults[j], d = weight_decay * wd_mults[j],
  *   g' = fl32(widen(g) * s);  m = beta1*m + (1-beta1)*g';  v = beta2*v + (1-beta2)*g'^2;
  *   p -= a * ( (m/bc1) / (sqrt(v/bc2) + eps) + d*p )     (bc1 = bc2 = 1 without hp->bias_correction)
- * each line in double, rounded once, as in ob_adam_warmup_step; with d = 0, s = 1 the same bits as there.
+ * each line in double, rounded once, as in ob_adam_warmup_step; with d = 0, s = 1
+ * and finite p the same bits as there.
+ * Outputs must not alias inputs or each other.
  * p[t]: the parameters, updated in place.  master != NULL (fp32[state_elems]): for tensors of a 16-bit
  * type the master copy is the parameter, and p[t] gets its rounding to nearest; fp32 tensors do not use
  * it.  16-bit parameters without a master are widened, updated, rounded to fp32 and then to their type:
@@ -412,7 +415,7 @@ ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, 
 
 /* n fp32 moments into the 8-bit format, to nearest (v >= 0), and back; n >= 0, the last block may be short
  * (ceil(n / 256) scales).  Either moment may be left out: all its pointers NULL.  fp32 pointers 16-byte
- * aligned, codes 4 bytes, scales 4 bytes. */
+ * aligned, codes 4 bytes, scales 4 bytes.  Runs on the current device. */
 ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_codes, float* m_scales,
                            uint8_t* v_codes, float* v_scales, hipStream_t stream);
 ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,

@@ -341,6 +341,47 @@ def test_special_values(bits):
     L.check_guards()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("stochastic", [False, True])
+def test_parameters_that_nothing_moves_keep_their_bits(bits, p, stochastic):
+    """No gradient, moments or decay: zeros, subnormal numbers and the largest ones come back as they were."""
+    L = Lists([300], p, p, seed=8, bits=bits)
+    top = torch.finfo(DT[p]).max
+    tiny = torch.finfo(DT[p]).smallest_normal
+    L.params[0][:8] = torch.tensor([0.0, -0.0, tiny, tiny / 4, -tiny / 4, top, -top, 1.0], device=DEV).to(DT[p])
+    L.grads[0].zero_()
+    for x in ((L.m, L.v) if bits == 32 else (L.mq, L.vq)):
+        x[:300 if bits == 32 else 2] = 0
+    want = L.params[0].clone()
+    hp = hparams(weight_decay=0.0, step=1, rounding=int(stochastic), sr_seed=4)
+    L.step(hp)
+    torch.cuda.synchronize()
+    assert torch.equal(L.params[0].view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("p", ["bf16", "f16"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_copies_of_extreme_masters(p, bits):
+    """Masters that are subnormal in the copy's type, at its largest value and beyond it, and NaN."""
+    L = Lists([256, 7], "f32", p, seed=8, bits=bits, master=True)
+    fi = torch.finfo(DT[p])
+    x = torch.linspace(-3, 3, 256, device=DEV) * fi.smallest_normal
+    x[:7] = torch.tensor([float("nan"), float("inf"), fi.max, -fi.max * (1 - fi.eps / 8), min(fi.max * (1.0 + fi.eps / 2), 3.4e38),
+                          fi.tiny / 2 ** 9, 1.0], device=DEV)
+    L.master[:256] = x
+    for g in L.grads:
+        g.zero_()
+    for y in ((L.m, L.v) if bits == 32 else (L.mq, L.vq)):
+        y[:] = 0
+    L.step(hparams(weight_decay=0.0, step=1))
+    torch.cuda.synchronize()
+    # the infinite one turns NaN: the line's decay is 0 * inf
+    assert torch.equal(L.master[:256].view(torch.int32)[2:], x.view(torch.int32)[2:]) and torch.isnan(L.master[:2]).all()
+    got, want = L.params[0].cpu(), x.cpu().to(DT[p])
+    assert torch.isnan(got[:2]).all() and torch.equal(got[2:].view(torch.int16), want[2:].view(torch.int16))
+
+
 def test_huge_tensor():
     """Offsets past 2^32 elements: one bf16 tensor with 8-bit states; the places around 2^31, 2^32 and the end."""
     n = (1 << 32) + 4099
@@ -374,6 +415,48 @@ def test_huge_tensor():
         u = (m / ref.bc(hp.beta1, 1)) / (np.sqrt(v / ref.bc(hp.beta2, 1)) + 1e-8)
         want = 0.5 - float(hp.lr) * (u + float(hp.weight_decay) * 0.5)
         close(f64(p[a0:a1]), want, 2.0 ** -8 * np.abs(want), a)
+
+
+def test_huge_tensor_with_fp32_states():
+    """Offsets past 2^31 elements: the places around it and the end."""
+    n = (1 << 31) + 4099
+    lst = ob.ob_tensors_create([5, n], torch.bfloat16, torch.float32)
+    N, o = lst.state_elems, lst.state_offset(1)
+    g = torch.full((n,), 1e-3, dtype=torch.bfloat16, device=DEV)
+    p = torch.full((n,), 0.5, device=DEV)
+    m, v = torch.zeros(N, device=DEV), torch.zeros(N, device=DEV)
+    where = [0, (1 << 31) - 300, n - 600]
+    rng = np.random.default_rng(4)
+    for a in where:
+        g[a:a + 600] = torch.from_numpy(rng.standard_normal(600) * 1e-3).to(DEV).bfloat16()
+    hp = hparams(step=1)
+    ob.ob_adamw_step(lst, [None, g], [None, p], m, v, hp)
+    for a in where:
+        x = f64(g[a:a + 600])
+        wm, wv, wp, u = ref.adamw(x, 0 * x, 0 * x, 0 * x + 0.5, lr=float(hp.lr), beta1=hp.beta1, beta2=hp.beta2, eps=hp.eps,
+                                  wd=float(hp.weight_decay), bc1=ref.bc(hp.beta1, 1), bc2=ref.bc(hp.beta2, 1))
+        for got, want in ((m[o + a:o + a + 600], wm), (v[o + a:o + a + 600], wv), (p[a:a + 600], wp)):
+            close(f64(got), want, EPS32 / 2 * np.abs(want) * (1 + 1e-6) + 2.0 ** -46 * np.abs(float(hp.lr) * u), a)
+    assert not m[:o].any() and not v[:o].any()
+
+
+def test_huge_conversion():
+    n = (1 << 31) + 300
+    x = torch.zeros(n, device=DEV)
+    c, q = torch.zeros(n, dtype=torch.int8, device=DEV), torch.zeros(-(-n // 256), device=DEV)
+    where = [0, (1 << 31) - 256, n // 256 * 256 - 256]
+    rng = np.random.default_rng(6)
+    tail = n - where[-1]
+    parts = [rng.standard_normal(k).astype(np.float32) for k in (512, 256, tail)]
+    for a, y in zip(where, parts):
+        x[a:a + len(y)] = torch.from_numpy(y).to(DEV)
+    ob.ob_state8_encode(x, None, c, q, None, None)
+    x.zero_()
+    ob.ob_state8_decode(c, q, None, None, x, None)
+    for a, y in zip(where, parts):
+        wc, wq = ref.encode(y, False)
+        assert np.array_equal(c[a:a + len(y)].cpu().numpy(), wc) and np.array_equal(q[a // 256:][: len(wq)].cpu().numpy(), wq)
+        assert np.array_equal(f64(x[a:a + len(y)]), ref.decode(wc, wq, False))
 
 
 # ---- the norm and the control block ----
@@ -792,6 +875,8 @@ def test_driver_refusals():
         ob.AdamW([torch.zeros(8, 8, device=DEV).t()[:4]])
     with pytest.raises(ValueError, match="weight_decay"):
         ob.AdamW([{"params": list(net.parameters()), "weight_decay": 0.1}], weight_decay=0.0)
+    with pytest.raises(ValueError, match="elements"):
+        opt.load_state_dict({**opt.state_dict(), "m": opt.m[:256]})
     with pytest.raises(ValueError, match="master"):
         opt.load_state_dict({**opt.state_dict(), "master": opt.m})
     # a forward before the step keeps what its backward needs: a step in between is noticed
