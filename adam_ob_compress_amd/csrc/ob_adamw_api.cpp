@@ -39,6 +39,7 @@ constexpr int64_t kKeepBytes = int64_t(256) << 20;
 // elements in all: 5.4 us and 6.2 (6.0 and 9.6 with the call); 200 of 1e7 (610 blocks): 19 us and 9, as each
 // block's ticket makes its memory visible to the others.
 constexpr int kTicketGrid = 128;
+static_assert(kTicketGrid <= ob::kListBlock, "the last block reads one partial sum per thread");
 
 // Elements of one launch of a conversion (4096 per work group).
 constexpr int64_t kState8Part = ob::kMostGroups * 4096;

@@ -96,19 +96,9 @@ __device__ __forceinline__ void item_squares(const void* grad, const ListItem& i
     }
 }
 
-// The control block from the partial sums [0, grid), added in an order that the grid alone fixes.
-__device__ __forceinline__ void finish_norm(ob_control* ctl, unsigned grid, double* lds, const NormParams& np)
-{
-    const double* partials = reinterpret_cast<const double*>(ctl + 1);
-    double a = 0.0;
-    for (unsigned b = threadIdx.x; b < grid; b += kListBlock)
-        a += __hip_atomic_load(partials + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    write_control(ctl, block_sum(a, lds), np);
-}
-
 // A block takes every gridDim-th item, a lane 16 bytes of every 4 KB of it, eight of them in flight.  With np.ticket
 // the block that finishes last (by a ticket in the control block, which it sets back to zero) also finishes
-// the norm.
+// the norm; the grid has at most kListBlock blocks then.
 template <int G>
 __global__ __launch_bounds__(kListBlock) void k_grad_sumsq(ListLaunch L, NormPtrs ptrs, int64_t nt_items, ob_control* ctl,
                                                            NormParams np)
@@ -136,13 +126,26 @@ __global__ __launch_bounds__(kListBlock) void k_grad_sumsq(ListLaunch L, NormPtr
     __syncthreads();
     if (!last) return;
     if (threadIdx.x == 0) ctl->ticket = 0;
-    finish_norm(ctl, gridDim.x, lds, np);
+    const double a = threadIdx.x < gridDim.x
+                         ? __hip_atomic_load(partials + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                         : 0.0;
+    write_control(ctl, block_sum(a, lds), np);
 }
 
-__global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, unsigned grid, NormParams np)
+// The control block from the partial sums of a larger grid.
+__global__ __launch_bounds__(kListBlock) void k_grad_control(ob_control* ctl, int grid, NormParams np)
 {
     __shared__ double lds[kListBlock / 64];
-    finish_norm(ctl, grid, lds, np);
+    const double* partials = reinterpret_cast<const double*>(ctl + 1);
+    double a[OB_CONTROL_PARTIALS / kListBlock];
+#pragma unroll
+    for (int k = 0; k < OB_CONTROL_PARTIALS / kListBlock; ++k) {
+        const int b = k * kListBlock + static_cast<int>(threadIdx.x);
+        a[k] = b < grid ? partials[b] : 0.0;
+    }
+#pragma unroll
+    for (int k = 1; k < OB_CONTROL_PARTIALS / kListBlock; ++k) a[0] += a[k];
+    write_control(ctl, block_sum(a[0], lds), np);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -277,7 +280,7 @@ hipError_t launch_grad_sumsq(const ListLaunch& L, const NormPtrs& ptrs, int g_dt
 
 hipError_t launch_grad_control(ob_control* ctl, int grid, const NormParams& np, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_grad_control, dim3(1), dim3(kListBlock), 0, s, ctl, static_cast<unsigned>(grid), np);
+    hipLaunchKernelGGL(k_grad_control, dim3(1), dim3(kListBlock), 0, s, ctl, grid, np);
     return hipGetLastError();
 }
 
