@@ -25,7 +25,7 @@ constexpr float kBelow = 1.0f / 8192.0f;
 // one root more; the borders' own roundings): at most 3.8e-5 for m (y <= 127) and 8e-5 for v (y <= 255).
 constexpr float kNearM = 1.0f / 16384.0f, kNearV = 1.0f / 8192.0f;
 // The same for chance, in units of the 16 random bits: below 1.6 for m and 4.2 for v.
-constexpr float kNearChanceM = 2.0f, kNearChanceV = 5.0f;
+constexpr float kNearChanceM = 4.0f, kNearChanceV = 8.0f;
 
 typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 
