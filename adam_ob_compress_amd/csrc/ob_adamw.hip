@@ -1,10 +1,12 @@
 // ob_adamw.hip -- AdamW steps over lists of tensors, with states in fp32 (k_adamw) and in 8 bits
 // (k_adamw8); compiled once per gradient type (OB_AW_G: 0 fp32, 1 bf16, 2 fp16).
 //
-// Both are one pass over the data: every array is read once and written once, so HBM bounds them.  A
-// work block takes part of one tensor; a lane takes four consecutive elements of a 256-element state block
+// Both are one pass over the data: every array is read once and written once.  HBM bounds them, but for
+// 16-bit parameters with 8-bit states rounded by chance, where the vector ALU does (see k_adamw8).  A
+// work group takes part of one tensor; a lane takes four consecutive elements of a 256-element state block
 // per wave.  The tensors' addresses are launch arguments; parameters and gradients may start
-// at any element (vector loads of element alignment), states are aligned by their layout.
+// at any element (vector loads of element alignment), states are aligned by their layout.  Loads and stores are
+// nontemporal: no byte is touched twice.
 #include "ob_state8.h"
 
 #include <type_traits>
@@ -179,9 +181,13 @@ __device__ __forceinline__ void adamw_elem(float g, float& mm, float& vv, float&
     pp = static_cast<float>(pd - s.lr * u);
 }
 
-// One tile of an item per block.  (Two tiles per block, their loads ahead of the arithmetic, were 3 to 5 percent
-// slower: 1.56e9 bf16 parameters with a master 7.67 ms against 7.90, 1e9 without 3.79 against 3.93; consecutive
-// tiles on one XCD 1 to 7 percent; ordinary loads or stores 7 to 14 percent.)
+// m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2;  p -= lr ((m/bc1) / (sqrt(v/bc2) + eps) + wd p).
+// Bound by HBM: 22 to 28 bytes an element.  Measured (MI355X): 1.09e8 fp32 elements 500 us, 6.1 TB/s; 1.56e9 bf16
+// parameters with a master 6.8 to 7.7 ms by the placement of the buffers, 5.7 to 6.4 TB/s; the double-precision
+// lines hide (without the two divisions by bc1, bc2 the time is the same).
+// One tile of an item per work group.  Two tiles, their loads ahead of the arithmetic, were 3 to 5 percent
+// slower (1.56e9 bf16 parameters with a master 7.90 ms against 7.67, 1e9 without 3.93 against 3.79), consecutive
+// tiles on one XCD 1 to 7 percent, ordinary loads or stores 7 to 14 percent.
 template <int G, int PK, bool SR>
 __global__ __launch_bounds__(kListBlock) void k_adamw(ListLaunch L, ListPtrs ptrs, State32 st, AdamWParams ap)
 {
@@ -338,8 +344,14 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
     }
 }
 
-// S state blocks per wave.  A long list takes four, which pays for the scales once; a short one, which leaves most
-// of the card idle, takes one, so that more waves share the work.
+// The step with 8-bit states: decode, moments, parameter; then the scales of the new moments and their codes.
+// Bytes: 10 to 16 an element and 16 per 256.  Operations: 49 of the vector ALU an element to nearest, 86
+// by chance (random words 9, codes), 101 with 16-bit parameters rounded by chance too.  Measured (MI355X), 1e9
+// elements: fp32 parameters 2.36 ms and bf16 with a master 2.68 ms, 5.9 to 6.0 TB/s, bf16 1.65 ms, 6.1 TB/s, all by
+// HBM; bf16 by chance 2.44 ms, 4.1 TB/s, by the ALU (41e12 operations a second).
+// S state blocks per wave.  A long list takes four: their loads are in flight together (one block per trip:
+// 2.56 ms for fp32 parameters), and the scales' reductions and roots are paid once for four.  A short list, which
+// leaves most of the card idle, takes one, so that more waves share the work.
 template <int G, int PK, bool SR, int S>
 __global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs ptrs, State8 st, AdamWParams ap)
 {
