@@ -283,8 +283,8 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
     for (int j = 0; j < S; ++j) {
         const int64_t i = at + j * kStateBlock + lane4, si = state_off + i;
         const int cnt = FULL ? 4 : left - j * kStateBlock - lane4;
-        mw[j] = load_codes<FULL>(st.mc, si, cnt);
-        vw[j] = load_codes<FULL>(st.vc, si, cnt);
+        mw[j] = load_codes<FULL, true>(st.mc, si, cnt);
+        vw[j] = load_codes<FULL, true>(st.vc, si, cnt);
         f4 g4{}, p4{};
         if (FULL || cnt >= 4) {
             g4 = load_any4<G>(g, i);
@@ -350,7 +350,8 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
 // elements: fp32 parameters 2.36 ms and bf16 with a master 2.68 ms, 5.9 to 6.0 TB/s, bf16 1.65 ms, 6.1 TB/s, all by
 // HBM; bf16 by chance 2.44 ms, 4.1 TB/s, by the ALU (41e12 operations a second).
 // S state blocks per wave.  A long list takes four: their loads are in flight together (one block per trip:
-// 2.56 ms for fp32 parameters), and the scales' reductions and roots are paid once for four.  A short list, which
+// 2.56 ms for fp32 parameters), and the scales' reductions and roots are paid once for four.  (The codes with ordinary
+// loads: 2.47 ms, with ordinary stores 2.59.)  A short list, which
 // leaves most of the card idle, takes one, so that more waves share the work.
 template <int G, int PK, bool SR, int S>
 __global__ __launch_bounds__(kListBlock) void k_adamw8(ListLaunch L, ListPtrs ptrs, State8 st, AdamWParams ap)

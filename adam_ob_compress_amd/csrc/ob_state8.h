@@ -235,12 +235,12 @@ __device__ __forceinline__ void decode4(uint32_t w, float q, float x[4])
     }
 }
 
-// A lane's four codes, `cnt` of them in the tensor (4 or more: all).
-template <bool FULL>
+// A lane's four codes, `cnt` of them in the tensor (4 or more: all); NT: nontemporal.
+template <bool FULL, bool NT>
 __device__ __forceinline__ uint32_t load_codes(const void* codes, int64_t i, int cnt)
 {
     const uint8_t* c = static_cast<const uint8_t*>(codes) + i;
-    if (FULL || cnt >= 4) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(c));
+    if (FULL || cnt >= 4) return ldv<NT>(reinterpret_cast<const uint32_t*>(c));
     uint32_t w = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)

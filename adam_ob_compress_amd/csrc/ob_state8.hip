@@ -206,7 +206,7 @@ __device__ __forceinline__ void decode_span(int64_t n, int64_t at, const uint8_t
     const f4 q = load_scales<kSpan, FULL>(scales, at / kStateBlock, blocks);
     uint32_t w[kSpan];
 #pragma unroll
-    for (int j = 0; j < kSpan; ++j) w[j] = load_codes<FULL>(codes, at + j * kStateBlock + lane4, left - j * kStateBlock - lane4);
+    for (int j = 0; j < kSpan; ++j) w[j] = load_codes<FULL, false>(codes, at + j * kStateBlock + lane4, left - j * kStateBlock - lane4);
 #pragma unroll
     for (int j = 0; j < kSpan; ++j) {
         const int o = j * kStateBlock + lane4;
@@ -233,7 +233,7 @@ __device__ __forceinline__ int64_t span_start()
 
 // Bound by HBM's reads: 1e9 elements 1620 us, 6.2 TB/s.
 // The blocks of a launch's first row encode m, those of the second v.  (Both moments in each block: 1e9
-// elements 1714 us against 1614.  The decoder does not gain by it: 1833 against 1840.)
+// elements 1714 us against 1614.  The decoder does not gain by it.)
 __global__ __launch_bounds__(kListBlock) void k_state8_encode(int64_t n, const float* m, const float* v, uint8_t* mc,
                                                               float* mq, uint8_t* vc, float* vq)
 {
@@ -255,8 +255,9 @@ __global__ __launch_bounds__(kListBlock) void k_state8_encode(int64_t n, const f
     }
 }
 
-// Bound by HBM's writes (8 of 10 bytes an element): 1e9 elements 1833 us, 5.5 TB/s, where a fill of one of its
-// outputs runs at 6.6.  Ordinary stores: the same; several spans per wave one after the other: 1 to 6 percent slower.
+// Bound by HBM's writes (8 of 10 bytes an element): 1e9 elements 1.76 ms, 5.7 TB/s, where a fill of one of its
+// outputs runs at 6.6.  The codes by nontemporal loads: 1.83 ms; ordinary stores: the same; several spans per wave one
+// after the other: 1 to 6 percent slower.
 __global__ __launch_bounds__(kListBlock) void k_state8_decode(int64_t n, const uint8_t* mc, const float* mq,
                                                               const uint8_t* vc, const float* vq, float* m, float* v)
 {
