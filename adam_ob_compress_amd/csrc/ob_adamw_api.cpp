@@ -3,6 +3,7 @@
 #include "ob_adam.h"
 #include "ob_adamw.h"
 
+#include <algorithm>
 #include <cstddef>
 #include <vector>
 
@@ -12,8 +13,8 @@ static_assert(sizeof(ob_control) == 64 && offsetof(ob_control, bc1) == 24 && off
 namespace {
 
 struct Table {
-    std::vector<int64_t> first;      // [T + 1]: blocks of the tensor in place k are [first[k], first[k+1])
-    ob::ListItem* d_items = nullptr;
+    std::vector<int64_t> first;      // [T + 1]: items of the tensor in place k are [first[k], first[k+1])
+    const ob::ListItem* d_items = nullptr;
 };
 
 }  // namespace
@@ -22,7 +23,8 @@ struct ob_tensors_s {
     int device = 0;
     ob::ListShape shape;
     Table step, norm;
-    ob::ListTensor* d_tensors = nullptr;        // by place
+    const ob::ListTensor* d_tensors = nullptr;  // by place
+    void* d_tables = nullptr;                   // one allocation: the items of both tables, the tensors
 };
 
 namespace {
@@ -50,40 +52,30 @@ T* at(T* p, int64_t i)
     return p ? p + i : nullptr;
 }
 
+// The list's device is current for the duration of a call.
 struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
+    int back = -1;   // the device to return to; -1: none was left
+    bool ok;
     explicit DeviceGuard(int dev)
     {
-        if (hipGetDevice(&prev) != hipSuccess) {
-            ok = false;
-            return;
+        int cur = -1;
+        ok = hipGetDevice(&cur) == hipSuccess;
+        if (ok && cur != dev) {
+            ok = hipSetDevice(dev) == hipSuccess;
+            back = cur;
         }
-        if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
     }
     ~DeviceGuard()
     {
-        int cur = -1;
-        if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
+        if (back >= 0) (void)hipSetDevice(back);
     }
 };
 
 void free_list(ob_tensors l)
 {
     if (!l) return;
-    if (l->step.d_items) (void)hipFree(l->step.d_items);
-    if (l->norm.d_items) (void)hipFree(l->norm.d_items);
-    if (l->d_tensors) (void)hipFree(l->d_tensors);
+    if (l->d_tables) (void)hipFree(l->d_tables);
     delete l;
-}
-
-template <class T>
-hipError_t upload(T** to, const std::vector<T>& from)
-{
-    if (from.empty()) return hipSuccess;
-    const hipError_t e = hipMalloc(to, from.size() * sizeof(T));
-    if (e != hipSuccess) return e;
-    return hipMemcpy(*to, from.data(), from.size() * sizeof(T), hipMemcpyHostToDevice);
 }
 
 ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const int32_t* pd, const float* lr,
@@ -101,10 +93,21 @@ ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const 
     for (int32_t t : l->shape.order) tensors.push_back({l->shape.state_off[t], lr ? lr[t] : 1.0f, wd ? wd[t] : 1.0f});
 
     if (hipGetDevice(&l->device) != hipSuccess) return OB_ERR_HIP;
-    hipError_t e = upload(&l->step.d_items, step);
-    if (e == hipSuccess) e = upload(&l->norm.d_items, norm);
-    if (e == hipSuccess) e = upload(&l->d_tensors, tensors);
-    if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
+    const size_t a = step.size() * sizeof(ob::ListItem), b = norm.size() * sizeof(ob::ListItem);
+    const size_t bytes = a + b + tensors.size() * sizeof(ob::ListTensor);
+    if (bytes > 0) {
+        std::vector<char> tables(bytes);
+        std::copy_n(reinterpret_cast<const char*>(step.data()), a, tables.data());
+        std::copy_n(reinterpret_cast<const char*>(norm.data()), b, tables.data() + a);
+        std::copy_n(reinterpret_cast<const char*>(tensors.data()), bytes - a - b, tables.data() + a + b);
+        hipError_t e = hipMalloc(&l->d_tables, bytes);
+        if (e == hipSuccess) e = hipMemcpy(l->d_tables, tables.data(), bytes, hipMemcpyHostToDevice);
+        if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
+        const char* d = static_cast<const char*>(l->d_tables);
+        l->step.d_items = reinterpret_cast<const ob::ListItem*>(d);
+        l->norm.d_items = reinterpret_cast<const ob::ListItem*>(d + a);
+        l->d_tensors = reinterpret_cast<const ob::ListTensor*>(d + a + b);
+    }
     *out = l;
     return OB_OK;
 }
