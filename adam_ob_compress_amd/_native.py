@@ -1,4 +1,5 @@
-"""ctypes binding of libobadam.so: the C-ABI entry points under the same names.
+"""Binding of libobadam.so: the C-ABI entry points under the same names, by ctypes, and the calls over lists of
+tensors by the compiled module _obtorch (csrc/ob_torch.cpp).
 
 Argument marshalling only: torch tensors are turned into device pointers (``data_ptr()``) and torch's
 current HIP stream; every step of the optimizer runs in the library's HIP kernels.  There is no
@@ -131,6 +132,7 @@ def _obtorch():
     """Load the _obtorch module (raises if it has not been built)."""
     global _torch_module
     if _torch_module is None:
+        lib()   # the library that the module links to
         if not os.path.exists(os.path.join(_PKG, "_obtorch.so")):
             raise RuntimeError(f"{_PKG}/_obtorch.so is missing: build it with __graft_entry__.build()")
         from . import _obtorch as module
@@ -413,11 +415,6 @@ def ob_plan_read_timing(plan: Plan, kernel: int) -> tuple[float, int]:
 
 # ---- AdamW over lists of tensors ----
 
-# types of flat buffers by torch's scalar type codes: float32, int8, uint8, int32
-_KIND_DTYPES = {6: torch.float32, 1: torch.int8, 0: torch.uint8, 3: torch.int32}
-_F32, _I8, _U8, _I32 = b"\x06", b"\x01", b"\x00", b"\x03"
-
-
 class Tensors:
     """Owner of an ob_tensors handle (destroyed with the object): a list of tensors by size and type."""
 
@@ -428,13 +425,9 @@ class Tensors:
         self.p_dtypes = tuple(p_dtypes)
         self.device = device
         self.state_elems = int(lib().ob_tensors_state_elems(handle))
-        N, B, C = self.state_elems, self.state_elems // OB_STATE_BLOCK, OB_CONTROL_BYTES // 4
-        self._numels32, self._numels8, self._numels_control = (N, N, N, C), (N, N, B, N, B, C), (C,)
-        T = len(self.sizes)
-        self._array = ctypes.c_void_p * T
-        self._numels = (ctypes.c_int64 * T)(*self.sizes)
-        self._codes = {ds: (ctypes.c_int8 * T)(*[_obtorch().scalar_type(d) for d in ds])
-                       for ds in (self.g_dtypes, self.p_dtypes)}
+        module = _obtorch()
+        self.native = module.list(handle.value, self.sizes, bytes(module.scalar_type(d) for d in self.g_dtypes),
+                                  bytes(module.scalar_type(d) for d in self.p_dtypes), device.index, self.state_elems)
 
     def __len__(self) -> int:
         return len(self.sizes)
@@ -448,6 +441,7 @@ class Tensors:
 
     def destroy(self):
         if self.handle:
+            self.native = None
             _check(lib().ob_tensors_destroy(self.handle), "ob_tensors_destroy")
             self.handle = None
 
@@ -457,20 +451,22 @@ class Tensors:
         except Exception:
             pass
 
-    def _pointers(self, tensors, name, dtypes, others=None):
-        """The list's tensors as an array of device addresses; None (for others: where others has None) -> NULL."""
-        if not isinstance(tensors, (list, tuple)):
-            tensors = list(tensors)
-        if len(tensors) != len(self.sizes):
-            raise ValueError(f"{name} must have {len(self.sizes)} tensors, got {len(tensors)}")
-        out = self._array()
-        j = _obtorch().pointers(tensors, others, ctypes.addressof(self._numels), ctypes.addressof(self._codes[dtypes]),
-                                self.device.index, ctypes.addressof(out))
-        if j >= 0:
-            if tensors[j] is None:
+    def _fail(self, code, what, lists, flats):
+        """Raise what a call's code says: a status of the library, or the place of the first argument that is
+        not as it should be (lists: gradients, parameters; flats: (name, tensor, type, elements))."""
+        if code > 0:
+            raise ObError(code, what)
+        where, j = divmod(-code - 1, 1 << 32)
+        if where >= 2:
+            name, t, dtype, numel = flats[where - 2]
+        else:
+            name, ts = ("grads", "params")[where], lists[where]
+            if len(ts) != len(self.sizes):
+                raise ValueError(f"{name} must have {len(self.sizes)} tensors, got {len(ts)}")
+            if ts[j] is None:
                 raise TypeError(f"{name}[{j}] must be a torch.Tensor")
-            self._refuse(tensors[j], f"{name}[{j}]", dtypes[j], self.sizes[j])
-        return out
+            name, t, dtype, numel = f"{name}[{j}]", ts[j], (self.g_dtypes, self.p_dtypes)[where][j], self.sizes[j]
+        self._refuse(t, name, dtype, numel)
 
     def _refuse(self, t, name, dtype, numel):
         if not isinstance(t, torch.Tensor):
@@ -482,13 +478,6 @@ class Tensors:
         if t.is_neg():
             raise ValueError(f"{name} must not be a negated view")
         raise ValueError(f"{name} must be on {self.device}, the list's device (got {t.device})")
-
-    def _flat(self, tensors, names, kinds, numels):
-        """Device addresses of flat buffers on the list's device (None -> NULL); kinds: their types' codes."""
-        out = _obtorch().addresses(tensors, numels, kinds, self.device.index)
-        if isinstance(out, int):
-            self._refuse(tensors[out], names[out], _KIND_DTYPES[kinds[out]], numels[out])
-        return out
 
 
 def _dtype_list(d, count, name):
@@ -550,6 +539,19 @@ def _list_stream(tensors: Tensors, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _list(x):
+    return x if isinstance(x, (list, tuple)) else list(x)
+
+
+def _hparams(hp):
+    if type(hp) is not ob_adamw_hparams:
+        raise TypeError(f"hp must be made by adamw_hparams, got {type(hp)}")
+    return ctypes.addressof(hp)
+
+
+_CONTROL = (torch.int32, OB_CONTROL_BYTES // 4)
+
+
 def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp: ob_adamw_hparams | None = None,
                  stream=None):
     """Global norm of the gradients (a list; None: no gradient) and the factor that clips it to max_norm
@@ -557,39 +559,41 @@ def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp:
     corrections of the step that follows."""
     if control is None:
         raise TypeError("control must be a torch.Tensor")
-    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
-    c, = tensors._flat((control,), ("control",), _I32, tensors._numels_control)
-    _check(lib().ob_grad_norm(tensors.handle, g, g_mult, max_norm, None if hp is None else ctypes.byref(hp), c,
-                              _list_stream(tensors, stream)), "ob_grad_norm")
+    grads = _list(grads)
+    code = _obtorch().grad_norm(tensors.native, grads, g_mult, max_norm, None if hp is None else _hparams(hp), control,
+                                _list_stream(tensors, stream))
+    if code:
+        tensors._fail(code, "ob_grad_norm", (grads,), (("control", control, *_CONTROL),))
 
 
 def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None):
     """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems."""
-    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
-    p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
-    f = tensors._flat((master, m, v, control), ("master", "m", "v", "control"), _F32 * 3 + _I32, tensors._numels32)
-    _check(lib().ob_adamw_step(tensors.handle, g, p, *f[:3], ctypes.byref(hp), f[3], _list_stream(tensors, stream)),
-           "ob_adamw_step")
+    grads, params = _list(grads), _list(params)
+    code = _obtorch().adamw_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master, m, v,
+                                 control)
+    if code:
+        f32 = (torch.float32, tensors.state_elems)
+        tensors._fail(code, "ob_adamw_step", (grads, params),
+                      (("master", master, *f32), ("m", m, *f32), ("v", v, *f32), ("control", control, *_CONTROL)))
 
 
 def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, v_scales, hp: ob_adamw_hparams,
                    master=None, control=None, stream=None):
     """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256."""
-    g = tensors._pointers(grads, "grads", tensors.g_dtypes)
-    p = tensors._pointers(params, "params", tensors.p_dtypes, grads)
-    f = tensors._flat((master, m_codes, m_scales, v_codes, v_scales, control),
-                      ("master", "m_codes", "m_scales", "v_codes", "v_scales", "control"),
-                      _F32 + _I8 + _F32 + _U8 + _F32 + _I32, tensors._numels8)
-    _check(lib().ob_adamw8_step(tensors.handle, g, p, *f[:5], ctypes.byref(hp), f[5], _list_stream(tensors, stream)),
-           "ob_adamw8_step")
+    grads, params = _list(grads), _list(params)
+    code = _obtorch().adamw8_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master,
+                                  m_codes, m_scales, v_codes, v_scales, control)
+    if code:
+        N = tensors.state_elems
+        scales = (torch.float32, N // OB_STATE_BLOCK)
+        tensors._fail(code, "ob_adamw8_step", (grads, params),
+                      (("master", master, torch.float32, N), ("m_codes", m_codes, torch.int8, N),
+                       ("m_scales", m_scales, *scales), ("v_codes", v_codes, torch.uint8, N),
+                       ("v_scales", v_scales, *scales), ("control", control, *_CONTROL)))
 
 
-_STATE8_NAMES = ("m", "v", "m_codes", "m_scales", "v_codes", "v_scales")
-
-
-def _state8_pointers(*tensors):
-    """(n, device index, addresses) of a conversion's tensors in the order of _STATE8_NAMES, checked; either moment may
-    be None throughout."""
+def _state8(what, encode, stream, *tensors):
+    """A conversion of (m, v, m_codes, m_scales, v_codes, v_scales); either moment may be None throughout."""
     m, v = tensors[:2]
     lead = m if m is not None else v
     if lead is None:
@@ -597,35 +601,34 @@ def _state8_pointers(*tensors):
     for name, x, codes, scales in (("m", m, *tensors[2:4]), ("v", v, *tensors[4:])):
         if (x is None) != (codes is None) or (x is None) != (scales is None):
             raise ValueError(f"{name}, {name}_codes and {name}_scales come together")
-    n = lead.numel()
-    blocks = -(-n // OB_STATE_BLOCK)
-    index = lead.get_device()
-    numels, kinds = (n, n, n, blocks, n, blocks), _F32 * 2 + _I8 + _F32 + _U8 + _F32
-    out = _obtorch().addresses(tensors, numels, kinds, index)
-    if isinstance(out, int):
-        for t, name, kind, numel in zip(tensors, _STATE8_NAMES, kinds, numels):
-            _want(t, name, _KIND_DTYPES[kind], numel)
-        for t, name in zip(tensors, _STATE8_NAMES):
+    n, index = lead.numel(), lead.get_device()
+    if index < 0:
+        code = -1   # not on a GPU
+    elif index == torch.cuda.current_device():
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream).value or 0
+        code = _obtorch().state8(encode, n, index, s, *tensors)
+    else:
+        with torch.cuda.device(index):
+            code = _obtorch().state8(encode, n, index, _stream(stream).value or 0, *tensors)
+    if code > 0:
+        raise ObError(code, what)
+    if code < 0:
+        blocks = -(-n // OB_STATE_BLOCK)
+        names = ("m", "v", "m_codes", "m_scales", "v_codes", "v_scales")
+        dtypes = (torch.float32, torch.float32, torch.int8, torch.float32, torch.uint8, torch.float32)
+        for t, name, dtype, numel in zip(tensors, names, dtypes, (n, n, n, blocks, n, blocks)):
+            _want(t, name, dtype, numel)
+        for t, name in zip(tensors, names):
             _dev(t, name)
-        raise ValueError(f"{_STATE8_NAMES[out]} must be on {lead.device} (got {tensors[out].device})")
-    return n, index, out
-
-
-def _on_device(index, stream, call):
-    """call(raw stream) with the device current, as a call without a handle of its own needs it."""
-    if index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
-    with torch.cuda.device(index):
-        return call(_stream(stream))
+        j = (-code - 1 >> 32) - 2
+        raise ValueError(f"{names[j]} must be on {lead.device} (got {tensors[j].device})")
 
 
 def ob_state8_encode(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
     """fp32 moments into the 8-bit format, rounded to nearest (m or v with its codes and scales: None)."""
-    n, index, a = _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales)
-    _check(_on_device(index, stream, lambda s: lib().ob_state8_encode(n, *a, s)), "ob_state8_encode")
+    _state8("ob_state8_encode", True, stream, m, v, m_codes, m_scales, v_codes, v_scales)
 
 
 def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
     """The fp32 moments that 8-bit codes and scales stand for (m or v with its codes and scales: None)."""
-    n, index, (pm, pv, *codes) = _state8_pointers(m, v, m_codes, m_scales, v_codes, v_scales)
-    _check(_on_device(index, stream, lambda s: lib().ob_state8_decode(n, *codes, pm, pv, s)), "ob_state8_decode")
+    _state8("ob_state8_decode", False, stream, m, v, m_codes, m_scales, v_codes, v_scales)

@@ -80,15 +80,16 @@ TORCH_LIB = os.path.join(PKG, "_obtorch.so")
 
 
 def build_torch(verbose: bool = False) -> str:
-    """Compile the Python module that reads device addresses out of lists of torch tensors."""
+    """Compile the Python module that takes the calls over lists of torch tensors to libobadam.so (built before)."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{root}/include",
-           f"-I{root}/include/torch/csrc/api/include", "-I" + sysconfig.get_paths()["include"], "-o", TORCH_LIB + ".tmp",
-           TORCH_SRC, f"-L{root}/lib", "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-I{INCLUDE}", f"-I{root}/include",
+           f"-I{root}/include/torch/csrc/api/include", "-I" + sysconfig.get_paths()["include"], "-I/opt/rocm/include",
+           "-o", TORCH_LIB + ".tmp", TORCH_SRC, f"-L{root}/lib", "-lc10", "-ltorch_cpu", "-ltorch_python", f"-L{PKG}",
+           "-lobadam", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

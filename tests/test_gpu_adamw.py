@@ -711,6 +711,24 @@ def test_refusals():
         call(v_scales=L.vq[:1])
     with pytest.raises(ValueError, match="control"):
         call(control=ctl[:16])
+    with pytest.raises(ValueError, match="control"):
+        ob.ob_grad_norm(L.list, L.grads, ctl[:16])
+    with pytest.raises(ValueError, match=r"m_codes must be on the GPU"):
+        call(m_codes=L.mc.cpu())
+    with pytest.raises(TypeError, match=r"grads\[0\]"):
+        call(grads=[3, L.grads[1]])
+    with pytest.raises(ValueError, match="dense"):
+        call(grads=[torch.zeros(300, dtype=torch.bfloat16, device=DEV).to_sparse(), L.grads[1]])
+    with pytest.raises(TypeError, match="adamw_hparams"):
+        call(hp=ob.hparams())
+    with pytest.raises(TypeError):
+        ob.ob_grad_norm(L.list, L.grads, ctl, "1")
+    with pytest.raises(TypeError):
+        ob.ob_grad_norm(L.list, L.grads, ctl[:16], "1")
+    with pytest.raises(ValueError, match="destroyed"):
+        gone = ob.ob_tensors_create([300, 5], torch.bfloat16, torch.bfloat16)
+        gone.destroy()
+        call(tensors=gone)
     with pytest.raises(ob.ObError) as e:
         call(params=[L.params[0], L.params[0][10:15]])   # one parameter inside another
     assert e.value.status == 1
@@ -724,7 +742,7 @@ def test_refusals():
                             torch.zeros(2, device=DEV), None, None)
     assert e.value.status == 2
     # straight to the C ABI: missing states and addresses
-    g, p = (L.list._pointers(x, "x", L.list.g_dtypes) for x in (L.grads, L.params))
+    g, p = ((ctypes.c_void_p * 2)(*[t.data_ptr() for t in x]) for x in (L.grads, L.params))
     lib, P = ob.lib(), ctypes.c_void_p
     h = ctypes.byref(hp)
     assert lib.ob_adamw_step(L.list.handle, g, p, None, None, P(0x1000), h, None, None) == 1
