@@ -475,9 +475,17 @@ class Tensors:
             raise ValueError(f"{name} must be a dense tensor, got {t.layout}")
         _want(t, name, dtype, numel)
         _dev(t, name)
-        if t.is_neg():
-            raise ValueError(f"{name} must not be a negated view")
+        _want_memory(t, name)
         raise ValueError(f"{name} must be on {self.device}, the list's device (got {t.device})")
+
+
+def _want_memory(t, name):
+    if t is None:
+        return
+    if t.is_neg():
+        raise ValueError(f"{name} must not be a negated view")
+    if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size():
+        raise ValueError(f"{name} must have its memory (its storage was released or shrunk)")
 
 
 def _dtype_list(d, count, name):
@@ -620,6 +628,7 @@ def _state8(what, encode, stream, *tensors):
             _want(t, name, dtype, numel)
         for t, name in zip(tensors, names):
             _dev(t, name)
+            _want_memory(t, name)
         j = (-code - 1 >> 32) - 2
         raise ValueError(f"{names[j]} must be on {lead.device} (got {tensors[j].device})")
 

@@ -37,20 +37,23 @@ struct Bad {
     PyObject* code() const { return PyLong_FromLongLong(-(1 + (where << 32) + index)); }
 };
 
-// The address of a dense GPU tensor of this kind; throws Bad otherwise.  A tensor without memory of its own (a fake one)
-// throws c10's error, which the callers take for Bad too.
+// The address of a dense GPU tensor of this kind; throws Bad otherwise, also for one whose storage does not hold it (released
+// or shrunk: its address is NULL, which would mean that the tensor is left out, or its end is behind the memory).
 void* address(PyObject* item, at::ScalarType type, int64_t numel, long device, Bad at)
 {
     if (!THPVariable_Check(item)) throw at;
     const at::Tensor& t = THPVariable_Unpack(item);
     if (t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != device || t.is_neg() || t.scalar_type() != type ||
-        t.numel() != numel || !t.is_contiguous())
+        t.numel() != numel || !t.is_contiguous() || !t.has_storage())
         throw at;
-    try {
-        return numel > 0 ? t.data_ptr() : nullptr;
+    if (numel == 0) return nullptr;
+    void* p = nullptr;
+    try {   // a tensor without memory of its own (a fake one) throws c10's error
+        if (t.storage().nbytes() / t.itemsize() >= static_cast<size_t>(t.storage_offset() + numel)) p = t.data_ptr();
     } catch (...) {
-        throw at;
     }
+    if (!p) throw at;
+    return p;
 }
 
 // The same for an optional flat buffer: None -> NULL.

@@ -755,6 +755,43 @@ def test_refusals():
     assert all(np.array_equal(x, y) for x, y in zip(before["p"], after["p"])) and np.array_equal(before["mc"], after["mc"])
 
 
+def test_tensors_without_their_memory_are_refused():
+    """A released storage has no address, which would read as an argument left out; a shrunk one ends too early.  All
+    are refused on the host, before a launch."""
+    def gone(like, nbytes=0):
+        t = like.clone()
+        t.untyped_storage().resize_(nbytes)
+        return t
+
+    for bits in (32, 8):
+        L = Lists([300, 5], "bf16", "bf16", seed=1, bits=bits, master=True)
+        hp, ctl = hparams(), ob.control_create(DEV)
+        states = dict(m=L.m, v=L.v) if bits == 32 else dict(m_codes=L.mc, m_scales=L.mq, v_codes=L.vc, v_scales=L.vq)
+        good = dict(tensors=L.list, grads=L.grads, params=L.params, hp=hp, master=L.master, control=ctl, **states)
+        step = ob.ob_adamw_step if bits == 32 else ob.ob_adamw8_step
+        tensors = [*L.params, L.master, *states.values()]
+        before = [t.clone() for t in tensors]
+        for nbytes in (0, 4):
+            for k in ("master", "control", *states):
+                with pytest.raises(ValueError, match=f"{k} must have its memory"):
+                    step(**{**good, k: gone(good[k], nbytes)})
+            for k in ("grads", "params"):
+                with pytest.raises(ValueError, match=rf"{k}\[0\] must have its memory"):
+                    step(**{**good, k: [gone(good[k][0], nbytes), good[k][1]]})
+            with pytest.raises(ValueError, match=r"grads\[1\] must have its memory"):
+                ob.ob_grad_norm(L.list, [L.grads[0], gone(L.grads[1], nbytes)], ctl)
+            with pytest.raises(ValueError, match="control must have its memory"):
+                ob.ob_grad_norm(L.list, L.grads, gone(ctl, nbytes))
+        for t, b in zip(tensors, before):
+            assert torch.equal(t, b)
+    x = torch.zeros(300, device=DEV)
+    codes, scales = torch.zeros(300, dtype=torch.int8, device=DEV), torch.zeros(2, device=DEV)
+    for call in (lambda: ob.ob_state8_encode(gone(x), None, codes, scales, None, None),
+                 lambda: ob.ob_state8_decode(codes, gone(scales), None, None, x, None)):
+        with pytest.raises(ValueError, match="must have its memory"):
+            call()
+
+
 def test_empty_lists():
     hp, ctl = hparams(), ob.control_create(DEV)
     for sizes in ([], [0, 0]):
