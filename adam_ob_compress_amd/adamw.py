@@ -107,11 +107,16 @@ class AdamW:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("a captured step needs max_norm (inf: no clipping): its count is kept on the GPU")
             self.hp.step += 1
-        if self.state_bits == 32:
-            nat.ob_adamw_step(self.list, grads, self.params, self.m, self.v, self.hp, self.master, self.control, stream)
-        else:
-            nat.ob_adamw8_step(self.list, grads, self.params, self.m_codes, self.m_scales, self.v_codes, self.v_scales,
-                               self.hp, self.master, self.control, stream)
+        try:
+            if self.state_bits == 32:
+                nat.ob_adamw_step(self.list, grads, self.params, self.m, self.v, self.hp, self.master, self.control, stream)
+            else:
+                nat.ob_adamw8_step(self.list, grads, self.params, self.m_codes, self.m_scales, self.v_codes,
+                                   self.v_scales, self.hp, self.master, self.control, stream)
+        except Exception:
+            if self.control is None:
+                self.hp.step -= 1   # a refused step is not counted
+            raise
         torch.autograd.graph.increment_version([p for p, g in zip(self.params, grads) if g is not None])
 
     def moments(self):

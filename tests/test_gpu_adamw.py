@@ -940,3 +940,19 @@ def test_driver_refusals():
     opt.step([torch.zeros_like(p) for p in net.parameters()])
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_driver_does_not_count_a_refused_step(bits, max_norm):
+    a, b = _model(torch.float32), _model(torch.float32)
+    first, second = (ob.AdamW(net.parameters(), lr=1e-2, state_bits=bits, max_norm=max_norm) for net in (a, b))
+    for bad in ([p.half() for p in a.parameters()], [p.detach().cpu() for p in a.parameters()], []):
+        with pytest.raises((TypeError, ValueError)):
+            first.step(bad)
+        assert first.steps() == 0
+    _train(a, first, 2)
+    _train(b, second, 2)
+    assert first.steps() == second.steps() == 2
+    for p, q in zip(a.parameters(), b.parameters()):
+        assert torch.equal(p, q)
