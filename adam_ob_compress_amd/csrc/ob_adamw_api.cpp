@@ -102,6 +102,8 @@ ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const 
         std::copy_n(reinterpret_cast<const char*>(tensors.data()), bytes - a - b, tables.data() + a + b);
         hipError_t e = hipMalloc(&l->d_tables, bytes);
         if (e == hipSuccess) e = hipMemcpy(l->d_tables, tables.data(), bytes, hipMemcpyHostToDevice);
+        // a first call may be on a stream that does not wait for the null stream
+        if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
         if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
         const char* d = static_cast<const char*>(l->d_tables);
         l->step.d_items = reinterpret_cast<const ob::ListItem*>(d);
