@@ -28,7 +28,7 @@ struct NormPtrs {
 };
 
 // How a tensor's parameters are held.
-enum { PK_F32 = 0, PK_BF16 = 1, PK_F16 = 2, PK_MASTER_BF16 = 3, PK_MASTER_F16 = 4, kParKinds = 5 };
+enum { PK_F32 = 0, PK_BF16 = 1, PK_F16 = 2, PK_MASTER_BF16 = 3, PK_MASTER_F16 = 4 };
 
 struct ListLaunch {
     const ListItem* items;       // of this launch
