@@ -24,7 +24,7 @@ constexpr float kBelow = 1.0f / 8192.0f;
 // relative error of its parts (1/q and root 1 ulp each, product half an ulp, under a root that halves them; for v
 // one root more; the borders' own roundings): at most 3.8e-5 for m (y <= 127) and 8e-5 for v (y <= 255).
 constexpr float kNearM = 1.0f / 16384.0f, kNearV = 1.0f / 8192.0f;
-// The same for chance, in units of the 16 random bits: below 1.6 for m and 4.2 for v.
+// The same for chance, in units of the 16 random bits, around the circle of 65536 of them: below 1.6 for m and 4.2 for v.
 constexpr float kNearChanceM = 4.0f, kNearChanceV = 8.0f;
 
 typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
@@ -210,7 +210,9 @@ __device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4
                 gap = odd;
             }
             const float e = fmaf(num, 65536.0f, -static_cast<float>(bits(k)) * gap);
-            near = near || fabsf(e) < (V ? kNearChanceV : kNearChanceM) * gap;
+            // Near: |e| close to 0, or to 65536 gaps, where a value so close to a code may have been counted from
+            // the wrong side of it and the bits are at the other end of their range.
+            near = near || fabsf(fmaf(gap, -32768.0f, fabsf(e))) > (32768.0f - (V ? kNearChanceV : kNearChanceM)) * gap;
             const float up = c + fminf(fmaxf(e * 0x1p100f, 0.0f), 1.0f);   // one above where e > 0
             put(V ? fmaxf(up, x[k] > 0.0f ? 1.0f : 0.0f) : up, k);
         }

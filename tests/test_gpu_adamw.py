@@ -956,3 +956,53 @@ def test_driver_does_not_count_a_refused_step(bits, max_norm):
     assert first.steps() == second.steps() == 2
     for p, q in zip(a.parameters(), b.parameters()):
         assert torch.equal(p, q)
+
+
+def _check_codes(L, g, hp, t, blocks):
+    """The given state blocks of a list of one fp32 tensor after its first step, against the rule."""
+    words = ref.philox_words(hp.sr_seed, t, L.N).reshape(-1, 256)[blocks]
+    m, v = ref.adamw8_moments(g.reshape(-1, 256)[blocks].reshape(-1).astype(np.float64), 0.0, 0.0, beta1=hp.beta1, beta2=hp.beta2)
+    where = torch.from_numpy(blocks).to(DEV)
+    for x, second, c, q in ((m, False, L.mc, L.mq), (v, True, L.vc, L.vq)):
+        codes, scales = ref.encode(x, second, words.reshape(-1))
+        got = c.view(-1, 256)[where].cpu().numpy().reshape(-1)
+        bad = np.nonzero(got != codes)[0]
+        assert np.array_equal(q[where].cpu().numpy(), scales), (second, t)
+        assert len(bad) == 0, (second, t, len(bad), x[bad][:4], scales[bad // 256][:4], words.reshape(-1)[bad][:4], got[bad][:4], codes[bad][:4])
+
+
+def _first_step_by_chance(L, g, t, seed):
+    """One step from zero moments in which they become g and fl(g^2)."""
+    L.mc.zero_(), L.mq.zero_(), L.vc.zero_(), L.vq.zero_()
+    L.grads = [torch.from_numpy(g).to(DEV)]
+    hp = hparams(beta1=0.0, beta2=0.0, step=t, rounding=1, sr_seed=seed)
+    L.step(hp)
+    torch.cuda.synchronize()
+    return hp
+
+
+@pytest.mark.parametrize("second", [False, True])
+@pytest.mark.parametrize("blocks,steps", [(4000, 12), (36_000, 4)])   # one and four state blocks per wave
+def test_codes_by_chance_beside_whole_codes(blocks, steps, second):
+    """Moments within 3 fp32 steps of a code's value, where the random bits are the 4 smallest or largest ones: the rule's
+    code there depends on which side of the value a moment lies."""
+    n = blocks * 256
+    L = Lists([n], "f32", "f32", seed=31, bits=8, shift=False)
+    rng = np.random.default_rng(31)
+    top = rng.uniform(0.5, 2.0, blocks).astype(np.float32)
+    if second:
+        q = ref.r32(ref.r32(np.sqrt(ref.r32(top.astype(np.float64) ** 2))) * ref.r32(1 / 255 ** 2))
+    else:
+        q = ref.r32(top.astype(np.float64) * ref.r32(1 / 127 ** 2))
+    for t in range(1, steps + 1):
+        words = ref.philox_words(5, t, n)
+        bits = words >> 16 if second else words & 0xFFFF
+        at = np.nonzero(((bits < 4) | (bits > 65531)) & (np.arange(n) % 256 != 0))[0]
+        k = rng.integers(1, 255 if second else 127, len(at))
+        x = ref.code_value(k, q[at // 256], second).astype(np.float32)
+        x = (x.view(np.int32) + rng.integers(-3, 4, len(at), dtype=np.int32)).view(np.float32)
+        g = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+        g[::256] = top
+        g[at] = np.sqrt(x.astype(np.float64)) if second else x * rng.choice(np.float32([-1, 1]), len(at))
+        hp = _first_step_by_chance(L, g, t, 5)
+        _check_codes(L, g, hp, t, np.unique(at // 256))
