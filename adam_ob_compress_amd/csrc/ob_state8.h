@@ -26,6 +26,9 @@ constexpr float kBelow = 1.0f / 8192.0f;
 constexpr float kNearM = 1.0f / 16384.0f, kNearV = 1.0f / 8192.0f;
 // The same for chance, in units of the 16 random bits, around the circle of 65536 of them: below 1.6 for m and 4.2 for v.
 constexpr float kNearChanceM = 4.0f, kNearChanceV = 8.0f;
+// Scales of v below 2^-63 are settled as well by chance: their code 1 stands for a subnormal q^2, and the hardware's root of
+// a subnormal v, which may be due code 2, is 0.  (To nearest that v has code 1: the border to 2 is 5 q^2 > 2^-126.)
+constexpr uint32_t kSmallScaleBits = 0x20000000u;  // 2^-63
 
 typedef float f4e __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -217,7 +220,8 @@ __device__ __forceinline__ uint32_t encode4(const float x[4], const float root[4
             put(V ? fmaxf(up, x[k] > 0.0f ? 1.0f : 0.0f) : up, k);
         }
     }
-    if (__builtin_amdgcn_ballot_w64(near) != 0) {
+    const bool small = V && SR && __float_as_uint(q) - 1u < kSmallScaleBits - 1u;   // 0 < q < 2^-63
+    if (small || __builtin_amdgcn_ballot_w64(near) != 0) {
         r = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) put(code_by_rule<V, SR>(fabsf(x[k]), V ? root[k] : 0.0f, q, rq, bits(k)), k);

@@ -1006,3 +1006,17 @@ def test_codes_by_chance_beside_whole_codes(blocks, steps, second):
         g[at] = np.sqrt(x.astype(np.float64)) if second else x * rng.choice(np.float32([-1, 1]), len(at))
         hp = _first_step_by_chance(L, g, t, 5)
         _check_codes(L, g, hp, t, np.unique(at // 256))
+
+
+@pytest.mark.parametrize("blocks", [64, 40_000])   # one and four state blocks per wave
+def test_codes_by_chance_of_subnormal_second_moments(blocks):
+    """The smallest blocks that have a scale: largest v in [2^-96, 2^-92), the others subnormal, where some get code 2."""
+    n = blocks * 256
+    L = Lists([n], "f32", "f32", seed=32, bits=8, shift=False)
+    rng = np.random.default_rng(32)
+    v = 2.0 ** rng.uniform(-129, -125, n)
+    v[::256] = 2.0 ** rng.uniform(-96, -92, blocks)
+    g = np.sqrt(v).astype(np.float32)
+    hp = _first_step_by_chance(L, g, 1, 6)
+    assert int((L.vc == 2).sum()) > n // 64
+    _check_codes(L, g, hp, 1, np.arange(64))
