@@ -203,7 +203,11 @@ __global__ __launch_bounds__(kListBlock) void k_adamw(ListLaunch L, ListPtrs ptr
     if (s.skip) return;
     const int64_t i = it.start + at, si = tn.state_off + i;
     u4 w{};
-    if (SR) w = philox_lanes(ap.seed, s.t | kParStream, (si - 4 * static_cast<int>(threadIdx.x)) >> 2, threadIdx.x);
+    if (SR) {   // by wave: a tensor's state starts at a multiple of 256 elements, which are a wave's 64 lanes
+        const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+        const int64_t first = tn.state_off + it.start + static_cast<int>(blockIdx.x % kStepTiles) * kListTile + wave * kStateBlock;
+        w = philox_lanes(ap.seed, s.t | kParStream, first >> 2, threadIdx.x & 63);
+    }
     if (cnt >= 4) {
         const f4 gv = load_any4<G>(g, i);
         f4 mv = ld4<true>(st.m, si), vv = ld4<true>(st.v, si), pv = P::load4(p, st.master, i, si);

@@ -129,8 +129,8 @@ __device__ __forceinline__ float code_value(float k, float q)
     return V ? mul(r, r) : r;
 }
 
-// Philox4x32-10 (ob_device.h) at the counter (blk, t) with blk = base + lane: base is uniform and a multiple of the
-// lanes that add to it, so the counter's high word and all that depends on it alone stay in scalar registers.
+// Philox4x32-10 (ob_device.h) at the counter (blk, t) with blk = base + lane: base is uniform and a multiple of 64, lane below
+// 64, so the counter's high word and all that depends on it alone stay in scalar registers.
 __device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) { return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96); }
 
 __device__ __forceinline__ u4 philox_lanes(uint64_t seed, uint64_t t, int64_t base, uint32_t lane)

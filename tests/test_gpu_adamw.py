@@ -1020,3 +1020,31 @@ def test_codes_by_chance_of_subnormal_second_moments(blocks):
     hp = _first_step_by_chance(L, g, 1, 6)
     assert int((L.vc == 2).sum()) > n // 64
     _check_codes(L, g, hp, 1, np.arange(64))
+
+
+def test_words_by_chance_past_a_counter_of_32_bits():
+    """fp32 states around state index 2^34, where the generator's counter passes 32 bits, in a work group that starts
+    256 and 768 elements before: the words of the rule.  The tensors before have no gradient."""
+    where = (1 << 34) - 256
+    for first in (0, 512):
+        lst = ob.ob_tensors_create([where - first, 4099 + first], torch.bfloat16, torch.bfloat16)
+        o, n = lst.state_offset(1), 4099 + first
+        assert o == where - first
+        m, v = (torch.empty(lst.state_elems, device=DEV) for _ in range(2))   # 64 GiB each, written in the second tensor only
+        m[o:], v[o:] = 0, 0
+        rng = np.random.default_rng(3)
+        x = torch.from_numpy(rng.standard_normal(n) * 0.05).to(DEV).bfloat16()
+        g = torch.from_numpy(rng.standard_normal(n) * 1e-3).to(DEV).bfloat16()
+        p = x.clone()
+        hp = hparams(step=1, rounding=1, sr_seed=0xABCDEF0123456789)
+        ob.ob_adamw_step(lst, [None, g], [None, p], m, v, hp)
+        _, _, want, u = ref.adamw(f64(g), 0.0, 0.0, f64(x), lr=float(hp.lr), beta1=hp.beta1, beta2=hp.beta2, eps=hp.eps,
+                                  wd=float(hp.weight_decay), bc1=ref.bc(hp.beta1, 1), bc2=ref.bc(hp.beta2, 1))
+        tol = EPS32 / 2 * np.abs(want) * (1 + 1e-6) + 2.0 ** -46 * (np.abs(f64(x)) + np.abs(float(hp.lr) * u))
+        lo, hi = (from16(oracle.to_format_sr(y.astype(np.float32), "bf16", hp.sr_seed, 1 | ref.PAR_STREAM, o), "bf16")
+                  for y in (want - tol, want + tol))
+        got = f64(p)
+        bad = np.nonzero(~((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))))[0]
+        assert len(bad) == 0, (first, len(bad), bad[:5])
+        del m, v
+        torch.cuda.empty_cache()
