@@ -114,6 +114,8 @@ def lib() -> ctypes.CDLL:
         "ob_grad_norm": (I32, [P, P, ctypes.c_float, ctypes.c_float, ctypes.POINTER(ob_adamw_hparams), P, P]),
         "ob_adamw_step": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P, P]),
         "ob_adamw8_step": (I32, [P, P, P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P, P]),
+        "ob_adamw_check": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P]),
+        "ob_adamw8_check": (I32, [P, P, P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P]),
         "ob_state8_encode": (I32, [I64, P, P, P, P, P, P, P]),
         "ob_state8_decode": (I32, [I64, P, P, P, P, P, P, P]),
     }
@@ -574,11 +576,19 @@ def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp:
         tensors._fail(code, "ob_grad_norm", (grads,), (("control", control, *_CONTROL),))
 
 
-def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None):
-    """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems."""
+def _norm_control(norm, control):
+    if norm is not None and control is None:
+        raise TypeError("control must be a torch.Tensor")
+    return norm
+
+
+def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None,
+                  norm=None):
+    """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems.  norm=(g_mult,
+    max_norm): ob_grad_norm with these and hp first, once the arguments of both are checked."""
     grads, params = _list(grads), _list(params)
     code = _obtorch().adamw_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master, m, v,
-                                 control)
+                                 control, _norm_control(norm, control))
     if code:
         f32 = (torch.float32, tensors.state_elems)
         tensors._fail(code, "ob_adamw_step", (grads, params),
@@ -586,11 +596,12 @@ def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, m
 
 
 def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, v_scales, hp: ob_adamw_hparams,
-                   master=None, control=None, stream=None):
-    """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256."""
+                   master=None, control=None, stream=None, norm=None):
+    """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256.  norm as
+    ob_adamw_step."""
     grads, params = _list(grads), _list(params)
     code = _obtorch().adamw8_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master,
-                                  m_codes, m_scales, v_codes, v_scales, control)
+                                  m_codes, m_scales, v_codes, v_scales, control, _norm_control(norm, control))
     if code:
         N = tensors.state_elems
         scales = (torch.float32, N // OB_STATE_BLOCK)

@@ -99,8 +99,9 @@ class AdamW:
     def step(self, grads=None, loss_scale: float = 1.0, stream=None):
         """One step; loss_scale: what the gradients were multiplied with (other than 1 needs max_norm)."""
         grads = [p.grad for p in self.params] if grads is None else list(grads)
+        norm = None
         if self.control is not None:
-            nat.ob_grad_norm(self.list, grads, self.control, 1.0 / loss_scale, self.max_norm, self.hp, stream)
+            norm = (1.0 / loss_scale, self.max_norm)
         else:
             if loss_scale != 1.0:
                 raise ValueError("a loss scale needs max_norm (inf: no clipping)")
@@ -109,10 +110,11 @@ class AdamW:
             self.hp.step += 1
         try:
             if self.state_bits == 32:
-                nat.ob_adamw_step(self.list, grads, self.params, self.m, self.v, self.hp, self.master, self.control, stream)
+                nat.ob_adamw_step(self.list, grads, self.params, self.m, self.v, self.hp, self.master, self.control, stream,
+                                  norm)
             else:
                 nat.ob_adamw8_step(self.list, grads, self.params, self.m_codes, self.m_scales, self.v_codes,
-                                   self.v_scales, self.hp, self.master, self.control, stream)
+                                   self.v_scales, self.hp, self.master, self.control, stream, norm)
         except Exception:
             if self.control is None:
                 self.hp.step -= 1   # a refused step is not counted

@@ -245,14 +245,23 @@ try {
     return OB_ERR_OOM;
 }
 
-ob_status ob_adamw_step(ob_tensors list, const void* const* g, void* const* p, float* master, float* m, float* v,
-                        const ob_adamw_hparams* hp, const ob_control* control, hipStream_t stream)
+ob_status ob_adamw_check(ob_tensors list, const void* const* g, void* const* p, const float* master, const float* m,
+                         const float* v, const ob_adamw_hparams* hp, const ob_control* control)
 try {
     if (!list) return OB_ERR_ARG;
     if (ob_status st = ob::check_step(list->shape, g, p, master, false, hp, control)) return st;
     if (list->shape.n == 0) return OB_OK;
     if (!m || !v) return OB_ERR_ARG;
-    if (!ob::is_aligned(m, 16) || !ob::is_aligned(v, 16)) return OB_ERR_ALIGN;
+    return ob::is_aligned(m, 16) && ob::is_aligned(v, 16) ? OB_OK : OB_ERR_ALIGN;
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+ob_status ob_adamw_step(ob_tensors list, const void* const* g, void* const* p, float* master, float* m, float* v,
+                        const ob_adamw_hparams* hp, const ob_control* control, hipStream_t stream)
+try {
+    if (ob_status st = ob_adamw_check(list, g, p, master, m, v, hp, control)) return st;
+    if (list->shape.n == 0) return OB_OK;
     const ob::AdamWParams ap = adamw_params(hp, control);
     const ob::State32 state{master, m, v};
     DeviceGuard guard(list->device);
@@ -267,9 +276,9 @@ try {
     return OB_ERR_OOM;
 }
 
-ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, float* master, int8_t* m_codes,
-                         float* m_scales, uint8_t* v_codes, float* v_scales, const ob_adamw_hparams* hp,
-                         const ob_control* control, hipStream_t stream)
+ob_status ob_adamw8_check(ob_tensors list, const void* const* g, void* const* p, const float* master,
+                          const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes, const float* v_scales,
+                          const ob_adamw_hparams* hp, const ob_control* control)
 try {
     if (!list) return OB_ERR_ARG;
     if (ob_status st = ob::check_step(list->shape, g, p, master, true, hp, control)) return st;
@@ -277,6 +286,17 @@ try {
     if (!m_codes || !m_scales || !v_codes || !v_scales) return OB_ERR_ARG;
     if (!ob::is_aligned(m_codes, 4) || !ob::is_aligned(v_codes, 4) || !ob::is_aligned(m_scales, 4) || !ob::is_aligned(v_scales, 4))
         return OB_ERR_ALIGN;
+    return OB_OK;
+} catch (...) {
+    return OB_ERR_OOM;
+}
+
+ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, float* master, int8_t* m_codes,
+                         float* m_scales, uint8_t* v_codes, float* v_scales, const ob_adamw_hparams* hp,
+                         const ob_control* control, hipStream_t stream)
+try {
+    if (ob_status st = ob_adamw8_check(list, g, p, master, m_codes, m_scales, v_codes, v_scales, hp, control)) return st;
+    if (list->shape.n == 0) return OB_OK;
     const ob::AdamWParams ap = adamw_params(hp, control);
     const ob::State8 state{master, m_codes, m_scales, v_codes, v_scales};
     DeviceGuard guard(list->device);

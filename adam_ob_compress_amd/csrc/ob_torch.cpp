@@ -152,6 +152,30 @@ PyObject* list(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// The norm that a step's call takes first, by a pair (g_mult, max_norm) or None.
+struct Norm {
+    bool on;
+    float g_mult = 1.0f, max_norm = 0.0f;
+    explicit Norm(PyObject* pair) : on(pair != Py_None)
+    {
+        if (!on) return;
+        if (!PyTuple_Check(pair) || PyTuple_GET_SIZE(pair) != 2) throw std::invalid_argument("norm must be (g_mult, max_norm)");
+        g_mult = static_cast<float>(PyFloat_AsDouble(PyTuple_GET_ITEM(pair, 0)));
+        max_norm = static_cast<float>(PyFloat_AsDouble(PyTuple_GET_ITEM(pair, 1)));
+    }
+    // check, then the norm (which counts the step) and the step: what the step refuses is not counted
+    template <class Check, class Step>
+    ob_status with(const List& l, const std::vector<void*>& g, const ob_adamw_hparams* hp, ob_control* ctl, hipStream_t s,
+                   Check&& check, Step&& step) const
+    {
+        if (on) {
+            if (ob_status st = check()) return st;
+            if (ob_status st = ob_grad_norm(l.handle, g.data(), g_mult, max_norm, hp, ctl, s)) return st;
+        }
+        return step();
+    }
+};
+
 // grad_norm(list, grads, g_mult, max_norm, hparams' address or None, control, stream)
 PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
@@ -166,10 +190,10 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
-// adamw_step(list, grads, params, hparams' address, stream, master, m, v, control)
+// adamw_step(list, grads, params, hparams' address, stream, master, m, v, control, norm)
 PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return guarded(n, 9, [&] {
+    return guarded(n, 10, [&] {
         const List& l = list_of(args[0]);
         const std::vector<void*> g = addresses(args[1], nullptr, l, l.g_types, 0);
         const std::vector<void*> p = addresses(args[2], args[1], l, l.p_types, 1);
@@ -177,15 +201,20 @@ PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n)
         hipStream_t s = stream_of(args[4]);
         float* f[3];
         for (int j = 0; j < 3; ++j) f[j] = static_cast<float*>(flat(args[5 + j], at::kFloat, l.state_elems, l.device, 2 + j));
-        const ob_control* ctl = control_of(args[8], l, 5);
-        return status_of([&] { return ob_adamw_step(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl, s); });
+        ob_control* ctl = control_of(args[8], l, 5);
+        const Norm norm(args[9]);
+        return status_of([&] {
+            return norm.with(
+                l, g, hp, ctl, s, [&] { return ob_adamw_check(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl); },
+                [&] { return ob_adamw_step(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl, s); });
+        });
     });
 }
 
-// adamw8_step(list, grads, params, hparams' address, stream, master, m_codes, m_scales, v_codes, v_scales, control)
+// adamw8_step(list, grads, params, hparams' address, stream, master, m_codes, m_scales, v_codes, v_scales, control, norm)
 PyObject* adamw8_step(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return guarded(n, 11, [&] {
+    return guarded(n, 12, [&] {
         const List& l = list_of(args[0]);
         const std::vector<void*> g = addresses(args[1], nullptr, l, l.g_types, 0);
         const std::vector<void*> p = addresses(args[2], args[1], l, l.p_types, 1);
@@ -197,8 +226,13 @@ PyObject* adamw8_step(PyObject*, PyObject* const* args, Py_ssize_t n)
         auto* mq = static_cast<float*>(flat(args[7], at::kFloat, B, l.device, 4));
         auto* vc = static_cast<uint8_t*>(flat(args[8], at::kByte, N, l.device, 5));
         auto* vq = static_cast<float*>(flat(args[9], at::kFloat, B, l.device, 6));
-        const ob_control* ctl = control_of(args[10], l, 7);
-        return status_of([&] { return ob_adamw8_step(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl, s); });
+        ob_control* ctl = control_of(args[10], l, 7);
+        const Norm norm(args[11]);
+        return status_of([&] {
+            return norm.with(
+                l, g, hp, ctl, s, [&] { return ob_adamw8_check(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl); },
+                [&] { return ob_adamw8_step(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl, s); });
+        });
     });
 }
 

@@ -413,6 +413,15 @@ ob_status ob_adamw8_step(ob_tensors list, const void* const* g, void* const* p, 
                          float* m_scales, uint8_t* v_codes, float* v_scales, const ob_adamw_hparams* hp,
                          const ob_control* control, hipStream_t stream);
 
+/* The status with which ob_adamw_step (ob_adamw8_step) would refuse these arguments, or OB_OK; no GPU work.  For
+ * callers that count a step with ob_grad_norm, which does not see the step's own arguments: called before it, a step
+ * that is refused is not counted. */
+ob_status ob_adamw_check(ob_tensors list, const void* const* g, void* const* p, const float* master, const float* m,
+                         const float* v, const ob_adamw_hparams* hp, const ob_control* control);
+ob_status ob_adamw8_check(ob_tensors list, const void* const* g, void* const* p, const float* master,
+                          const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes, const float* v_scales,
+                          const ob_adamw_hparams* hp, const ob_control* control);
+
 /* n fp32 moments into the 8-bit format, to nearest (v >= 0), and back; n >= 0, the last block may be short
  * (ceil(n / 256) scales).  Either moment may be left out: all its pointers NULL.  fp32 pointers 16-byte
  * aligned, codes 4 bytes, scales 4 bytes.  Runs on the current device. */

@@ -171,3 +171,9 @@ def test_reference_step_is_torchs():
                                bc2=ref.bc(0.99, t))
         m, v = ref.r32(m), ref.r32(v)
     assert np.allclose(x, p.detach().numpy(), rtol=0, atol=5 * 1e-2 * 2.0 ** -22)
+
+
+def test_checks_of_a_step_refuse_null_handles():
+    lib, hp = ob.lib(), ob.adamw_hparams()
+    assert lib.ob_adamw_check(None, None, None, None, None, None, ctypes.byref(hp), None) == ob._native.OB_ERR_ARG
+    assert lib.ob_adamw8_check(None, None, None, None, None, None, None, None, ctypes.byref(hp), None) == ob._native.OB_ERR_ARG

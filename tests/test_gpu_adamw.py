@@ -1048,3 +1048,81 @@ def test_words_by_chance_past_a_counter_of_32_bits():
         assert len(bad) == 0, (first, len(bad), bad[:5])
         del m, v
         torch.cuda.empty_cache()
+
+
+def _refused_by_the_step_alone(net, opt):
+    """Calls that a norm would take and the step refuses, each mended after it."""
+    first = next(net.parameters())
+    grads = [torch.ones_like(p) for p in net.parameters()]
+    keep = first.data
+    first.data = keep.half()                      # another type
+    yield grads, (TypeError,)
+    first.data = keep.clone()
+    first.data.untyped_storage().resize_(0)       # released
+    yield grads, (ValueError,)
+    first.data = keep[:0]                         # another size
+    yield grads, (ValueError,)
+    first.data = keep
+    if opt.state_bits == 8:
+        state, opt.m_scales = opt.m_scales, opt.m_scales[:1]
+        yield grads, (ValueError,)
+        opt.m_scales = state
+        opt.hp.eps = 0.0
+        yield grads, (ob.ObError,)
+        opt.hp.eps = 1e-8
+    opt.hp.beta2 = 1.0
+    yield grads, (ob.ObError,)
+    opt.hp.beta2 = 0.999
+
+
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_driver_does_not_count_a_step_that_only_the_step_refuses(bits, max_norm):
+    a, b = _model(torch.float32), _model(torch.float32)
+    first, second = (ob.AdamW(net.parameters(), lr=1e-2, state_bits=bits, max_norm=max_norm) for net in (a, b))
+    for grads, errors in _refused_by_the_step_alone(a, first):
+        before = None if max_norm is None else first.control.clone()
+        with pytest.raises(errors):
+            first.step(grads)
+        assert first.steps() == 0 and (before is None or torch.equal(first.control, before))
+    _train(a, first, 2)
+    _train(b, second, 2)
+    assert first.steps() == second.steps() == 2
+    for p, q in zip(a.parameters(), b.parameters()):
+        assert torch.equal(p, q)
+
+
+def test_driver_does_not_count_a_step_of_parameters_in_each_other():
+    flat = torch.zeros(1000, device=DEV)
+    opt = ob.AdamW([flat[:600], flat[500:]], max_norm=1.0)
+    with pytest.raises(ob.ObError):
+        opt.step([torch.ones(600, device=DEV), torch.ones(500, device=DEV)])
+    assert opt.steps() == 0 and not flat.any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_norm_and_step_in_one_call(bits):
+    """norm=(g_mult, max_norm): the results of the two calls; refused as a whole."""
+    hp = hparams(rounding=1, sr_seed=3)
+    out = []
+    for together in (False, True):
+        L = Lists(SIZES, "bf16", "bf16", seed=9, bits=bits, grad_sigma=0.5)
+        ctl = ob.control_create(DEV)
+        states = dict(m=L.m, v=L.v) if bits == 32 else dict(m_codes=L.mc, m_scales=L.mq, v_codes=L.vc, v_scales=L.vq)
+        call = dict(tensors=L.list, grads=L.grads, params=L.params, hp=hp, control=ctl, **states)
+        step = ob.ob_adamw_step if bits == 32 else ob.ob_adamw8_step
+        for _ in range(3):
+            if together:
+                step(**call, norm=(0.5, 0.1))
+            else:
+                ob.ob_grad_norm(L.list, L.grads, ctl, 0.5, 0.1, hp)
+                step(**call)
+        out.append([x.clone() for x in [*L.params, *states.values(), ctl[:16]]])
+        if together:
+            for bad in (dict(norm=(0.0, 1.0)), dict(norm=(1.0, float("nan"))), dict(params=[L.params[0]] * len(SIZES)),
+                        dict(control=None)):
+                with pytest.raises((ob.ObError, TypeError, ValueError)):
+                    step(**{**call, "norm": (1.0, 1.0), **bad})
+            assert torch.equal(ctl[:16], out[-1][-1])
+    for x, y in zip(*out):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
