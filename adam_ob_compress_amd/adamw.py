@@ -133,14 +133,23 @@ class AdamW:
     _STATES = ("m", "v", "m_codes", "m_scales", "v_codes", "v_scales", "master")
 
     def state_dict(self) -> dict:
-        """Step count and flat states (references); restoring it gives the same steps bit for bit."""
-        return {"step": self.steps(), "state_bits": self.state_bits,
-                **{k: getattr(self, k) for k in self._STATES if getattr(self, k) is not None}}
+        """Step count and flat states (references), with max_norm also the factor of set_lr_scale and the count of steps
+        left out.  Restored into an AdamW made with the same arguments, with the same values in hp, it gives
+        the same steps bit for bit."""
+        d = {"step": self.steps(), "state_bits": self.state_bits,
+             **{k: getattr(self, k) for k in self._STATES if getattr(self, k) is not None}}
+        if self.control is not None:
+            f = nat.control_fields(self.control)
+            d.update(lr_scale=float(f["lr_scale"]), skipped=int(f["skipped"]))
+        return d
 
     def load_state_dict(self, d: dict):
-        """Restore a state_dict of the same list, also one with states of the other width."""
+        """Restore a state_dict of the same list, also one with states of the other width.  What it does not hold of
+        the rate's factor and the steps left out stays as it is."""
         if (self.master is None) != ("master" not in d):
             raise ValueError("the state has a master copy and this optimizer none, or the other way round")
+        if self.control is None and d.get("lr_scale", 1.0) != 1.0:
+            raise ValueError("the state has a factor of the rate (lr_scale), which needs max_norm")
         dev = self.list.device
         for k in self._STATES:
             want = self.list.state_elems // (nat.OB_STATE_BLOCK if k.endswith("_scales") else 1)
@@ -158,7 +167,10 @@ class AdamW:
             self.master.copy_(d["master"])
         self.hp.step = d["step"]
         if self.control is not None:
-            nat.control_fields(self.control)["step"].fill_(d["step"])
+            f = nat.control_fields(self.control)
+            for k in ("step", "lr_scale", "skipped"):
+                if k in d:
+                    f[k].fill_(d[k])
 
 
 def _ratio(value, base, name):

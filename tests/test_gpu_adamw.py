@@ -1126,3 +1126,35 @@ def test_norm_and_step_in_one_call(bits):
             assert torch.equal(ctl[:16], out[-1][-1])
     for x, y in zip(*out):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_driver_resumes_its_schedule(bits):
+    """The factor of the rate and the count of left-out steps are part of the state."""
+    kw = dict(lr=1e-2, state_bits=bits, max_norm=1.0)
+    a = _model(torch.float32)
+    opt = ob.AdamW(a.parameters(), **kw)
+    opt.step([torch.full_like(p, float("nan")) for p in a.parameters()])
+    opt.set_lr_scale(0.3)
+    _train(a, opt, 2)
+    b = _model(torch.float32, seed=1)
+    b.load_state_dict(a.state_dict())
+    again = ob.AdamW(b.parameters(), **kw)
+    again.load_state_dict(opt.state_dict())
+    f = ob.control_fields(again.control)
+    assert float(f["lr_scale"]) == np.float32(0.3) and int(f["skipped"]) == 1 and again.steps() == 2
+    _train(a, opt, 2, seed=8)
+    _train(b, again, 2, seed=8)
+    for p, q in zip(a.parameters(), b.parameters()):
+        assert torch.equal(p, q)
+    # a state without them leaves both; one with a factor needs a control block to hold it
+    older = {k: x for k, x in opt.state_dict().items() if k not in ("lr_scale", "skipped")}
+    again.load_state_dict(older)
+    assert float(f["lr_scale"]) == np.float32(0.3) and int(f["skipped"]) == 1
+    host = ob.AdamW(b.parameters(), lr=1e-2, state_bits=bits)
+    host.load_state_dict(older)
+    with pytest.raises(ValueError, match="max_norm"):
+        host.load_state_dict(opt.state_dict())
+    opt.set_lr_scale(1.0)
+    host.load_state_dict(opt.state_dict())
+    assert host.steps() == 4
