@@ -17,8 +17,8 @@ _ROUNDING = {"nearest": nat.OB_ROUND_NEAREST, "stochastic": nat.OB_ROUND_STOCHAS
 class AdamW:
     """AdamW with decoupled weight decay, states in fp32 or in 8 bits.
 
-    ``params``: tensors (fp32, bf16, fp16; contiguous, on one GPU), or parameter groups as dicts with "params" and
-    optionally "lr" and "weight_decay".  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of
+    ``params``: tensors (fp32, bf16, fp16; contiguous, on one GPU), or parameter groups as dicts with "params" (tensors, or
+    one) and optionally "lr" and "weight_decay".  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of
     16-bit parameters (taken from them here).  ``max_norm``: clip by the global gradient norm and leave out
     steps whose norm is not finite (inf: only the latter); None: neither.  ``rounding="stochastic"`` rounds 8-bit states
     and 16-bit parameters without a master by chance, with bits from (``sr_seed``, the step).
@@ -37,12 +37,14 @@ class AdamW:
                  state_bits=32, master=False, rounding="nearest", sr_seed=0, bias_correction=True, grad_dtype=None):
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        if isinstance(params, torch.Tensor):
+            raise TypeError("params must be a list of tensors or groups, got a tensor")
         groups = list(params)
         if groups and not isinstance(groups[0], dict):
             groups = [{"params": groups}]
         self.params, lr_mults, wd_mults = [], [], []
         for group in groups:
-            for p in group["params"]:
+            for p in [group["params"]] if isinstance(group["params"], torch.Tensor) else group["params"]:
                 self.params.append(p)
                 lr_mults.append(_ratio(group.get("lr", lr), lr, "lr"))
                 wd_mults.append(_ratio(group.get("weight_decay", weight_decay), weight_decay, "weight_decay"))
@@ -56,6 +58,7 @@ class AdamW:
                 raise ValueError(f"all parameters must be on {dev} (got {p.device})")
             if not p.is_contiguous():
                 raise ValueError(f"parameter {j} must be contiguous")
+        self._no_leaves = [(j, p) for j, p in enumerate(self.params) if not p.is_leaf]
         self.state_bits, self.max_norm = state_bits, max_norm
         self.list = nat.ob_tensors_create([p.numel() for p in self.params],
                                           grad_dtype or [p.dtype for p in self.params],
@@ -98,7 +101,13 @@ class AdamW:
     @torch.no_grad()
     def step(self, grads=None, loss_scale: float = 1.0, stream=None):
         """One step; loss_scale: what the gradients were multiplied with (other than 1 needs max_norm)."""
-        grads = [p.grad for p in self.params] if grads is None else list(grads)
+        if grads is None:
+            for j, p in self._no_leaves:
+                if not p.retains_grad and p.grad is None:   # its .grad stays None, as of a parameter to leave alone
+                    raise ValueError(f"parameter {j} is no leaf and has no .grad of its own: give the gradients to step")
+            grads = [p.grad for p in self.params]
+        else:
+            grads = list(grads)
         norm = None
         if self.control is not None:
             norm = (1.0 / loss_scale, self.max_norm)

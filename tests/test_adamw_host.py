@@ -177,3 +177,9 @@ def test_checks_of_a_step_refuse_null_handles():
     lib, hp = ob.lib(), ob.adamw_hparams()
     assert lib.ob_adamw_check(None, None, None, None, None, None, ctypes.byref(hp), None) == ob._native.OB_ERR_ARG
     assert lib.ob_adamw8_check(None, None, None, None, None, None, None, None, ctypes.byref(hp), None) == ob._native.OB_ERR_ARG
+
+
+def test_driver_refuses_a_bare_tensor():
+    """It would be taken row by row."""
+    with pytest.raises(TypeError, match="list"):
+        ob.AdamW(torch.zeros(4, 4))

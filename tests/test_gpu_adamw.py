@@ -1158,3 +1158,37 @@ def test_driver_resumes_its_schedule(bits):
     opt.set_lr_scale(1.0)
     host.load_state_dict(opt.state_dict())
     assert host.steps() == 4
+
+
+def test_driver_takes_a_group_of_one_tensor():
+    """A group's "params" may be a tensor; it is one parameter, not its rows."""
+    a, b = (torch.nn.Parameter(torch.ones(7, 300, device=DEV)) for _ in range(2))
+    for p, params in ((a, [{"params": a}]), (b, [{"params": [b]}])):
+        opt = ob.AdamW(params)
+        assert len(opt.params) == 1 and opt.params[0] is p
+        p.grad = torch.full_like(p, 0.5)
+        opt.step()
+    assert torch.equal(a, b) and not torch.any(a == 1)
+
+
+def test_driver_refuses_to_leave_out_what_is_no_leaf():
+    """Rows of a parameter get no .grad of their own; with gradients given to the step they are stepped."""
+    w = torch.nn.Parameter(torch.ones(2, 300, device=DEV))
+    rows = list(w)
+    opt = ob.AdamW(rows)
+    w.grad = torch.ones_like(w)
+    with pytest.raises(ValueError, match="leaf"):
+        opt.step()
+    assert opt.steps() == 0 and torch.all(w == 1)
+    opt.step([torch.ones(300, device=DEV) for _ in rows])
+    assert opt.steps() == 1 and not torch.any(w == 1)
+    for x in rows:   # set by hand
+        x.grad = torch.ones(300, device=DEV)
+    opt.step()
+    assert opt.steps() == 2
+    kept = (torch.nn.Parameter(torch.ones(300, device=DEV)) * 1)
+    kept.retain_grad()
+    opt = ob.AdamW([kept])
+    kept.sum().backward()
+    opt.step()
+    assert not torch.any(kept == 1)
