@@ -18,10 +18,11 @@ class AdamW:
     """AdamW with decoupled weight decay, states in fp32 or in 8 bits.
 
     ``params``: tensors (fp32, bf16, fp16; contiguous, on one GPU), or parameter groups as dicts with "params" (tensors, or
-    one) and optionally "lr" and "weight_decay".  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of
-    16-bit parameters (taken from them here).  ``max_norm``: clip by the global gradient norm and leave out
-    steps whose norm is not finite (inf: only the latter); None: neither.  ``rounding="stochastic"`` rounds 8-bit states
-    and 16-bit parameters without a master by chance, with bits from (``sr_seed``, the step).
+    one) and optionally "lr" and "weight_decay", which can not be changed later on; no other argument can differ between
+    groups, and a common value of 0 allows no other.  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of 16-bit
+    parameters (taken from them here).  ``max_norm``: clip by the global gradient norm and leave out steps whose norm is
+    not finite (inf, 0 or less: only the latter); None: neither.  ``rounding="stochastic"`` rounds 8-bit states and
+    16-bit parameters without a master by chance, with bits from (``sr_seed``, the step).
 
     ``step()`` takes ``p.grad`` of every parameter (or the list it is given); a parameter without a gradient is
     left alone.  Everything is enqueued on the current stream and nothing waits for the GPU, so a step can be captured
@@ -43,7 +44,12 @@ class AdamW:
         if groups and not isinstance(groups[0], dict):
             groups = [{"params": groups}]
         self.params, lr_mults, wd_mults = [], [], []
+        common = dict(betas=tuple(betas), eps=eps, max_norm=max_norm, state_bits=state_bits, master=master, rounding=rounding,
+                      sr_seed=sr_seed, bias_correction=bias_correction, grad_dtype=grad_dtype, amsgrad=False, maximize=False)
         for group in groups:
+            for k, own in common.items():
+                if k in group and (group[k] if k != "betas" else tuple(group[k])) != own:
+                    raise ValueError(f"a group cannot have its own {k}")
             for p in [group["params"]] if isinstance(group["params"], torch.Tensor) else group["params"]:
                 self.params.append(p)
                 lr_mults.append(_ratio(group.get("lr", lr), lr, "lr"))

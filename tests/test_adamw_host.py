@@ -183,3 +183,16 @@ def test_driver_refuses_a_bare_tensor():
     """It would be taken row by row."""
     with pytest.raises(TypeError, match="list"):
         ob.AdamW(torch.zeros(4, 4))
+
+
+@pytest.mark.parametrize("key", ["betas", "eps", "bias_correction", "max_norm", "state_bits", "master", "rounding", "sr_seed",
+                                 "grad_dtype", "amsgrad", "maximize"])
+def test_driver_refuses_what_a_group_cannot_have(key):
+    """Only the rate and the decay can differ between groups; another setting would be passed over."""
+    with pytest.raises(ValueError, match=key):
+        ob.AdamW([{"params": [torch.zeros(4)]}, {"params": [torch.zeros(4)], key: (7, 8) if key == "betas" else 7}])
+    with pytest.raises(ValueError, match="GPU"):   # a name is none
+        ob.AdamW([{"params": [torch.zeros(4)], "name": "a"}])
+    own = {"amsgrad": False, "maximize": False, "betas": [0.8, 0.99]}
+    with pytest.raises(ValueError, match="GPU"):   # nor is what all have
+        ob.AdamW([{"params": [torch.zeros(4)], **own}], betas=(0.8, 0.99))
