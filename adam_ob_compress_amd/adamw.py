@@ -91,6 +91,18 @@ class AdamW:
         o, p = self.list.state_offset(t), self.params[t]
         return flat[o:o + p.numel()].view(p.shape)
 
+    def _capturing(self, stream):
+        """Whether the stream that a step is enqueued on is being captured."""
+        dev = self.list.device
+        if stream is None:
+            if dev.index == torch.cuda.current_device():
+                return torch.cuda.is_current_stream_capturing()
+            stream = torch.cuda.current_stream(dev)
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), dev)
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
     def set_lr_scale(self, factor: float):
         """Factor of every rate from the next step or replay on (needs max_norm)."""
         nat.control_fields(self.control)["lr_scale"].fill_(factor)
@@ -120,7 +132,7 @@ class AdamW:
         else:
             if loss_scale != 1.0:
                 raise ValueError("a loss scale needs max_norm (inf: no clipping)")
-            if torch.cuda.is_current_stream_capturing():
+            if self._capturing(stream):
                 raise RuntimeError("a captured step needs max_norm (inf: no clipping): its count is kept on the GPU")
             self.hp.step += 1
         try:

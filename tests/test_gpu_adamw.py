@@ -1192,3 +1192,25 @@ def test_driver_refuses_to_leave_out_what_is_no_leaf():
     kept.sum().backward()
     opt.step()
     assert not torch.any(kept == 1)
+
+
+def test_driver_looks_at_its_own_stream_for_a_capture(monkeypatch):
+    """A step counted on the host is refused where the stream that it is given is being captured."""
+    net = _model(torch.float32)
+    opt = ob.AdamW(net.parameters())
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: torch.cuda.current_stream().cuda_stream == s.cuda_stream)
+    grads = [torch.ones_like(p) for p in net.parameters()]
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step(grads, stream=stream)
+    assert opt.steps() == 0
+    for stream in (other, other.cuda_stream, 0):
+        opt.step(grads, stream=stream)
+    with torch.cuda.stream(s):
+        opt.step(grads, stream=other)
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step(grads)
+    assert opt.steps() == 4
+    torch.cuda.synchronize()
