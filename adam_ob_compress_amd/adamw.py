@@ -177,12 +177,19 @@ class AdamW:
             raise ValueError("the state has a master copy and this optimizer none, or the other way round")
         if self.control is None and d.get("lr_scale", 1.0) != 1.0:
             raise ValueError("the state has a factor of the rate (lr_scale), which needs max_norm")
+        if d.get("state_bits") not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {d.get('state_bits')}")
+        if not isinstance(d.get("step"), int):
+            raise ValueError(f"step must be a whole number, got {d.get('step')}")
         dev = self.list.device
+        for k in self._STATES[:2] if d["state_bits"] == 32 else self._STATES[2:6]:
+            if not isinstance(d.get(k), torch.Tensor):
+                raise ValueError(f"the state lacks {k}")
         for k in self._STATES:
             want = self.list.state_elems // (nat.OB_STATE_BLOCK if k.endswith("_scales") else 1)
             if k in d and d[k].numel() != want:
                 raise ValueError(f"{k} must have {want} elements, got {d[k].numel()}")
-        d = {k: x.to(dev) if isinstance(x, torch.Tensor) else x for k, x in d.items()}
+        d = {k: x.to(dev).reshape(-1) if isinstance(x, torch.Tensor) else x for k, x in d.items()}
         if d["state_bits"] == self.state_bits:
             for k in self._STATES[:2] if self.state_bits == 32 else self._STATES[2:6]:
                 getattr(self, k).copy_(d[k])

@@ -1214,3 +1214,26 @@ def test_driver_looks_at_its_own_stream_for_a_capture(monkeypatch):
             opt.step(grads)
     assert opt.steps() == 4
     torch.cuda.synchronize()
+
+
+def test_driver_loads_a_whole_state_or_nothing():
+    net = _model(torch.float32)
+    narrow, wide = (ob.AdamW(net.parameters(), state_bits=bits, max_norm=1.0) for bits in (8, 32))
+    for opt in (narrow, wide):
+        _train(net, opt, 2)
+    for opt, other in ((narrow, wide), (wide, narrow)):
+        for d in (opt.state_dict(), other.state_dict()):
+            d = {k: x.clone() + 1 if isinstance(x, torch.Tensor) else x for k, x in d.items()}
+            d["step"] = 7
+            before = {k: x.clone() if isinstance(x, torch.Tensor) else x for k, x in opt.state_dict().items()}
+            for k in d:
+                if k in ("lr_scale", "skipped"):
+                    continue
+                cut = {j: x for j, x in d.items() if j != k}
+                bad = {**d, k: d[k].double().cpu() if isinstance(d[k], torch.Tensor) else "x"}
+                bad = [cut] if isinstance(d[k], torch.Tensor) and d["state_bits"] == opt.state_bits else [cut, bad]
+                for b in bad:
+                    with pytest.raises((ValueError, TypeError), match=k):
+                        opt.load_state_dict(b)
+                    for j, x in opt.state_dict().items():
+                        assert torch.equal(x, before[j]) if isinstance(x, torch.Tensor) else x == before[j], (k, j)
