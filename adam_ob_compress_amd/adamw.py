@@ -105,6 +105,8 @@ class AdamW:
 
     def set_lr_scale(self, factor: float):
         """Factor of every rate from the next step or replay on (needs max_norm)."""
+        if self.control is None:
+            raise ValueError("a factor of the rate needs max_norm (inf: no clipping); without it change hp.lr")
         nat.control_fields(self.control)["lr_scale"].fill_(factor)
 
     @property

@@ -1237,3 +1237,9 @@ def test_driver_loads_a_whole_state_or_nothing():
                         opt.load_state_dict(b)
                     for j, x in opt.state_dict().items():
                         assert torch.equal(x, before[j]) if isinstance(x, torch.Tensor) else x == before[j], (k, j)
+
+
+def test_driver_has_a_rate_factor_with_max_norm_only():
+    opt = ob.AdamW(_model(torch.float32).parameters())
+    with pytest.raises(ValueError, match="max_norm"):
+        opt.set_lr_scale(0.5)
