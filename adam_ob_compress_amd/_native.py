@@ -576,19 +576,15 @@ def ob_grad_norm(tensors: Tensors, grads, control, g_mult=1.0, max_norm=0.0, hp:
         tensors._fail(code, "ob_grad_norm", (grads,), (("control", control, *_CONTROL),))
 
 
-def _norm_control(norm, control):
-    if norm is not None and control is None:
-        raise TypeError("control must be a torch.Tensor")
-    return norm
-
-
 def ob_adamw_step(tensors: Tensors, grads, params, m, v, hp: ob_adamw_hparams, master=None, control=None, stream=None,
                   norm=None):
     """AdamW step with fp32 states: m, v and the optional master copy flat, of tensors.state_elems.  norm=(g_mult,
     max_norm): ob_grad_norm with these and hp first, once the arguments of both are checked."""
+    if norm is not None and control is None:
+        raise TypeError("control must be a torch.Tensor")
     grads, params = _list(grads), _list(params)
     code = _obtorch().adamw_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master, m, v,
-                                 control, _norm_control(norm, control))
+                                 control, norm)
     if code:
         f32 = (torch.float32, tensors.state_elems)
         tensors._fail(code, "ob_adamw_step", (grads, params),
@@ -599,9 +595,11 @@ def ob_adamw8_step(tensors: Tensors, grads, params, m_codes, m_scales, v_codes, 
                    master=None, control=None, stream=None, norm=None):
     """AdamW step with 8-bit states: int8 / uint8 codes of tensors.state_elems, one fp32 scale per 256.  norm as
     ob_adamw_step."""
+    if norm is not None and control is None:
+        raise TypeError("control must be a torch.Tensor")
     grads, params = _list(grads), _list(params)
     code = _obtorch().adamw8_step(tensors.native, grads, params, _hparams(hp), _list_stream(tensors, stream), master,
-                                  m_codes, m_scales, v_codes, v_scales, control, _norm_control(norm, control))
+                                  m_codes, m_scales, v_codes, v_scales, control, norm)
     if code:
         N = tensors.state_elems
         scales = (torch.float32, N // OB_STATE_BLOCK)

@@ -2,8 +2,8 @@
 arithmetic here).
 
 It stands beside OneBitAdam: OneBitAdam steps one flat fp32 buffer and compresses what workers exchange;
-AdamW steps the tensors of a model where they lie, in their own types.  The dense first steps of a 1-bit
-run can be taken with either.
+AdamW steps the tensors of a model where they lie, in their own types.  Their state layouts differ (one flat
+buffer; each tensor's part from a multiple of 256 elements), and nothing converts one into the other.
 """
 from __future__ import annotations
 
@@ -27,8 +27,8 @@ class AdamW:
     ``step()`` takes ``p.grad`` of every parameter (or the list it is given); a parameter without a gradient is
     left alone.  Everything is enqueued on the current stream and nothing waits for the GPU, so a step can be captured
     into a HIP graph; with ``max_norm`` the step count then lives in ``self.control``, where a replay
-    advances it, and ``set_lr_scale`` changes the rate between replays.  Without ``max_norm`` the count is a host
-    value, which a captured step would repeat: capturing then raises.
+    advances it, and ``set_lr_scale`` changes the rate between replays; the optimizer must outlive the graph.  Without
+    ``max_norm`` the count is a host value, which a captured step would repeat: capturing then raises.
 
     ``self.hp`` holds the step's parameters; what is changed there (``hp.lr``) holds from the next step on.  The groups'
     rates and decays keep their ratios to it.
@@ -69,6 +69,7 @@ class AdamW:
         self.list = nat.ob_tensors_create([p.numel() for p in self.params],
                                           grad_dtype or [p.dtype for p in self.params],
                                           [p.dtype for p in self.params], lr_mults, wd_mults, dev)
+        self._index = self.list.device.index
         self.hp = nat.adamw_hparams(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
                                     bias_correction=bias_correction, step=0, rounding=_ROUNDING[rounding], sr_seed=sr_seed)
         N = self.list.state_elems
@@ -93,13 +94,12 @@ class AdamW:
 
     def _capturing(self, stream):
         """Whether the stream that a step is enqueued on is being captured."""
-        dev = self.list.device
         if stream is None:
-            if dev.index == torch.cuda.current_device():
+            if torch._C._cuda_getDevice() == self._index:   # what current_device() asks
                 return torch.cuda.is_current_stream_capturing()
-            stream = torch.cuda.current_stream(dev)
+            stream = torch.cuda.current_stream(self.list.device)
         elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), dev)
+            stream = torch.cuda.ExternalStream(int(stream), self.list.device)
         with torch.cuda.stream(stream):
             return torch.cuda.is_current_stream_capturing()
 
