@@ -191,7 +191,7 @@ class AdamW:
             want = self.list.state_elems // (nat.OB_STATE_BLOCK if k.endswith("_scales") else 1)
             if k in d and d[k].numel() != want:
                 raise ValueError(f"{k} must have {want} elements, got {d[k].numel()}")
-        d = {k: x.to(dev).reshape(-1) if isinstance(x, torch.Tensor) else x for k, x in d.items()}
+        d = {k: x.to(dev).reshape(-1) if k in self._STATES else x for k, x in d.items()}
         if d["state_bits"] == self.state_bits:
             for k in self._STATES[:2] if self.state_bits == 32 else self._STATES[2:6]:
                 getattr(self, k).copy_(d[k])

@@ -352,7 +352,7 @@ __device__ __forceinline__ void span8(const void* g, void* p, const State8& st, 
 // Bytes: 10 to 16 an element and 16 per 256.  Operations: 49 of the vector ALU an element to nearest, 86
 // by chance (random words 9, codes), 101 with 16-bit parameters rounded by chance too.  Measured (MI355X), 1e9
 // elements: fp32 parameters 2.36 ms and bf16 with a master 2.68 ms, 5.9 to 6.0 TB/s, bf16 1.65 ms, 6.1 TB/s, all by
-// HBM; bf16 by chance 2.44 ms, 4.1 TB/s, by the ALU (41e12 operations a second).
+// HBM; bf16 by chance 2.51 to 2.55 ms, 4.0 TB/s, by the ALU (40e12 operations a second).
 // S state blocks per wave.  A long list takes four: their loads are in flight together (one block per trip:
 // 2.56 ms for fp32 parameters), and the scales' reductions and roots are paid once for four.  (The codes with ordinary
 // loads: 2.47 ms, with ordinary stores 2.59.)  A short list, which

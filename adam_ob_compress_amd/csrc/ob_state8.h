@@ -2,11 +2,11 @@
 // at any alignment.
 //
 // The codes are square-law: an m is c|c| q, a v is (k^2 q)^2, and the borders between codes are fp32 numbers by the
-// format's rule, so the codes are the same wherever they are computed.  What bounds the 8-bit step is the
-// vector ALU (1e9 bf16 parameters: about 60 operations each, at 33e12 a second), so a code is first taken from
-// the hardware's roots, rounded, together with its distance from the next border.  Only where a block has
-// an element closer to a border than the roots' error could reach (a few blocks in a hundred) are its codes
-// settled by comparing with the borders themselves.
+// format's rule, so the codes are the same wherever they are computed.  Taken by comparing with the borders they
+// made the vector ALU the bound of the 8-bit step (1e9 bf16 parameters 1867 us, 1690 now, then by HBM; by chance 3131
+// and 2527, still by the ALU), so a code is first taken from the hardware's roots, rounded, together with its
+// distance from the next border.  Only where a block has an element closer to a border than the roots' error could reach (a
+// few blocks in a hundred), or a scale so small that a root may be lost, are its codes settled by the borders themselves.
 #pragma once
 
 #include "ob_adamw.h"

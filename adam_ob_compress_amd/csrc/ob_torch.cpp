@@ -4,7 +4,8 @@
 //
 // Why compiled: asked from Python, the five properties of a tensor cost 0.3 us, here 0.01 to 0.02.  A step's call with
 // 16 tensors took 17.6 us all in Python, 6.3 to 6.6 with the addresses read here and the call made by ctypes, and takes
-// 4.9 to 5.1 now (time until the call returns); the others went from 5.4 to 5.9 (ctypes) to 4.4 to 4.7.
+// 4.9 to 5.4 now (time until the call returns; every call is a fifth shorter in some processes); the others went from
+// 5.4 to 5.9 (ctypes) to 4.5 to 5.1.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
