@@ -68,6 +68,16 @@ def adamw_hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, 
                             sr_seed)
 
 
+class ob_product(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("a_row", ctypes.c_int64), ("a_col", ctypes.c_int64), ("a_batch", ctypes.c_int64),
+                ("b", ctypes.c_void_p), ("b_row", ctypes.c_int64), ("b_col", ctypes.c_int64), ("b_batch", ctypes.c_int64),
+                ("c", ctypes.c_void_p), ("c_row", ctypes.c_int64), ("c_batch", ctypes.c_int64),
+                ("d", ctypes.c_void_p), ("d_row", ctypes.c_int64), ("d_batch", ctypes.c_int64),
+                ("in_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("symmetric", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -118,6 +128,7 @@ def lib() -> ctypes.CDLL:
         "ob_adamw8_check": (I32, [P, P, P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P]),
         "ob_state8_encode": (I32, [I64, P, P, P, P, P, P, P]),
         "ob_state8_decode": (I32, [I64, P, P, P, P, P, P, P]),
+        "ob_matmul": (I32, [ctypes.POINTER(ob_product), P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -650,3 +661,62 @@ def ob_state8_encode(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
 def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
     """The fp32 moments that 8-bit codes and scales stand for (m or v with its codes and scales: None)."""
     _state8("ob_state8_decode", False, stream, m, v, m_codes, m_scales, v_codes, v_scales)
+
+
+# ---- matrix products ----
+
+def _refuse_product(a, b, out, c):
+    """Raise what the binding saw in a product's tensors."""
+    ts = [("a", a), ("b", b), ("out", out)] + ([] if c is None else [("c", c)])
+    for name, t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    for name, t in ts:
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU (got {t.device}); there is no CPU path")
+        if t.layout is not torch.strided:
+            raise ValueError(f"{name} must be a dense tensor, got {t.layout}")
+        if t.is_neg() or t.is_conj():
+            raise ValueError(f"{name} must not be a negated or conjugated view")
+        if t.dim() != out.dim() or t.dim() not in (2, 3):
+            raise ValueError(f"{name} must have two dimensions, or all three of them three (got {tuple(t.shape)})")
+        if t.device != out.device:
+            raise ValueError(f"{name} must be on {out.device} (got {t.device})")
+    for name, t in ts[:2]:
+        if t.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if b.dtype != a.dtype:
+        raise TypeError(f"b must be {a.dtype}, got {b.dtype}")
+    if out.dtype not in _ERR_DTYPES:
+        raise TypeError(f"out must be float32, bfloat16 or float16, got {out.dtype}")
+    want = (*out.shape[:-2], a.shape[-2], b.shape[-1])
+    if tuple(out.shape) != want or b.shape[-2] != a.shape[-1] or a.shape[:-2] != out.shape[:-2] or b.shape[:-2] != out.shape[:-2]:
+        raise ValueError(f"shapes {tuple(a.shape)}, {tuple(b.shape)} and {tuple(out.shape)} are no product")
+    if c is not None:
+        if c.shape != out.shape:
+            raise ValueError(f"c must have out's shape {tuple(out.shape)}, got {tuple(c.shape)}")
+        if c.dtype != out.dtype:
+            raise TypeError(f"c must be {out.dtype}, got {c.dtype}")
+    for name, t in ts[2:]:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must lie by rows (strides {t.stride()})")
+    for name, t in ts:
+        if t.untyped_storage().nbytes() < (t.storage_offset() + 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size():
+            raise ValueError(f"{name} must have its memory (its storage was released or shrunk)")
+    raise ValueError("the tensors are refused")
+
+
+def ob_matmul(a, b, out, alpha=1.0, beta=0.0, c=None, symmetric=False, stream=None):
+    """out = alpha * a @ b + beta * c for matrices or batches of them: a, b bfloat16 or float16, either by rows or transposed
+    views; out and c (which may be out) float32, bfloat16 or float16, by rows.  symmetric: the caller knows that a @ b and
+    c are; what is below the diagonal is computed and written above it too."""
+    if stream is None:
+        index = out.get_device() if isinstance(out, torch.Tensor) else -1
+        s = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    code = _obtorch().matmul(a, b, out, c, alpha, beta, symmetric, s)
+    if code > 0:
+        raise ObError(code, "ob_matmul")
+    if code < 0:
+        _refuse_product(a, b, out, c)

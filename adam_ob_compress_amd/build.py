@@ -23,6 +23,9 @@ UNITS = [
     ("ob_adamw.hip", ["-DOB_AW_G=2"]),         # fp16
     ("ob_state8.hip", []),
     ("ob_adamw_api.cpp", []),
+    ("ob_matmul.hip", ["-DOB_MM_BF16=0"]),     # products, by operand type: fp16
+    ("ob_matmul.hip", ["-DOB_MM_BF16=1"]),     # bf16
+    ("ob_matmul_api.cpp", []),
 ]
 BUILD_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -2,6 +2,7 @@
 // ob_adam.h): checks of arguments, the list's work-block tables, and the launches.
 #include "ob_adam.h"
 #include "ob_adamw.h"
+#include "ob_list_handle.h"
 
 #include <algorithm>
 #include <cstddef>
@@ -12,26 +13,9 @@ static_assert(sizeof(ob_control) == 64 && offsetof(ob_control, bc1) == 24 && off
 
 namespace {
 
-struct Table {
-    std::vector<int64_t> first;      // [T + 1]: items of the tensor in place k are [first[k], first[k+1])
-    const ob::ListItem* d_items = nullptr;
-};
-
-}  // namespace
-
-struct ob_tensors_s {
-    int device = 0;
-    ob::ListShape shape;
-    Table step, norm;
-    const ob::ListTensor* d_tensors = nullptr;  // by place
-    void* d_tables = nullptr;                   // one allocation: the items of both tables, the tensors
-};
-
-namespace {
-
-// Elements per item of the steps and of the norm.
-constexpr int64_t kStepElems = ob::kStepTiles * ob::kListTile;
-constexpr int64_t kNormElems = 16 * ob::kListTile;
+using ob::DeviceGuard;
+using ob::kNormElems;
+using ob::kStepElems;
 // Gradient bytes at a call's end that the norm reads with ordinary loads, which leave them in the last-level
 // cache for the step that follows; what comes before is read nontemporally, which is faster.  Norm and step
 // of 1.09e8 elements: bf16 278 us with ordinary loads and 293 nontemporal, fp32 (436 MB) 554 and 592; norm alone
@@ -51,25 +35,6 @@ T* at(T* p, int64_t i)
 {
     return p ? p + i : nullptr;
 }
-
-// The list's device is current for the duration of a call.
-struct DeviceGuard {
-    int back = -1;   // the device to return to; -1: none was left
-    bool ok;
-    explicit DeviceGuard(int dev)
-    {
-        int cur = -1;
-        ok = hipGetDevice(&cur) == hipSuccess;
-        if (ok && cur != dev) {
-            ok = hipSetDevice(dev) == hipSuccess;
-            back = cur;
-        }
-    }
-    ~DeviceGuard()
-    {
-        if (back >= 0) (void)hipSetDevice(back);
-    }
-};
 
 void free_list(ob_tensors l)
 {

@@ -1,0 +1,146 @@
+// ob_matmul.hip -- matrix products with a residual; compiled once per operand type (OB_MM_BF16: 0 fp16, 1 bf16).
+#include "ob_any.h"
+#include "ob_matmul.h"
+#include "ob_mfma.h"
+
+#ifndef OB_MM_BF16
+#error "OB_MM_BF16 selects the operands' type"
+#endif
+
+namespace ob {
+namespace {
+
+// Row and column of a matrix's tile `t`.  All: panels of eight rows of tiles, column after column, so that the
+// work groups that run together share rows and columns in their XCD's L2.  Symmetric: row after row below the diagonal.
+__device__ __forceinline__ void tile_at(const ProductArgs& p, int64_t t, int& i, int& j)
+{
+    if (p.symmetric) {
+        i = static_cast<int>((sqrt(8.0 * static_cast<double>(t) + 1.0) - 1.0) * 0.5);
+        while (static_cast<int64_t>(i) * (i + 1) / 2 > t) --i;
+        while (static_cast<int64_t>(i + 1) * (i + 2) / 2 <= t) ++i;
+        j = static_cast<int>(t - static_cast<int64_t>(i) * (i + 1) / 2);
+        return;
+    }
+    const int64_t panel = static_cast<int64_t>(8) * p.tiles_n, q = t / panel;
+    const int rows = min(8, p.tiles_m - static_cast<int>(q) * 8), r = static_cast<int>(t - q * panel);
+    i = static_cast<int>(q) * 8 + r % rows;
+    j = r / rows;
+}
+
+// Work groups go around the eight XCDs; give each XCD a range of consecutive tiles.
+__device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n)
+{
+    const int64_t each = n / 8, more = n % 8, x = b % 8;
+    return x * each + (x < more ? x : more) + b / 8;
+}
+
+template <int D>
+__device__ __forceinline__ f4 load_row4(const void* p, int64_t i, int left)
+{
+    if (left >= 4) {
+        if constexpr (D == 0) return *reinterpret_cast<const f4e*>(static_cast<const float*>(p) + i);
+        const u2e u = *reinterpret_cast<const u2e*>(static_cast<const uint16_t*>(p) + i);
+        return f4{widen16<D>(u.x & 0xffffu), widen16<D>(u.x >> 16), widen16<D>(u.y & 0xffffu), widen16<D>(u.y >> 16)};
+    }
+    f4 r{};
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < left) r[e] = load_any1<D>(p, i + e);
+    return r;
+}
+
+template <int D>
+__device__ __forceinline__ void store_row4(void* p, int64_t i, f4 x, int left)
+{
+    if (left >= 4) {
+        if constexpr (D == 0) {
+            *reinterpret_cast<f4e*>(static_cast<float*>(p) + i) = x;
+        } else {
+            u2e u;
+            u.x = round16x2<D, false>(x.x, x.y, 0, 0);
+            u.y = round16x2<D, false>(x.z, x.w, 0, 0);
+            *reinterpret_cast<u2e*>(static_cast<uint16_t*>(p) + i) = u;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < left) store_any1<D, false>(p, i + e, x[e], 0);
+}
+
+template <int D, class P>
+__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, int64_t batch, int m0, int n0, bool mirror)
+{
+    constexpr int64_t kBytes = D == 0 ? 4 : 2;
+    const char* c = static_cast<const char*>(p.c) + batch * p.batch_c * kBytes;
+    char* d = static_cast<char*>(p.d) + batch * p.batch_d * kBytes;
+    tile.each([&](int r, int col, f4v sum) {
+        const int i = m0 + r, j = n0 + col, left = p.n - j;
+        if (i >= p.m || left <= 0) return;
+        f4 x;
+        if (p.beta != 0.0f) {
+            const f4 y = load_row4<D>(c, i * p.ldc + j, left);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
+        }
+        store_row4<D>(d, i * p.ldd + j, x, left);
+        if (mirror) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left) store_any1<D, false>(d, (j + e) * p.ldd + i, x[e], 0);
+        }
+    });
+}
+
+template <int TM, int WM, int WN, bool AK, bool BK, bool CHUNKS>
+__global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_product(ProductArgs p)
+{
+    using P = TileProduct<TM, TM, WM, WN, OB_MM_BF16 != 0, AK, BK, CHUNKS>;
+    __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+    const int64_t t = p.first + by_xcd(blockIdx.x, gridDim.x), batch = t / p.tiles;
+    int ti, tj;
+    tile_at(p, t - batch * p.tiles, ti, tj);
+    const int m0 = ti * TM, n0 = tj * TM;
+    P tile;
+    tile.run(Operand{p.a + batch * p.batch_a + (AK ? m0 * p.lda : m0), p.lda, p.m - m0, p.k},
+             Operand{p.b + batch * p.batch_b + (BK ? n0 * p.ldb : n0), p.ldb, p.n - n0, p.k}, lds);
+    const bool mirror = p.symmetric && ti != tj;
+    if (p.out_type == OB_F32)
+        finish<0>(p, tile, batch, m0, n0, mirror);
+    else if (p.out_type == OB_BF16)
+        finish<1>(p, tile, batch, m0, n0, mirror);
+    else
+        finish<2>(p, tile, batch, m0, n0, mirror);
+}
+
+template <int TM, int WM, int WN, bool CHUNKS>
+hipError_t launch(const ProductArgs& p, bool ak, bool bk, int64_t count, hipStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(count)), block(64 * (TM / WM) * (TM / WN));
+    if (ak && bk)
+        hipLaunchKernelGGL((k_product<TM, WM, WN, true, true, CHUNKS>), grid, block, 0, s, p);
+    else if (ak)
+        hipLaunchKernelGGL((k_product<TM, WM, WN, true, false, CHUNKS>), grid, block, 0, s, p);
+    else if (bk)
+        hipLaunchKernelGGL((k_product<TM, WM, WN, false, true, CHUNKS>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((k_product<TM, WM, WN, false, false, CHUNKS>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <bool BF16>
+hipError_t launch_product(const ProductArgs& p, int tile, bool ak, bool bk, bool chunks, int64_t count, hipStream_t s)
+{
+    if (tile == TILE_256) return chunks ? launch<256, 128, 64, true>(p, ak, bk, count, s) : hipErrorInvalidValue;
+    if (tile == TILE_128) return chunks ? launch<128, 64, 64, true>(p, ak, bk, count, s) : launch<128, 64, 64, false>(p, ak, bk, count, s);
+    return chunks ? launch<64, 32, 32, true>(p, ak, bk, count, s) : launch<64, 32, 32, false>(p, ak, bk, count, s);
+}
+
+template hipError_t launch_product<OB_MM_BF16 != 0>(const ProductArgs&, int, bool, bool, bool, int64_t, hipStream_t);
+
+}  // namespace ob

@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <memory>
@@ -257,6 +258,96 @@ PyObject* state8(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// A matrix or a batch of them: a dense GPU tensor of two or three dimensions with its memory; throws Bad otherwise.
+const at::Tensor& matrix(PyObject* item, int64_t where)
+{
+    if (!THPVariable_Check(item)) throw Bad{where, 0};
+    const at::Tensor& t = THPVariable_Unpack(item);
+    if (t.layout() != at::kStrided || !t.is_cuda() || t.is_neg() || t.is_conj() || (t.dim() != 2 && t.dim() != 3) || !t.has_storage())
+        throw Bad{where, 0};
+    return t;
+}
+
+void* matrix_address(const at::Tensor& t, int64_t where)
+{
+    if (t.numel() == 0) return nullptr;
+    int64_t last = t.storage_offset();
+    for (int64_t d = 0; d < t.dim(); ++d) last += (t.size(d) - 1) * t.stride(d);
+    void* p = nullptr;
+    try {
+        if (t.storage().nbytes() / t.itemsize() > static_cast<size_t>(last)) p = t.data_ptr();
+    } catch (...) {
+    }
+    if (!p) throw Bad{where, 0};
+    return p;
+}
+
+int32_t type_of(const at::Tensor& t, int64_t where)
+{
+    switch (t.scalar_type()) {
+    case at::kFloat: return OB_F32;
+    case at::kBFloat16: return OB_BF16;
+    case at::kHalf: return OB_F16;
+    default: throw Bad{where, 0};
+    }
+}
+
+// matmul(a, b, out, c or None, alpha, beta, symmetric, stream): a product on the tensors' device
+PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        const at::Tensor &a = matrix(args[0], 0), &b = matrix(args[1], 1), &d = matrix(args[2], 2);
+        const at::Tensor* c = args[3] == Py_None ? nullptr : &matrix(args[3], 3);
+        const int64_t dim = d.dim(), x = dim - 2, y = dim - 1;
+        ob_product p{};
+        p.batch = dim == 3 ? d.size(0) : 1;
+        p.m = d.size(x);
+        p.n = d.size(y);
+        p.k = a.dim() == dim ? a.size(y) : -1;
+        auto fits = [&](const at::Tensor& t, int64_t rows, int64_t cols, int64_t where) {
+            if (t.dim() != dim || t.size(x) != rows || t.size(y) != cols || (dim == 3 && t.size(0) != p.batch) ||
+                t.get_device() != d.get_device())
+                throw Bad{where, 0};
+        };
+        fits(a, p.m, p.k, 0);
+        fits(b, p.k, p.n, 1);
+        p.a = matrix_address(a, 0);
+        p.a_row = a.stride(x);
+        p.a_col = a.stride(y);
+        p.a_batch = dim == 3 ? a.stride(0) : 0;
+        p.b = matrix_address(b, 1);
+        p.b_row = b.stride(x);
+        p.b_col = b.stride(y);
+        p.b_batch = dim == 3 ? b.stride(0) : 0;
+        // an extent of one has a stride of no meaning
+        if (p.m <= 1 && p.a_col != 1) p.a_row = 1;
+        if (p.k <= 1 && p.a_row != 1) p.a_col = 1;
+        if (p.k <= 1 && p.b_col != 1) p.b_row = 1;
+        if (p.n <= 1 && p.b_row != 1) p.b_col = 1;
+        if (p.n > 1 && d.stride(y) != 1) throw Bad{2, 0};
+        p.d = matrix_address(d, 2);
+        p.d_row = d.stride(x);
+        p.d_batch = dim == 3 ? d.stride(0) : 0;
+        p.in_type = type_of(a, 0);
+        if (type_of(b, 1) != p.in_type) throw Bad{1, 0};
+        p.out_type = type_of(d, 2);
+        if (c) {
+            fits(*c, p.m, p.n, 3);
+            if (type_of(*c, 3) != p.out_type || (p.n > 1 && c->stride(y) != 1)) throw Bad{3, 0};
+            p.c = matrix_address(*c, 3);
+            p.c_row = c->stride(x);
+            p.c_batch = dim == 3 ? c->stride(0) : 0;
+        }
+        p.alpha = static_cast<float>(PyFloat_AsDouble(args[4]));
+        p.beta = static_cast<float>(PyFloat_AsDouble(args[5]));
+        p.symmetric = PyObject_IsTrue(args[6]) == 1;
+        hipStream_t s = stream_of(args[7]);
+        if (PyErr_Occurred()) throw Bad{0, 0};
+        const c10::DeviceGuard guard(d.device());
+        return status_of([&] { return ob_matmul(&p, s); });
+    });
+}
+
 // scalar_type(dtype): its code in the type strings of list()
 PyObject* scalar_type(PyObject*, PyObject* dtype)
 {
@@ -278,6 +369,7 @@ PyMethodDef methods[] = {fast<list>("list"),
                          fast<adamw_step>("adamw_step"),
                          fast<adamw8_step>("adamw8_step"),
                          fast<state8>("state8"),
+                         fast<matmul>("matmul"),
                          {"scalar_type", scalar_type, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

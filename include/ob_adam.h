@@ -430,6 +430,43 @@ ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_
 ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,
                            const float* v_scales, float* m, float* v, hipStream_t stream);
 
+/* ---- matrix products ----
+ * D = alpha * A B + beta * C over a batch, 16-bit operands, sums in fp32: statistics of gradients (L = b L + a G G^T),
+ * projections of gradients, and what the Muon step below is made of.
+ *
+ * A is m x k, B k x n, C and D m x n; element (i, j) of a matrix is at i*row + j*col (elements), and a batch's next
+ * matrix at + batch.  Of A's (B's) two strides one is 1 and the other arbitrary (>= 0), so that an operand
+ * may be a transposed view; C and D lie by rows, col = 1.  Stride 0 repeats an operand's row, column or matrix.
+ * Every pointer needs the alignment of its element only; operands whose pointers are 16-byte aligned, whose row (or
+ * column) and batch strides are multiples of 8 and whose extent along the unit stride is one are read faster.
+ *   in_type   of A and B: OB_BF16 or OB_F16
+ *   out_type  of C and D: OB_F32, OB_BF16 or OB_F16; every element is fma(alpha, sum, fl(beta * C)) in fp32, rounded once
+ *   beta = 0  C is not read and may be NULL
+ *   k = 0     the sums are 0
+ *   symmetric 1: m = n, and the caller knows that A B is symmetric (B = A^T, or powers of one symmetric matrix) and
+ *             C is: what is below the diagonal is computed, and written above it too.
+ * D may be C itself (same pointer and strides) and overlaps nothing else.  Zero extents give no work.
+ * Extents are at most 2^31 - 1 - 256, offsets within a matrix and a batch below 2^60 elements; OB_ERR_ARG beyond.
+ * Sums run in an order that depends on the extents, layouts and alignment alone.  Runs on the current device; allocates
+ * nothing, synchronises nothing and records kernels only. */
+typedef struct {
+    int64_t batch, m, n, k;
+    const void* a;
+    int64_t a_row, a_col, a_batch;
+    const void* b;
+    int64_t b_row, b_col, b_batch;
+    const void* c;
+    int64_t c_row, c_batch;
+    void* d;
+    int64_t d_row, d_batch;
+    int32_t in_type, out_type;
+    float alpha, beta;       /* finite */
+    int32_t symmetric;       /* 0 or 1 */
+    int32_t reserved;        /* 0 */
+} ob_product;
+
+ob_status ob_matmul(const ob_product* product, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
