@@ -18,7 +18,11 @@ from ._native import (  # noqa: F401
     ob_plan_set_timing,
     ob_server_reduce, ob_status_str, ob_unpack,
     OB_CONTROL_BYTES, OB_STATE_BLOCK, Tensors, adamw_hparams, control_create, control_fields, ob_adamw8_step,
-    ob_adamw_hparams, ob_adamw_step, ob_grad_norm, ob_matmul, ob_product, ob_state8_decode, ob_state8_encode, ob_tensors_create,
+    ob_adamw_hparams, ob_adamw_step, ob_grad_norm, ob_matmul, ob_product,
+    MuonPlan, OB_MUON_MATCH_RMS, OB_MUON_PLAIN, OB_MUON_SHAPE, OB_NORM_2, OB_NORM_MAX, muon_hparams, ob_clip_grads,
+    ob_muon_create, ob_muon_hparams, ob_muon_step, ob_tensor_norms, ob_tensor_norms_workspace,
+    ob_state8_decode, ob_state8_encode, ob_tensors_create,
 )
 from .adamw import AdamW  # noqa: F401
+from .muon import GradClip, Muon  # noqa: F401
 from .schedule import OneBitAdam, OneBitLamb, step_kind  # noqa: F401

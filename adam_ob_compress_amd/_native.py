@@ -8,6 +8,7 @@ fallback: if the library is not built, or a tensor is not on the GPU, a call rai
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -20,6 +21,8 @@ OB_NOALLOC_SCRATCH_BYTES = 64 << 20
 OB_F32, OB_BF16, OB_F16 = 0, 1, 2
 OB_EF_PLAIN, OB_EF_EMA = 0, 1
 OB_ROUND_NEAREST, OB_ROUND_STOCHASTIC = 0, 1
+OB_NORM_2, OB_NORM_MAX = 0, 1
+OB_MUON_PLAIN, OB_MUON_SHAPE, OB_MUON_MATCH_RMS = 0, 1, 2
 OB_STATE_BLOCK = 256
 OB_CONTROL_PARTIALS = 2048
 OB_CONTROL_BYTES = 64 + 8 * OB_CONTROL_PARTIALS
@@ -66,6 +69,17 @@ def adamw_hparams(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, 
                   rounding=OB_ROUND_NEAREST, sr_seed=0) -> ob_adamw_hparams:
     return ob_adamw_hparams(lr, beta1, beta2, eps, weight_decay, 1 if bias_correction else 0, step, rounding, 0,
                             sr_seed)
+
+
+class ob_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float), ("eps", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("iterations", ctypes.c_int32), ("scale", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def muon_hparams(lr=1e-3, momentum=0.95, weight_decay=0.1, eps=1e-7, nesterov=True, iterations=5,
+                 scale=OB_MUON_MATCH_RMS) -> ob_muon_hparams:
+    return ob_muon_hparams(lr, momentum, weight_decay, eps, 1 if nesterov else 0, iterations, scale, 0)
 
 
 class ob_product(ctypes.Structure):
@@ -128,6 +142,14 @@ def lib() -> ctypes.CDLL:
         "ob_adamw8_check": (I32, [P, P, P, P, P, P, P, P, ctypes.POINTER(ob_adamw_hparams), P]),
         "ob_state8_encode": (I32, [I64, P, P, P, P, P, P, P]),
         "ob_state8_decode": (I32, [I64, P, P, P, P, P, P, P]),
+        "ob_tensor_norms_workspace": (I64, [P]),
+        "ob_tensor_norms": (I32, [P, P, ctypes.c_float, I32, P, P, P]),
+        "ob_clip_grads": (I32, [P, P, P, P, ctypes.c_float, ctypes.c_float, I32, P]),
+        "ob_muon_create": (I32, [P, P, P, ctypes.POINTER(P)]),
+        "ob_muon_destroy": (I32, [P]),
+        "ob_muon_workspace": (I64, [P]),
+        "ob_muon_step": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_muon_hparams), P, P]),
+        "ob_muon_check": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_muon_hparams), P]),
         "ob_matmul": (I32, [ctypes.POINTER(ob_product), P]),
     }
     for name, (res, args) in sig.items():
@@ -438,6 +460,7 @@ class Tensors:
         self.p_dtypes = tuple(p_dtypes)
         self.device = device
         self.state_elems = int(lib().ob_tensors_state_elems(handle))
+        self.norm_bytes = int(lib().ob_tensor_norms_workspace(handle))
         module = _obtorch()
         self.native = module.list(handle.value, self.sizes, bytes(module.scalar_type(d) for d in self.g_dtypes),
                                   bytes(module.scalar_type(d) for d in self.p_dtypes), device.index, self.state_elems)
@@ -464,7 +487,7 @@ class Tensors:
         except Exception:
             pass
 
-    def _fail(self, code, what, lists, flats):
+    def _fail(self, code, what, lists, flats, names=("grads", "params")):
         """Raise what a call's code says: a status of the library, or the place of the first argument that is
         not as it should be (lists: gradients, parameters; flats: (name, tensor, type, elements))."""
         if code > 0:
@@ -473,7 +496,7 @@ class Tensors:
         if where >= 2:
             name, t, dtype, numel = flats[where - 2]
         else:
-            name, ts = ("grads", "params")[where], lists[where]
+            name, ts = names[where], lists[where]
             if len(ts) != len(self.sizes):
                 raise ValueError(f"{name} must have {len(self.sizes)} tensors, got {len(ts)}")
             if ts[j] is None:
@@ -661,6 +684,112 @@ def ob_state8_encode(m, v, m_codes, m_scales, v_codes, v_scales, stream=None):
 def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
     """The fp32 moments that 8-bit codes and scales stand for (m or v with its codes and scales: None)."""
     _state8("ob_state8_decode", False, stream, m, v, m_codes, m_scales, v_codes, v_scales)
+
+
+# ---- norms of many tensors, and clipped gradients ----
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace, or a new one that is kept until the call's work is done."""
+    if workspace is not None:
+        return workspace
+    w = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        w.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device))
+    return w
+
+
+def _fail_workspace(tensors, workspace, nbytes, code, place):
+    """Raise where a call's code names its workspace."""
+    if code < 0 and (-code - 1) >> 32 == place:
+        if isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.numel() < nbytes:
+            raise ValueError(f"workspace must have at least {nbytes} bytes, got {workspace.numel()}")
+        tensors._refuse(workspace, "workspace", torch.uint8, workspace.numel() if isinstance(workspace, torch.Tensor) else 0)
+
+
+def ob_tensor_norms_workspace(tensors: Tensors) -> int:
+    """Bytes of the workspace of ob_tensor_norms."""
+    return int(lib().ob_tensor_norms_workspace(tensors.handle))
+
+
+def ob_tensor_norms(tensors: Tensors, grads, norms, g_mult=1.0, kind=OB_NORM_2, workspace=None, stream=None):
+    """Norm of every gradient (a list; None: 0) times |g_mult|, and behind them the norm of all, into norms (fp32, one more than
+    tensors).  kind: OB_NORM_2 or OB_NORM_MAX.  workspace: a byte tensor of ob_tensor_norms_workspace, or None for a new one."""
+    grads = _list(grads)
+    need = tensors.norm_bytes
+    workspace = _workspace(workspace, need, tensors.device, stream)
+    code = _obtorch().tensor_norms(tensors.native, grads, norms, workspace, need, g_mult, kind, _list_stream(tensors, stream))
+    if code:
+        _fail_workspace(tensors, workspace, need, code, 3)
+        tensors._fail(code, "ob_tensor_norms", (grads,), (("norms", norms, torch.float32, len(tensors) + 1),))
+
+
+def ob_clip_grads(tensors: Tensors, grads, norms, max_norm, g_mult=1.0, out=None, per_tensor=False, stream=None):
+    """The gradients times g_mult min(1, max_norm / (norm + 1e-6)) (max_norm <= 0 or infinite: times g_mult), by the norm of
+    all or, per_tensor, each by its own; a norm that is not finite makes them NaN.  out: tensors of the list's parameter
+    types; None: in place."""
+    grads, out = _list(grads), None if out is None else _list(out)
+    code = _obtorch().clip_grads(tensors.native, grads, out, norms, max_norm, g_mult, per_tensor, _list_stream(tensors, stream))
+    if code:
+        tensors._fail(code, "ob_clip_grads", (grads, out), (("norms", norms, torch.float32, len(tensors) + 1),), ("grads", "out"))
+
+
+# ---- Muon over lists of matrices ----
+
+class MuonPlan:
+    """Owner of an ob_muon handle (destroyed with the object): the matrices of a list's tensors."""
+
+    def __init__(self, handle: ctypes.c_void_p, tensors: Tensors):
+        self.handle, self.tensors = handle, tensors
+        self.workspace_bytes = int(lib().ob_muon_workspace(handle))
+
+    def destroy(self):
+        if self.handle:
+            _check(lib().ob_muon_destroy(self.handle), "ob_muon_destroy")
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def ob_muon_create(tensors: Tensors, shapes) -> MuonPlan:
+    """Plan for a list whose tensors have these shapes: (rows, columns), or more dimensions in front for matrices behind each
+    other."""
+    shapes = [tuple(int(n) for n in s) for s in shapes]
+    if len(shapes) != len(tensors):
+        raise ValueError(f"shapes must have {len(tensors)} entries, got {len(shapes)}")
+    for j, (s, n) in enumerate(zip(shapes, tensors.sizes)):
+        if len(s) < 2:
+            raise ValueError(f"tensor {j} is no matrix: shape {s}")
+        if math.prod(s) != n:
+            raise ValueError(f"tensor {j} has {n} elements, its shape {s} has {math.prod(s)}")
+    rows, cols = ((ctypes.c_int64 * len(shapes))(*[max(s[d], 1) if math.prod(s) == 0 else s[d] for s in shapes]) for d in (-2, -1))
+    h = ctypes.c_void_p()
+    _check(lib().ob_muon_create(tensors.handle, rows, cols, ctypes.byref(h)), "ob_muon_create")
+    return MuonPlan(h, tensors)
+
+
+def ob_muon_step(plan: MuonPlan, grads, params, m, hp: ob_muon_hparams, workspace, master=None, control=None, stream=None,
+                 norm=None):
+    """Muon step: m and the optional master copy flat, of the list's state_elems; workspace: a byte tensor of
+    plan.workspace_bytes.  norm=(g_mult, max_norm): ob_grad_norm with these first, once the arguments of both are checked; it
+    counts the step in control."""
+    if norm is not None and control is None:
+        raise TypeError("control must be a torch.Tensor")
+    if type(hp) is not ob_muon_hparams:
+        raise TypeError(f"hp must be made by muon_hparams, got {type(hp)}")
+    if not plan.handle:
+        raise ValueError("the plan is destroyed")
+    grads, params, tensors = _list(grads), _list(params), plan.tensors
+    code = _obtorch().muon_step(tensors.native, plan.handle.value, grads, params, ctypes.addressof(hp), _list_stream(tensors, stream),
+                                master, m, workspace, plan.workspace_bytes, control, norm)
+    if code:
+        _fail_workspace(tensors, workspace, plan.workspace_bytes, code, 4)
+        f32 = (torch.float32, tensors.state_elems)
+        tensors._fail(code, "ob_muon_step", (grads, params),
+                      (("master", master, *f32), ("m", m, *f32), None, ("control", control, *_CONTROL)))
 
 
 # ---- matrix products ----

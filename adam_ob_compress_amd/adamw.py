@@ -14,38 +14,18 @@ from . import _native as nat
 _ROUNDING = {"nearest": nat.OB_ROUND_NEAREST, "stochastic": nat.OB_ROUND_STOCHASTIC}
 
 
-class AdamW:
-    """AdamW with decoupled weight decay, states in fp32 or in 8 bits.
+class ListOptimizer:
+    """What the optimizers over a model's tensors share: their parameters, the list that describes them, the control block and
+    a master copy."""
 
-    ``params``: tensors (fp32, bf16, fp16; contiguous, on one GPU), or parameter groups as dicts with "params" (tensors, or
-    one) and optionally "lr" and "weight_decay", which can not be changed later on; no other argument can differ between
-    groups, and a common value of 0 allows no other.  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of 16-bit
-    parameters (taken from them here).  ``max_norm``: clip by the global gradient norm and leave out steps whose norm is
-    not finite (inf, 0 or less: only the latter); None: neither.  ``rounding="stochastic"`` rounds 8-bit states and
-    16-bit parameters without a master by chance, with bits from (``sr_seed``, the step).
-
-    ``step()`` takes ``p.grad`` of every parameter (or the list it is given); a parameter without a gradient is
-    left alone.  Everything is enqueued on the current stream and nothing waits for the GPU, so a step can be captured
-    into a HIP graph; with ``max_norm`` the step count then lives in ``self.control``, where a replay
-    advances it, and ``set_lr_scale`` changes the rate between replays; the optimizer must outlive the graph.  Without
-    ``max_norm`` the count is a host value, which a captured step would repeat: capturing then raises.
-
-    ``self.hp`` holds the step's parameters; what is changed there (``hp.lr``) holds from the next step on.  The groups'
-    rates and decays keep their ratios to it.
-    """
-
-    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None,
-                 state_bits=32, master=False, rounding="nearest", sr_seed=0, bias_correction=True, grad_dtype=None):
-        if state_bits not in (8, 32):
-            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+    def _collect(self, params, lr, weight_decay, common):
+        """Parameters and their factors of rate and decay from tensors or groups; common: what no group may have of its own."""
         if isinstance(params, torch.Tensor):
             raise TypeError("params must be a list of tensors or groups, got a tensor")
         groups = list(params)
         if groups and not isinstance(groups[0], dict):
             groups = [{"params": groups}]
         self.params, lr_mults, wd_mults = [], [], []
-        common = dict(betas=tuple(betas), eps=eps, max_norm=max_norm, state_bits=state_bits, master=master, rounding=rounding,
-                      sr_seed=sr_seed, bias_correction=bias_correction, grad_dtype=grad_dtype, amsgrad=False, maximize=False)
         for group in groups:
             for k, own in common.items():
                 if k in group and (group[k] if k != "betas" else tuple(group[k])) != own:
@@ -65,27 +45,33 @@ class AdamW:
             if not p.is_contiguous():
                 raise ValueError(f"parameter {j} must be contiguous")
         self._no_leaves = [(j, p) for j, p in enumerate(self.params) if not p.is_leaf]
-        self.state_bits, self.max_norm = state_bits, max_norm
+        return lr_mults, wd_mults
+
+    def _begin(self, lr_mults, wd_mults, grad_dtype, master, max_norm):
+        """The list, the master copy and the control block."""
+        dev = self.params[0].device
+        self.max_norm = max_norm
         self.list = nat.ob_tensors_create([p.numel() for p in self.params],
                                           grad_dtype or [p.dtype for p in self.params],
                                           [p.dtype for p in self.params], lr_mults, wd_mults, dev)
         self._index = self.list.device.index
-        self.hp = nat.adamw_hparams(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
-                                    bias_correction=bias_correction, step=0, rounding=_ROUNDING[rounding], sr_seed=sr_seed)
-        N = self.list.state_elems
-        self.m = self.v = self.m_codes = self.m_scales = self.v_codes = self.v_scales = self.master = None
-        if state_bits == 32:
-            self.m, self.v = (torch.zeros(N, dtype=torch.float32, device=dev) for _ in range(2))
-        else:
-            self.m_codes = torch.zeros(N, dtype=torch.int8, device=dev)
-            self.v_codes = torch.zeros(N, dtype=torch.uint8, device=dev)
-            self.m_scales, self.v_scales = (torch.zeros(N // nat.OB_STATE_BLOCK, dtype=torch.float32, device=dev)
-                                            for _ in range(2))
+        self.master = None
         if master:
-            self.master = torch.zeros(N, dtype=torch.float32, device=dev)
+            self.master = torch.zeros(self.list.state_elems, dtype=torch.float32, device=dev)
             for t, p in enumerate(self.params):
                 self._part(self.master, t).copy_(p.detach())
         self.control = nat.control_create(dev) if max_norm is not None else None
+
+    def _gradients(self, grads):
+        if grads is not None:
+            return list(grads)
+        for j, p in self._no_leaves:
+            if not p.retains_grad and p.grad is None:   # its .grad stays None, as of a parameter to leave alone
+                raise ValueError(f"parameter {j} is no leaf and has no .grad of its own: give the gradients to step")
+        return [p.grad for p in self.params]
+
+    def _changed(self, grads):
+        torch.autograd.graph.increment_version([p for p, g in zip(self.params, grads) if g is not None])
 
     def _part(self, flat, t):
         """Tensor t's part of a flat state buffer, in the parameter's shape."""
@@ -118,16 +104,51 @@ class AdamW:
         """Steps taken (waits for the GPU with max_norm)."""
         return self.hp.step if self.control is None else int(nat.control_fields(self.control)["step"])
 
+
+class AdamW(ListOptimizer):
+    """AdamW with decoupled weight decay, states in fp32 or in 8 bits.
+
+    ``params``: tensors (fp32, bf16, fp16; contiguous, on one GPU), or parameter groups as dicts with "params" (tensors, or
+    one) and optionally "lr" and "weight_decay", which can not be changed later on; no other argument can differ between
+    groups, and a common value of 0 allows no other.  ``state_bits``: 32 or 8.  ``master``: keep fp32 master copies of 16-bit
+    parameters (taken from them here).  ``max_norm``: clip by the global gradient norm and leave out steps whose norm is
+    not finite (inf, 0 or less: only the latter); None: neither.  ``rounding="stochastic"`` rounds 8-bit states and
+    16-bit parameters without a master by chance, with bits from (``sr_seed``, the step).
+
+    ``step()`` takes ``p.grad`` of every parameter (or the list it is given); a parameter without a gradient is
+    left alone.  Everything is enqueued on the current stream and nothing waits for the GPU, so a step can be captured
+    into a HIP graph; with ``max_norm`` the step count then lives in ``self.control``, where a replay
+    advances it, and ``set_lr_scale`` changes the rate between replays; the optimizer must outlive the graph.  Without
+    ``max_norm`` the count is a host value, which a captured step would repeat: capturing then raises.
+
+    ``self.hp`` holds the step's parameters; what is changed there (``hp.lr``) holds from the next step on.  The groups'
+    rates and decays keep their ratios to it.
+    """
+
+    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None,
+                 state_bits=32, master=False, rounding="nearest", sr_seed=0, bias_correction=True, grad_dtype=None):
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        common = dict(betas=tuple(betas), eps=eps, max_norm=max_norm, state_bits=state_bits, master=master, rounding=rounding,
+                      sr_seed=sr_seed, bias_correction=bias_correction, grad_dtype=grad_dtype, amsgrad=False, maximize=False)
+        self.state_bits = state_bits
+        self._begin(*self._collect(params, lr, weight_decay, common), grad_dtype, master, max_norm)
+        self.hp = nat.adamw_hparams(lr=lr, beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                                    bias_correction=bias_correction, step=0, rounding=_ROUNDING[rounding], sr_seed=sr_seed)
+        N, dev = self.list.state_elems, self.params[0].device
+        self.m = self.v = self.m_codes = self.m_scales = self.v_codes = self.v_scales = None
+        if state_bits == 32:
+            self.m, self.v = (torch.zeros(N, dtype=torch.float32, device=dev) for _ in range(2))
+        else:
+            self.m_codes = torch.zeros(N, dtype=torch.int8, device=dev)
+            self.v_codes = torch.zeros(N, dtype=torch.uint8, device=dev)
+            self.m_scales, self.v_scales = (torch.zeros(N // nat.OB_STATE_BLOCK, dtype=torch.float32, device=dev)
+                                            for _ in range(2))
+
     @torch.no_grad()
     def step(self, grads=None, loss_scale: float = 1.0, stream=None):
         """One step; loss_scale: what the gradients were multiplied with (other than 1 needs max_norm)."""
-        if grads is None:
-            for j, p in self._no_leaves:
-                if not p.retains_grad and p.grad is None:   # its .grad stays None, as of a parameter to leave alone
-                    raise ValueError(f"parameter {j} is no leaf and has no .grad of its own: give the gradients to step")
-            grads = [p.grad for p in self.params]
-        else:
-            grads = list(grads)
+        grads = self._gradients(grads)
         norm = None
         if self.control is not None:
             norm = (1.0 / loss_scale, self.max_norm)
@@ -148,7 +169,7 @@ class AdamW:
             if self.control is None:
                 self.hp.step -= 1   # a refused step is not counted
             raise
-        torch.autograd.graph.increment_version([p for p, g in zip(self.params, grads) if g is not None])
+        self._changed(grads)
 
     def moments(self):
         """The flat moments (m, v) in fp32; with 8-bit states what the codes stand for, in new tensors."""

@@ -26,6 +26,10 @@ UNITS = [
     ("ob_matmul.hip", ["-DOB_MM_BF16=0"]),     # products, by operand type: fp16
     ("ob_matmul.hip", ["-DOB_MM_BF16=1"]),     # bf16
     ("ob_matmul_api.cpp", []),
+    ("ob_clip.hip", []),
+    ("ob_clip_api.cpp", []),
+    ("ob_muon.hip", []),
+    ("ob_muon_api.cpp", []),
 ]
 BUILD_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -14,13 +14,9 @@ static_assert(sizeof(ob_control) == 64 && offsetof(ob_control, bc1) == 24 && off
 namespace {
 
 using ob::DeviceGuard;
+using ob::kKeepBytes;
 using ob::kNormElems;
 using ob::kStepElems;
-// Gradient bytes at a call's end that the norm reads with ordinary loads, which leave them in the last-level
-// cache for the step that follows; what comes before is read nontemporally, which is faster.  Norm and step
-// of 1.09e8 elements: bf16 278 us with ordinary loads and 293 nontemporal, fp32 (436 MB) 554 and 592; norm alone
-// of 3.1 GB: 513 and 452.
-constexpr int64_t kKeepBytes = int64_t(256) << 20;
 // Up to this many blocks the last one finishes the norm, beyond it another launch does.  12 tensors of 20,000
 // elements in all: 5.4 us and 6.2 (6.0 and 9.6 with the call); 200 of 1e7 (610 blocks): 19 us and 9, as each
 // block's ticket makes its memory visible to the others.
@@ -55,25 +51,33 @@ ob_status list_create(int64_t T, const int64_t* sizes, const int32_t* gd, const 
         !ob::build_items(l->shape, kNormElems, norm, l->norm.first))
         return OB_ERR_ARG;
     std::vector<ob::ListTensor> tensors;
-    for (int32_t t : l->shape.order) tensors.push_back({l->shape.state_off[t], lr ? lr[t] : 1.0f, wd ? wd[t] : 1.0f});
+    for (int32_t t : l->shape.order) {
+        l->lr_mults.push_back(lr ? lr[t] : 1.0f);
+        l->wd_mults.push_back(wd ? wd[t] : 1.0f);
+        tensors.push_back({l->shape.state_off[t], l->lr_mults.back(), l->wd_mults.back()});
+    }
 
     if (hipGetDevice(&l->device) != hipSuccess) return OB_ERR_HIP;
-    const size_t a = step.size() * sizeof(ob::ListItem), b = norm.size() * sizeof(ob::ListItem);
-    const size_t bytes = a + b + tensors.size() * sizeof(ob::ListTensor);
-    if (bytes > 0) {
-        std::vector<char> tables(bytes);
-        std::copy_n(reinterpret_cast<const char*>(step.data()), a, tables.data());
-        std::copy_n(reinterpret_cast<const char*>(norm.data()), b, tables.data() + a);
-        std::copy_n(reinterpret_cast<const char*>(tensors.data()), bytes - a - b, tables.data() + a + b);
-        hipError_t e = hipMalloc(&l->d_tables, bytes);
-        if (e == hipSuccess) e = hipMemcpy(l->d_tables, tables.data(), bytes, hipMemcpyHostToDevice);
+    std::vector<char> tables;
+    auto put = [&](const auto& v) {   // v behind what is there, at a multiple of 8 bytes; its offset
+        const size_t at = (tables.size() + 7) / 8 * 8, bytes = v.size() * sizeof(v[0]);
+        tables.resize(at + bytes);
+        std::copy_n(reinterpret_cast<const char*>(v.data()), bytes, tables.data() + at);
+        return at;
+    };
+    const size_t a = put(step), b = put(norm), c = put(tensors), f = put(l->norm.first), o = put(l->shape.order);
+    if (T > 0) {
+        hipError_t e = hipMalloc(&l->d_tables, tables.size());
+        if (e == hipSuccess) e = hipMemcpy(l->d_tables, tables.data(), tables.size(), hipMemcpyHostToDevice);
         // a first call may be on a stream that does not wait for the null stream
         if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
         if (e != hipSuccess) return e == hipErrorOutOfMemory ? OB_ERR_OOM : OB_ERR_HIP;
         const char* d = static_cast<const char*>(l->d_tables);
-        l->step.d_items = reinterpret_cast<const ob::ListItem*>(d);
-        l->norm.d_items = reinterpret_cast<const ob::ListItem*>(d + a);
-        l->d_tensors = reinterpret_cast<const ob::ListTensor*>(d + a + b);
+        l->step.d_items = reinterpret_cast<const ob::ListItem*>(d + a);
+        l->norm.d_items = reinterpret_cast<const ob::ListItem*>(d + b);
+        l->d_tensors = reinterpret_cast<const ob::ListTensor*>(d + c);
+        l->d_norm_first = reinterpret_cast<const int64_t*>(d + f);
+        l->d_order = reinterpret_cast<const int32_t*>(d + o);
     }
     *out = l;
     return OB_OK;

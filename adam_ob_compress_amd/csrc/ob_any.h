@@ -86,5 +86,64 @@ __device__ __forceinline__ void store_any1(void* __restrict__ p, int64_t i, floa
         static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(round16<D, SR>(x, w >> 16));
 }
 
+// ------------------------------------------------------------------------------------------------
+// sums of squares of a list's gradients: squares and sums in double
+// ------------------------------------------------------------------------------------------------
+
+typedef uint32_t u4e __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int G>
+__device__ __forceinline__ float load_grad1(const void* g, int64_t i)
+{
+    if (G == 0) return static_cast<const float*>(g)[i];
+    const uint32_t h = static_cast<const uint16_t*>(g)[i];
+    return G == 1 ? __uint_as_float(h << 16) : ErrF16::widen(h);
+}
+
+__device__ __forceinline__ void add_square(float x, double& s) { s = fma(static_cast<double>(x), static_cast<double>(x), s); }
+
+// Sum of the squares in 16 bytes of gradients into two sums (the second shortens the chain of additions).
+template <int G>
+__device__ __forceinline__ void add_squares(u4e u, double s[2])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (G == 0) {
+            add_square(__uint_as_float(u[k]), s[k & 1]);
+        } else {
+            add_square(G == 1 ? __uint_as_float(u[k] << 16) : ErrF16::widen(u[k] & 0xffffu), s[0]);
+            add_square(G == 1 ? __uint_as_float(u[k] & 0xffff0000u) : ErrF16::widen(u[k] >> 16), s[1]);
+        }
+    }
+}
+
+// The squares of an item's elements, by a block of kListBlock threads.
+template <int G, bool NT>
+__device__ __forceinline__ void item_squares(const void* grad, const ListItem& it, double s[2])
+{
+    constexpr int V = G == 0 ? 4 : 8, U = 8, kTrip = V * kListBlock * U;
+    const char* g = static_cast<const char*>(grad) + it.start * (16 / V);
+    const int tid = static_cast<int>(threadIdx.x);
+    int base = 0;
+    for (; base + kTrip <= it.len; base += kTrip) {
+        u4e x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const u4e* at = reinterpret_cast<const u4e*>(g + int64_t(base) * (16 / V)) + u * kListBlock + tid;
+            x[u] = NT ? __builtin_nontemporal_load(at) : *at;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add_squares<G>(x[u], s);
+    }
+    for (; base < it.len; base += V * kListBlock) {   // a tensor's last item
+        const int at = base + V * tid, cnt = it.len - at;
+        if (cnt >= V) {
+            add_squares<G>(*reinterpret_cast<const u4e*>(g + int64_t(at) * (16 / V)), s);
+        } else {
+            for (int k = 0; k < cnt; ++k) add_square(load_grad1<G>(g, at + k), s[0]);
+        }
+    }
+}
+
 }  // namespace
 }  // namespace ob

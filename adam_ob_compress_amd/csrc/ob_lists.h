@@ -130,6 +130,20 @@ inline ob_status check_hparams(const ob_adamw_hparams* hp, bool eight, bool has_
     return OB_OK;
 }
 
+// Places that a call writes, one range for each tensor that has some: apart from each other.
+struct WriteRange {
+    uintptr_t a, b;
+};
+inline ob_status check_apart(std::vector<WriteRange>& r)
+{
+    auto less = [](const WriteRange& x, const WriteRange& y) { return x.a < y.a; };
+    // ascending addresses, as of views into one buffer, need one look; others are sorted
+    if (!std::is_sorted(r.begin(), r.end(), less)) std::sort(r.begin(), r.end(), less);
+    for (size_t k = 1; k < r.size(); ++k)
+        if (r[k].a < r[k - 1].b) return OB_ERR_ARG;
+    return OB_OK;
+}
+
 // Addresses of one call (p == NULL: gradients only): none missing, aligned to their elements, parameters
 // apart from each other.
 inline ob_status check_pointers(const ListShape& l, const void* const* g, void* const* p)
@@ -145,23 +159,14 @@ inline ob_status check_pointers(const ListShape& l, const void* const* g, void* 
         if (!is_aligned(p[t], dtype_bytes(l.p_dtype[t]))) return OB_ERR_ALIGN;
     }
     if (!p) return OB_OK;
-    // ascending addresses, as of views into one buffer, need one look; others are sorted
-    struct Range {
-        uintptr_t a, b;
-    };
-    std::vector<Range> r;
+    std::vector<WriteRange> r;
     r.reserve(T);
-    bool sorted = true;
     for (size_t t = 0; t < T; ++t) {
         if (l.size[t] == 0 || !g[t]) continue;
         const uintptr_t a = reinterpret_cast<uintptr_t>(p[t]);
-        if (!r.empty() && a < r.back().a) sorted = false;
         r.push_back({a, a + static_cast<uintptr_t>(l.size[t] * dtype_bytes(l.p_dtype[t]))});
     }
-    if (!sorted) std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.a < y.a; });
-    for (size_t k = 1; k < r.size(); ++k)
-        if (r[k].a < r[k - 1].b) return OB_ERR_ARG;
-    return OB_OK;
+    return check_apart(r);
 }
 
 // Arguments of a step but for its states.
@@ -174,6 +179,37 @@ inline ob_status check_step(const ListShape& l, const void* const* g, void* cons
     if (!p) return OB_ERR_ARG;
     if (!is_aligned(master, 16)) return OB_ERR_ALIGN;
     return check_pointers(l, g, p);
+}
+
+inline ob_status check_tensor_norms(const ListShape& l, const void* const* g, float g_mult, int32_t kind, const float* norms,
+                                    const void* workspace)
+{
+    if (!std::isfinite(g_mult) || g_mult == 0.0f) return OB_ERR_ARG;
+    if (kind != OB_NORM_2 && kind != OB_NORM_MAX) return OB_ERR_ARG;
+    if (!norms || (!l.size.empty() && !workspace)) return OB_ERR_ARG;
+    if (!is_aligned(norms, 4) || !is_aligned(workspace, 8)) return OB_ERR_ALIGN;
+    return check_pointers(l, g, nullptr);
+}
+
+// out == NULL: in place
+inline ob_status check_clip(const ListShape& l, const void* const* g, void* const* out, const float* norms, float max_norm,
+                            float g_mult, int32_t per_tensor)
+{
+    if (!std::isfinite(g_mult) || g_mult == 0.0f || std::isnan(max_norm)) return OB_ERR_ARG;
+    if (per_tensor != 0 && per_tensor != 1) return OB_ERR_ARG;
+    if (!norms) return OB_ERR_ARG;
+    if (!is_aligned(norms, 4)) return OB_ERR_ALIGN;
+    if (out) return check_pointers(l, g, out);
+    if (ob_status st = check_pointers(l, g, nullptr)) return st;
+    if (l.n == 0) return OB_OK;
+    std::vector<WriteRange> r;
+    r.reserve(l.size.size());
+    for (size_t t = 0; t < l.size.size(); ++t)
+        if (l.size[t] > 0 && g[t]) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(g[t]);
+            r.push_back({a, a + static_cast<uintptr_t>(l.size[t] * dtype_bytes(l.g_dtype[t]))});
+        }
+    return check_apart(r);
 }
 
 inline ob_status check_norm(const ListShape& l, const void* const* g, float g_mult, float max_norm,

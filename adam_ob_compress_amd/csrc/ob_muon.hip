@@ -1,0 +1,308 @@
+// ob_muon.hip -- the Muon step over lists of matrices: momentum with the sums of squares, the normalised matrices in fp16, the
+// products of the iterations, and the update in the last product's epilogue.
+#include "ob_any.h"
+#include "ob_mfma.h"
+#include "ob_muon_kernels.h"
+
+namespace ob {
+namespace {
+
+// The iteration's polynomial, and the powers of two that its matrices are held times: X in fp16 times 2^9, A and
+// B = b A + c A^2 times 2^10.  |X| <= 1.3, |A| <= 1.5 and |B| < 12 throughout, so nothing overflows, and values down to 2^-14 / 2^9 of X keep all
+// their bits.  fp16 rounds eight times finer than bf16 at the same rate: X after five iterations is off by 1.2e-3 to 4e-3 (2-norm), in
+// bf16 by 1e-2 to 3e-2.
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kScaleX = 512.0f;
+constexpr float kGram = 1.0f / 256.0f;      // sums of X X^T (2^18) to A (2^10)
+constexpr float kUp = 1.0f / 1024.0f;       // sums of A A (2^20) to 2^10, of B X (2^19) to 2^9
+
+__device__ __forceinline__ bool skips(const MuonCall& c) { return c.control && c.control->skip != 0; }
+__device__ __forceinline__ float grad_scale(const MuonCall& c) { return c.control ? c.control->grad_scale : 1.0f; }
+
+// u from the scaled gradient and the new momentum
+__device__ __forceinline__ float direction(const MuonCall& c, float g, float m)
+{
+    return c.nesterov ? static_cast<float>((1.0 - c.momentum) * static_cast<double>(g) + c.momentum * static_cast<double>(m)) : m;
+}
+
+__device__ __forceinline__ f4 load4u(const float* p, int64_t i) { return *reinterpret_cast<const f4e*>(p + i); }
+
+// m = mu m + (1-mu) g', and the sum of u^2 of an item.  One pass: g and m in, m out.
+template <int G>
+__global__ __launch_bounds__(kListBlock) void k_muon_momentum(MuonCall c, ListPtrs ptrs)
+{
+    __shared__ double lds[kListBlock / 64];
+    if (skips(c)) return;
+    const MuonItem it = c.items[blockIdx.x];
+    const MuonMatrix& mt = c.matrices[it.matrix];
+    const void* g = ptrs.g[mt.place - c.place0];
+    if (g == nullptr) return;
+    const float scale = grad_scale(c);
+    const double mu = c.momentum;
+    const int64_t gi = mt.elem + it.start;
+    float* m = c.m + mt.state + it.start;
+    double s = 0.0;
+    auto one = [&](float x, float old) {
+        const float y = mul(x, scale);
+        const float now = static_cast<float>(mu * static_cast<double>(old) + (1.0 - mu) * static_cast<double>(y));
+        add_square(direction(c, y, now), s);
+        return now;
+    };
+    for (int at = 4 * static_cast<int>(threadIdx.x); at < it.len; at += kListTile) {
+        if (it.len - at >= 4) {
+            const f4 x = load_any4<G>(g, gi + at), old = load4u(m, at);
+            f4 now;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) now[e] = one(x[e], old[e]);
+            *reinterpret_cast<f4e*>(m + at) = now;
+        } else {
+            for (int e = at; e < it.len; ++e) m[e] = one(load_any1<G>(g, gi + e), m[e]);
+        }
+    }
+    s = block_sum(s, lds);
+    if (threadIdx.x == 0) c.parts[blockIdx.x] = s;
+}
+
+// What u is multiplied with: 2^9 / (|u| + eps), one work group for each matrix.
+__global__ __launch_bounds__(kListBlock) void k_muon_factor(MuonCall c)
+{
+    __shared__ double lds[kListBlock / 64];
+    if (skips(c)) return;
+    const MuonMatrix& mt = c.matrices[blockIdx.x];
+    double s = 0.0;
+    for (int i = static_cast<int>(threadIdx.x); i < mt.parts; i += kListBlock) s += c.parts[mt.part0 + i];
+    s = block_sum(s, lds);
+    if (threadIdx.x == 0) c.factor[blockIdx.x] = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(s) + c.eps));
+}
+
+// A tile of X from g and m, smaller side first, zeros where the sides are rounded up.  A matrix with more rows than columns is
+// turned over in LDS.
+template <int G>
+__global__ __launch_bounds__(kListBlock) void k_muon_write(MuonCall c, ListPtrs ptrs)
+{
+    constexpr int T = kMuonWriteTile;
+    __shared__ float turned[T][T + 1];
+    if (skips(c)) return;
+    const MuonTile tl = c.write[blockIdx.x];
+    const MuonMatrix& mt = c.matrices[tl.matrix];
+    const void* g = ptrs.g[mt.place - c.place0];
+    if (g == nullptr) return;
+    const float scale = grad_scale(c), f = c.factor[tl.matrix];
+    const bool tall = mt.rows > mt.cols;
+    // the tile in the parameter's orientation
+    const int row0 = (tall ? tl.j : tl.i) * T, col0 = (tall ? tl.i : tl.j) * T;
+    const int tid = static_cast<int>(threadIdx.x), line = tid >> 4, q = (tid & 15) * 4;
+    _Float16* x = reinterpret_cast<_Float16*>(c.half + mt.x[0]);
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+    const float* m = c.m + mt.state;
+    for (int i = line; i < T; i += 16) {
+        const int row = row0 + i, col = col0 + q;
+        float v[4] = {};
+        const int64_t at = static_cast<int64_t>(row) * mt.cols + col;
+        if (row < mt.rows && col + 4 <= mt.cols) {
+            const f4 gv = load_any4<G>(g, mt.elem + at), mv = load4u(m, at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = mul(direction(c, mul(gv[e], scale), mv[e]), f);
+        } else if (row < mt.rows) {
+            for (int e = 0; e < 4; ++e)
+                if (col + e < mt.cols) v[e] = mul(direction(c, mul(load_any1<G>(g, mt.elem + at + e), scale), m[at + e]), f);
+        }
+        if (tall) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) turned[q + e][i] = v[e];
+        } else if (row < mt.r && col < mt.k) {   // k is a multiple of 8
+            const h4 h = {static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1]), static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
+            *reinterpret_cast<h4*>(x + static_cast<int64_t>(row) * mt.k + col) = h;
+        }
+    }
+    if (!tall) return;
+    __syncthreads();
+    for (int i = line; i < T; i += 16) {
+        const int row = tl.i * T + i, col = tl.j * T + q;
+        if (row >= mt.r || col >= mt.k) continue;
+        const h4 h = {static_cast<_Float16>(turned[i][q]), static_cast<_Float16>(turned[i][q + 1]), static_cast<_Float16>(turned[i][q + 2]),
+                      static_cast<_Float16>(turned[i][q + 3])};
+        *reinterpret_cast<h4*>(x + static_cast<int64_t>(row) * mt.k + col) = h;
+    }
+}
+
+typedef _Float16 h4v __attribute__((ext_vector_type(4)));
+
+// The tile's sums for a product: rows from m0, columns from n0 on.
+template <int PRODUCT, class P>
+__device__ __forceinline__ void muon_sums(P& tile, const MuonCall& c, const MuonMatrix& mt, int turn, int m0, int n0, char* lds)
+{
+    const uint16_t* x = c.half + mt.x[turn & 1];
+    if constexpr (PRODUCT == MUON_GRAM)
+        tile.run(Operand{x + static_cast<int64_t>(m0) * mt.k, mt.k, mt.r - m0, mt.k},
+                 Operand{x + static_cast<int64_t>(n0) * mt.k, mt.k, mt.r - n0, mt.k}, lds);
+    else if constexpr (PRODUCT == MUON_POLY)
+        tile.run(Operand{c.half + mt.a + static_cast<int64_t>(m0) * mt.r, mt.r, mt.r - m0, mt.r},
+                 Operand{c.half + mt.a + static_cast<int64_t>(n0) * mt.r, mt.r, mt.r - n0, mt.r}, lds);
+    else
+        tile.run(Operand{c.half + mt.b + static_cast<int64_t>(m0) * mt.r, mt.r, mt.r - m0, mt.r},
+                 Operand{x + n0, mt.k, mt.k - n0, mt.r}, lds);
+}
+
+template <int TM, int WM, int WN, int PRODUCT>
+using MuonProduct = TileProduct<TM, TM, WM, WN, false, true, PRODUCT != MUON_STEP, true>;
+
+template <int TM, int WM, int WN, int PRODUCT>
+__global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_product(MuonCall c, const MuonTile* tiles, int turn)
+{
+    using P = MuonProduct<TM, WM, WN, PRODUCT>;
+    __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+    if (skips(c)) return;
+    const MuonTile tl = tiles[blockIdx.x];
+    const MuonMatrix mt = c.matrices[tl.matrix];
+    const int m0 = tl.i * TM, n0 = tl.j * TM;
+    P tile;
+    muon_sums<PRODUCT>(tile, c, mt, turn, m0, n0, lds);
+    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + (PRODUCT == MUON_STEP ? mt.x[turn & 1] : mt.a));
+    _Float16* to = reinterpret_cast<_Float16*>(c.half + (PRODUCT == MUON_GRAM ? mt.a : PRODUCT == MUON_POLY ? mt.b : mt.x[~turn & 1]));
+    const int64_t ld = PRODUCT == MUON_STEP ? mt.k : mt.r;
+    const int cols = PRODUCT == MUON_STEP ? mt.k : mt.r;
+    tile.each([&](int r, int col, f4v s) {
+        const int i = m0 + r, j = n0 + col;
+        if (i >= mt.r || j >= cols) return;   // both sides are multiples of 8
+        h4v h;
+        if constexpr (PRODUCT == MUON_GRAM) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(s[e] * kGram);
+        } else {
+            const h4v old = *reinterpret_cast<const h4v*>(from + i * ld + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float o = static_cast<float>(old[e]);
+                h[e] = static_cast<_Float16>(PRODUCT == MUON_POLY ? fmaf(kC * kUp, s[e], kB * o) : fmaf(kUp, s[e], kA * o));
+            }
+        }
+        *reinterpret_cast<h4v*>(to + i * ld + j) = h;
+        if (PRODUCT != MUON_STEP && tl.i != tl.j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[(j + e) * ld + i] = h[e];
+        }
+    });
+}
+
+// The last X and the update.
+template <int TM, int WM, int WN, int PK>
+__global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_last(MuonCall c, ListPtrs ptrs, const MuonTile* tiles, int turn)
+{
+    using P = MuonProduct<TM, WM, WN, MUON_STEP>;
+    constexpr bool kMaster = PK == PK_MASTER_BF16 || PK == PK_MASTER_F16;
+    constexpr int D = kMaster ? PK - 2 : PK;
+    __shared__ __attribute__((aligned(16))) char lds[P::kLds];
+    if (skips(c)) return;
+    const MuonTile tl = tiles[blockIdx.x];
+    const MuonMatrix mt = c.matrices[tl.matrix];
+    if (ptrs.g[mt.place - c.place0] == nullptr) return;
+    void* p = ptrs.p[mt.place - c.place0];
+    const int m0 = tl.i * TM, n0 = tl.j * TM;
+    P tile;
+    muon_sums<MUON_STEP>(tile, c, mt, turn, m0, n0, lds);
+
+    const double R = mt.rows, C = mt.cols, big = R > C ? R : C;
+    const double scale = c.scale == OB_MUON_MATCH_RMS ? 0.2 * sqrt(big) : c.scale == OB_MUON_SHAPE && R > C ? sqrt(R / C) : 1.0;
+    const float l = static_cast<float>(c.lr * static_cast<double>(mt.lr_mult) * (c.control ? static_cast<double>(c.control->lr_scale) : 1.0));
+    const float d = static_cast<float>(c.wd * static_cast<double>(mt.wd_mult)), sx = static_cast<float>(scale / kScaleX);
+    const bool tall = mt.rows > mt.cols;
+    const int rows = tall ? mt.cols : mt.rows, cols = tall ? mt.rows : mt.cols;   // of X, without what was rounded up
+    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + mt.x[turn & 1]);
+    float* master = kMaster ? c.master + mt.state : nullptr;
+    const u4 none{};
+    auto update = [&](float old, float x) { return fmaf(-l, fmaf(d, old, sx * x), old); };
+    auto one = [&](int64_t at, float x) {
+        const float now = update(kMaster ? master[at] : load_any1<D>(p, mt.elem + at), x);
+        if (kMaster) master[at] = now;
+        store_any1<D, false>(p, mt.elem + at, now, 0);
+    };
+    tile.each([&](int r, int col, f4v s) {
+        const int i = m0 + r, j = n0 + col;
+        if (i >= rows || j >= cols) return;
+        const h4v old = *reinterpret_cast<const h4v*>(from + static_cast<int64_t>(i) * mt.k + j);
+        f4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(kUp, s[e], kA * static_cast<float>(old[e]));
+        if (!tall && j + 4 <= cols) {
+            const int64_t at = static_cast<int64_t>(i) * mt.cols + j;
+            const f4 was = kMaster ? load4u(master, at) : load_any4<D>(p, mt.elem + at);
+            f4 now;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) now[e] = update(was[e], x[e]);
+            if (kMaster) *reinterpret_cast<f4e*>(master + at) = now;
+            store_any4<D, false>(p, mt.elem + at, now, none);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < cols) one(tall ? static_cast<int64_t>(j + e) * mt.cols + i : static_cast<int64_t>(i) * mt.cols + j + e, x[e]);
+        }
+    });
+}
+
+template <int TM, int WM, int WN>
+hipError_t product(const MuonCall& c, int product, const MuonTile* tiles, int64_t count, int turn, hipStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(count)), block(64 * (TM / WM) * (TM / WN));
+    if (product == MUON_GRAM)
+        hipLaunchKernelGGL((k_muon_product<TM, WM, WN, MUON_GRAM>), grid, block, 0, s, c, tiles, turn);
+    else if (product == MUON_POLY)
+        hipLaunchKernelGGL((k_muon_product<TM, WM, WN, MUON_POLY>), grid, block, 0, s, c, tiles, turn);
+    else
+        hipLaunchKernelGGL((k_muon_product<TM, WM, WN, MUON_STEP>), grid, block, 0, s, c, tiles, turn);
+    return hipGetLastError();
+}
+
+template <int TM, int WM, int WN>
+hipError_t last(const MuonCall& c, const ListPtrs& ptrs, const MuonTile* tiles, int64_t count, int turn, int pk, hipStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(count)), block(64 * (TM / WM) * (TM / WN));
+    switch (pk) {
+    case PK_F32: hipLaunchKernelGGL((k_muon_last<TM, WM, WN, PK_F32>), grid, block, 0, s, c, ptrs, tiles, turn); break;
+    case PK_BF16: hipLaunchKernelGGL((k_muon_last<TM, WM, WN, PK_BF16>), grid, block, 0, s, c, ptrs, tiles, turn); break;
+    case PK_F16: hipLaunchKernelGGL((k_muon_last<TM, WM, WN, PK_F16>), grid, block, 0, s, c, ptrs, tiles, turn); break;
+    case PK_MASTER_BF16: hipLaunchKernelGGL((k_muon_last<TM, WM, WN, PK_MASTER_BF16>), grid, block, 0, s, c, ptrs, tiles, turn); break;
+    case PK_MASTER_F16: hipLaunchKernelGGL((k_muon_last<TM, WM, WN, PK_MASTER_F16>), grid, block, 0, s, c, ptrs, tiles, turn); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_muon_momentum(const MuonCall& c, const ListPtrs& ptrs, int g, int64_t items, hipStream_t s)
+{
+    const auto k = g == OB_BF16 ? k_muon_momentum<1> : g == OB_F16 ? k_muon_momentum<2> : k_muon_momentum<0>;
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(items)), dim3(kListBlock), 0, s, c, ptrs);
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_factor(const MuonCall& c, int64_t matrices, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_muon_factor, dim3(static_cast<unsigned>(matrices)), dim3(kListBlock), 0, s, c);
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_write(const MuonCall& c, const ListPtrs& ptrs, int g, int64_t tiles, hipStream_t s)
+{
+    const auto k = g == OB_BF16 ? k_muon_write<1> : g == OB_F16 ? k_muon_write<2> : k_muon_write<0>;
+    hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(tiles)), dim3(kListBlock), 0, s, c, ptrs);
+    return hipGetLastError();
+}
+
+hipError_t launch_muon_product(const MuonCall& c, int kind, const MuonTile* tiles, int64_t count, int tile, int turn, hipStream_t s)
+{
+    return tile == 0   ? product<256, 128, 64>(c, kind, tiles, count, turn, s)
+           : tile == 1 ? product<128, 64, 64>(c, kind, tiles, count, turn, s)
+                       : product<64, 32, 32>(c, kind, tiles, count, turn, s);
+}
+
+hipError_t launch_muon_last(const MuonCall& c, const ListPtrs& ptrs, const MuonTile* tiles, int64_t count, int tile, int turn, int pk,
+                            hipStream_t s)
+{
+    return tile == 0   ? last<256, 128, 64>(c, ptrs, tiles, count, turn, pk, s)
+           : tile == 1 ? last<128, 64, 64>(c, ptrs, tiles, count, turn, pk, s)
+                       : last<64, 32, 32>(c, ptrs, tiles, count, turn, pk, s);
+}
+
+}  // namespace ob

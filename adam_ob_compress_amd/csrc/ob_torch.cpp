@@ -258,6 +258,70 @@ PyObject* state8(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
+// A workspace: a byte tensor of at least this size.
+void* room(PyObject* item, int64_t bytes, long device, int64_t where)
+{
+    if (!THPVariable_Check(item)) throw Bad{where, 0};
+    const int64_t n = THPVariable_Unpack(item).numel();
+    if (n < bytes) throw Bad{where, 0};
+    return address(item, at::kByte, n, device, Bad{where, 0});
+}
+
+// tensor_norms(list, grads, norms, workspace, bytes, g_mult, kind, stream)
+PyObject* tensor_norms(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        const List& l = list_of(args[0]);
+        const std::vector<void*> g = addresses(args[1], nullptr, l, l.g_types, 0);
+        auto* norms = static_cast<float*>(address(args[2], at::kFloat, static_cast<int64_t>(l.numel.size()) + 1, l.device, Bad{2, 0}));
+        void* work = room(args[3], PyLong_AsLongLong(args[4]), l.device, 3);
+        const float g_mult = static_cast<float>(PyFloat_AsDouble(args[5]));
+        const auto kind = static_cast<int32_t>(PyLong_AsLong(args[6]));
+        hipStream_t s = stream_of(args[7]);
+        return status_of([&] { return ob_tensor_norms(l.handle, g.data(), g_mult, kind, norms, work, s); });
+    });
+}
+
+// clip_grads(list, grads, out or None, norms, max_norm, g_mult, per_tensor, stream)
+PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded(n, 8, [&] {
+        const List& l = list_of(args[0]);
+        const std::vector<void*> g = addresses(args[1], nullptr, l, l.g_types, 0);
+        const bool to = args[2] != Py_None;
+        const std::vector<void*> out = to ? addresses(args[2], args[1], l, l.p_types, 1) : std::vector<void*>();
+        auto* norms = static_cast<const float*>(address(args[3], at::kFloat, static_cast<int64_t>(l.numel.size()) + 1, l.device, Bad{2, 0}));
+        const float max_norm = static_cast<float>(PyFloat_AsDouble(args[4])), g_mult = static_cast<float>(PyFloat_AsDouble(args[5]));
+        const int32_t each = PyObject_IsTrue(args[6]) == 1;
+        hipStream_t s = stream_of(args[7]);
+        return status_of([&] { return ob_clip_grads(l.handle, g.data(), to ? out.data() : nullptr, norms, max_norm, g_mult, each, s); });
+    });
+}
+
+// muon_step(list, plan, grads, params, hparams' address, stream, master, m, workspace, bytes, control, norm)
+PyObject* muon_step(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    return guarded(n, 12, [&] {
+        const List& l = list_of(args[0]);
+        auto* plan = static_cast<ob_muon>(PyLong_AsVoidPtr(args[1]));
+        const std::vector<void*> g = addresses(args[2], nullptr, l, l.g_types, 0);
+        const std::vector<void*> p = addresses(args[3], args[2], l, l.p_types, 1);
+        const auto* hp = static_cast<const ob_muon_hparams*>(PyLong_AsVoidPtr(args[4]));
+        hipStream_t s = stream_of(args[5]);
+        auto* master = static_cast<float*>(flat(args[6], at::kFloat, l.state_elems, l.device, 2));
+        auto* m = static_cast<float*>(flat(args[7], at::kFloat, l.state_elems, l.device, 3));
+        void* work = room(args[8], PyLong_AsLongLong(args[9]), l.device, 4);
+        ob_control* ctl = control_of(args[10], l, 5);
+        const Norm norm(args[11]);
+        ob_adamw_hparams count{};   // only counts the step
+        return status_of([&] {
+            return norm.with(
+                l, g, &count, ctl, s, [&] { return ob_muon_check(plan, g.data(), p.data(), master, m, work, hp, ctl); },
+                [&] { return ob_muon_step(plan, g.data(), p.data(), master, m, work, hp, ctl, s); });
+        });
+    });
+}
+
 // A matrix or a batch of them: a dense GPU tensor of two or three dimensions with its memory; throws Bad otherwise.
 const at::Tensor& matrix(PyObject* item, int64_t where)
 {
@@ -369,6 +433,9 @@ PyMethodDef methods[] = {fast<list>("list"),
                          fast<adamw_step>("adamw_step"),
                          fast<adamw8_step>("adamw8_step"),
                          fast<state8>("state8"),
+                         fast<tensor_norms>("tensor_norms"),
+                         fast<clip_grads>("clip_grads"),
+                         fast<muon_step>("muon_step"),
                          fast<matmul>("matmul"),
                          {"scalar_type", scalar_type, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -13,6 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import _native as nat
+from .muon import GradClip
 
 
 def step_kind(step_index: int, freeze_step: int = 0, refresh_period: int = 0) -> str:
@@ -37,12 +38,15 @@ class OneBitAdam:
     With ``diagnostics=True`` every compressed step also leaves, per chunk, the squared L2 norm of the
     error buffer it read (``err_sumsq``) and its number of +1 signs (``plus_count``) ([P1] sec. 6.2
     and 8); ``small_error_chunks`` applies the tutorial's warning threshold to them.
+
+    ``max_norm=...`` clips every step's gradient by its global norm first, in place in ``g`` (a norm that is not finite
+    makes it NaN); the norm of the last step is in ``self.norm`` (one element on the GPU).
     """
 
     def __init__(self, plan: nat.Plan, err, m, v, p, *, lr, beta1=0.9, beta2=0.999, eps=1e-8,
                  clip=0.0, ef_mode=nat.OB_EF_PLAIN, ef_beta=0.9, int8_signs=False,
                  count_nonfinite=False, freeze_step=0, refresh_period=0, bias_correction=False,
-                 diagnostics=False, err_rounding="nearest", sr_seed=0):
+                 diagnostics=False, err_rounding="nearest", sr_seed=0, max_norm=None):
         self.plan = plan
         self.err, self.m, self.v, self.p = err, m, v, p
         self.freeze_step, self.refresh_period = freeze_step, refresh_period
@@ -59,6 +63,7 @@ class OneBitAdam:
         self.nonfinite = torch.zeros(1, dtype=torch.int64, device=dev) if count_nonfinite else None
         self.step_index = 0
         self.dense_steps = 0
+        self.max_norm, self._clips, self.norm = max_norm, {}, None
         self.err_sumsq = self.plus_count = None
         if diagnostics:
             self.err_sumsq = torch.zeros(plan.num_chunks, dtype=torch.float64, device=dev)
@@ -70,6 +75,8 @@ class OneBitAdam:
 
     def step(self, g, stream=None) -> str:
         kind = self.kind()
+        if self.max_norm is not None:
+            self._clip(g, stream)
         if kind == "dense":
             self.dense_steps += 1
             self.hp.bias_correction = 1 if self.bias_correction else 0
@@ -80,6 +87,11 @@ class OneBitAdam:
             self._compressed(g, stream)
         self.step_index += 1
         return kind
+
+    def _clip(self, g, stream):
+        if g.dtype not in self._clips:   # a list of one tensor for each type that gradients come in
+            self._clips[g.dtype] = GradClip([self.p], max_norm=self.max_norm, grad_dtype=g.dtype)
+        self.norm = self._clips[g.dtype]([g], stream=stream)
 
     def small_error_chunks(self, threshold: float = 1e-6) -> list[int]:
         """Chunks whose error buffer, as the last compressed step read it, had an L2 norm below

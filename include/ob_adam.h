@@ -430,6 +430,35 @@ ob_status ob_state8_encode(int64_t n, const float* m, const float* v, int8_t* m_
 ob_status ob_state8_decode(int64_t n, const int8_t* m_codes, const float* m_scales, const uint8_t* v_codes,
                            const float* v_scales, float* m, float* v, hipStream_t stream);
 
+/* ---- norms of many tensors, and clipped gradients ----
+ * For gradients that more than one optimizer steps, that another type holds, or that are clipped tensor by tensor; a step over
+ * one list alone takes its norm from ob_grad_norm.
+ *
+ * ob_tensor_norms, with T = ob_tensors_count(list), into device memory:
+ *   norms[t] = |g_mult| * sqrt(sum g_t^2)   OB_NORM_2    squares and sums in double, in an order that depends on the
+ *            = |g_mult| * max |g_t|         OB_NORM_MAX  list alone (the same bits on every call)
+ *   norms[T] = the same over all tensors.  Rounded to fp32 once; a tensor without a gradient or elements has norm 0, a
+ *   NaN in a tensor gives NaN.
+ * norms: fp32[T + 1].  workspace: ob_tensor_norms_workspace(list) bytes, 8-byte aligned, of any content; calls that may
+ * overlap need their own.
+ *
+ * ob_clip_grads: out_t = fl(widen(g_t) * f), rounded once more to out_t's type, to nearest;
+ *   f = g_mult * min(1, max_norm / (norm + 1e-6)) in double, rounded once; norm = norms[T], or norms[t] with per_tensor;
+ *   max_norm <= 0 or infinite: f = g_mult;  norm not finite: f = NaN, so that whatever steps over these gradients and leaves out
+ *   steps whose norm is not finite leaves out this one in all its parts.
+ * norms: fp32[T + 1], as ob_tensor_norms left it or joined over workers by the caller; read on the GPU.
+ * out == NULL: the gradients themselves, in their types (with f = 1 nothing is written); they must not overlap each other then.
+ * Otherwise out[t]: tensors of the list's parameter types, for every t that has a gradient; each may be g[t] if the types are
+ * of one width, and overlaps no other gradient or output.
+ * g_mult: finite, not 0 (the same in both calls); removes a loss scale. */
+typedef enum { OB_NORM_2 = 0, OB_NORM_MAX = 1 } ob_norm_kind;
+
+int64_t ob_tensor_norms_workspace(ob_tensors list);   /* bytes; -1 for a NULL list */
+ob_status ob_tensor_norms(ob_tensors list, const void* const* g, float g_mult, int32_t kind, float* norms, void* workspace,
+                          hipStream_t stream);
+ob_status ob_clip_grads(ob_tensors list, const void* const* g, void* const* out, const float* norms, float max_norm,
+                        float g_mult, int32_t per_tensor, hipStream_t stream);
+
 /* ---- matrix products ----
  * D = alpha * A B + beta * C over a batch, 16-bit operands, sums in fp32: statistics of gradients (L = b L + a G G^T),
  * projections of gradients, and what the Muon step below is made of.
@@ -466,6 +495,54 @@ typedef struct {
 } ob_product;
 
 ob_status ob_matmul(const ob_product* product, hipStream_t stream);
+
+/* ---- Muon over lists of matrices ----
+ * The step of the Muon optimizer, for the matrices of a model (AdamW steps the rest): momentum, the momentum's nearest
+ * semi-orthogonal matrix by a polynomial iteration, decoupled decay and the update.  With f = grad_scale and r = lr_scale
+ * of `control` (NULL: 1), for each matrix of R rows and C columns:
+ *   g' = fl32(widen(g) * f);  m = fl32(mu*m + (1-mu)*g');  u = nesterov ? (1-mu)*g' + mu*m : m
+ *   X = u / (|u| + eps), |u| the Frobenius norm, its sum in double
+ *   `iterations` times, with X taken with its smaller side first:  A = X X^T,  X = a X + (b A + c A^2) X,
+ *     a, b, c = 3.4445, -4.7750, 2.0315: singular values in (0, 1] are driven into about [0.7, 1.2]
+ *   p -= l * (weight_decay * wd_mults[j] * p + s * X),  l = lr * r * lr_mults[j],
+ *     s = 1 (OB_MUON_PLAIN), sqrt(max(1, R / C)) (OB_MUON_SHAPE) or 0.2 sqrt(max(R, C)) (OB_MUON_MATCH_RMS: updates of about
+ *     the size of AdamW's, so that both take one rate and decay)
+ * Operands of the products are fp16 times powers of two (X 2^9, A and b A + c A^2 2^10; the iteration's bounds keep them in
+ * range), sums fp32: X is off by 1 to 4 parts in 1000 (2-norm, five iterations), the more the smaller its smallest singular
+ * values; directions whose singular value is below 2^-12 of |u| may come out as noise of that size, grown by the iteration as they
+ * would be themselves.
+ * The decay and the update are one fp32 expression, fma(-l, fma(d, p, s X), p), rounded once more to a 16-bit p without
+ * master.  control with skip set: nothing changes.
+ *
+ * The plan holds the matrices' shapes for a list: tensor t has sizes[t] = E * rows[t] * cols[t] elements, E >= 0 matrices behind
+ * each other, each by rows.  rows, cols: T host int64, 1 to 2^30.  It belongs to the list's device, copies what it needs of
+ * the list, and owns its device tables.
+ * m, master: flat, ob_tensors_state_elems(list) fp32 in the list's layout; g, p, master otherwise as in ob_adamw_step.
+ * workspace: ob_muon_workspace(plan) bytes of device memory, 16-byte aligned, of any content; calls that may overlap (other
+ * streams, captured graphs replayed at once) need their own.
+ * ob_muon_check: the status with which ob_muon_step would refuse these arguments; no GPU work. */
+typedef struct ob_muon_s* ob_muon;
+
+typedef enum { OB_MUON_PLAIN = 0, OB_MUON_SHAPE = 1, OB_MUON_MATCH_RMS = 2 } ob_muon_scale;
+
+typedef struct {
+    float lr;               /* finite */
+    float momentum;         /* mu in [0, 1) */
+    float weight_decay;     /* finite */
+    float eps;              /* > 0: at least 1e-30 */
+    int32_t nesterov;       /* 0 or 1 */
+    int32_t iterations;     /* 1 to 16 */
+    int32_t scale;          /* ob_muon_scale */
+    int32_t reserved;       /* 0 */
+} ob_muon_hparams;
+
+ob_status ob_muon_create(ob_tensors list, const int64_t* rows, const int64_t* cols, ob_muon* out);
+ob_status ob_muon_destroy(ob_muon plan);
+int64_t ob_muon_workspace(ob_muon plan);   /* bytes; -1 for a NULL plan */
+ob_status ob_muon_step(ob_muon plan, const void* const* g, void* const* p, float* master, float* m, void* workspace,
+                       const ob_muon_hparams* hp, const ob_control* control, hipStream_t stream);
+ob_status ob_muon_check(ob_muon plan, const void* const* g, void* const* p, const float* master, const float* m,
+                        const void* workspace, const ob_muon_hparams* hp, const ob_control* control);
 
 #ifdef __cplusplus
 }
