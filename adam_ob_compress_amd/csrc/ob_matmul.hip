@@ -69,30 +69,41 @@ __device__ __forceinline__ void store_row4(void* p, int64_t i, f4 x, int left)
 }
 
 template <int D, class P>
-__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, int64_t batch, int m0, int n0, bool mirror)
+__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
 {
     constexpr int64_t kBytes = D == 0 ? 4 : 2;
     const char* c = static_cast<const char*>(p.c) + batch * p.batch_c * kBytes;
     char* d = static_cast<char*>(p.d) + batch * p.batch_d * kBytes;
-    tile.each([&](int r, int col, f4v sum) {
-        const int i = m0 + r, j = n0 + col, left = p.n - j;
-        if (i >= p.m || left <= 0) return;
-        f4 x;
-        if (p.beta != 0.0f) {
-            const f4 y = load_row4<D>(c, i * p.ldc + j, left);
+    tile.finish(
+        lds, true,
+        [&](int r, int col, f4v sum) {
+            const int i = m0 + r, j = n0 + col, left = p.n - j;
+            if (i >= p.m || left <= 0) return;
+            f4 x;
+            if (p.beta != 0.0f) {
+                const f4 y = load_row4<D>(c, i * p.ldc + j, left);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
-        } else {
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
+            }
+            store_row4<D>(d, i * p.ldd + j, x, left);
+        },
+        mirror,
+        [&](int r, int col, f4v sum) {   // above the diagonal, with C's rows below it
+            const int i = m0 + r, j = n0 + col, left = p.m - i;
+            if (j >= p.n || left <= 0) return;
+            f4 x;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
-        }
-        store_row4<D>(d, i * p.ldd + j, x, left);
-        if (mirror) {
+            if (p.beta != 0.0f) {
+                const f4 y = load_row4<D>(c, j * p.ldc + i, left);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left) store_any1<D, false>(d, (j + e) * p.ldd + i, x[e], 0);
-        }
-    });
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
+            }
+            store_row4<D>(d, j * p.ldd + i, x, left);
+        });
 }
 
 template <int TM, int WM, int WN, bool AK, bool BK, bool CHUNKS>
@@ -109,11 +120,11 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_product(ProductA
              Operand{p.b + batch * p.batch_b + (BK ? n0 * p.ldb : n0), p.ldb, p.n - n0, p.k}, lds);
     const bool mirror = p.symmetric && ti != tj;
     if (p.out_type == OB_F32)
-        finish<0>(p, tile, batch, m0, n0, mirror);
+        finish<0>(p, tile, lds, batch, m0, n0, mirror);
     else if (p.out_type == OB_BF16)
-        finish<1>(p, tile, batch, m0, n0, mirror);
+        finish<1>(p, tile, lds, batch, m0, n0, mirror);
     else
-        finish<2>(p, tile, batch, m0, n0, mirror);
+        finish<2>(p, tile, lds, batch, m0, n0, mirror);
 }
 
 template <int TM, int WM, int WN, bool CHUNKS>

@@ -21,10 +21,11 @@ typedef uint32_t u4u __attribute__((ext_vector_type(4), aligned(2)));
 
 #define OB_LDS(T, p) ((__attribute__((address_space(3))) T*)(p))
 
-constexpr int kTileK = 64;    // K of a step: 128 bytes of a row
 
-// D[n][m] += R[n][k] L[m][k] for a 16 x 16 x 32 block: with R as the first operand a lane ends up with four
-// consecutive columns of one row of D, which is what a row-major D is stored by.
+// D[n][m] += R[n][k] L[m][k] for a 16 x 16 x 32 block: with R as the first operand a lane ends up with four consecutive
+// columns of one row of D, which is what a row-major D is stored by.  Blocks of 32 x 32 x 16 take as many cycles (8192^3: 1.34e6
+// and 1.35e6) but run at a lower clock, large products being bound by the power they draw: 931 us and 860.
+constexpr int kMfma = 16, kMfmaK = 32;
 template <bool BF16>
 __device__ __forceinline__ f4v mfma(s8v r, s8v l, f4v acc)
 {
@@ -42,21 +43,22 @@ struct Operand {
     int k;
 };
 
-// ROWS x kTileK elements of an operand in LDS, as 16-byte chunks whose places are permuted, so that neither the
-// reads of fragments nor the writes meet the same bank twice:
-//   K_MAJOR  a row's 8 chunks along K:  chunk c of row r at place c ^ (r & 7);
+// ROWS x KT elements (KT 64 or 32) of an operand in LDS, as 16-byte chunks whose places are permuted, so that the lanes that
+// read fragments together (lanes 0-3, 12-15 and 20-27 of a 16-byte read, and so on) meet different banks:
+//   K_MAJOR  a row's KT / 8 chunks along K:  chunk c of row r at place c ^ (r & 7), of four chunks at c ^ (r >> 1 & 3);
 //   else     a k's ROWS / 8 chunks along the rows:  chunk c of k at place c ^ 2 f(k), f(k) = k & 3 | (k >> 3 & 3) << 2
 //            (two chunks are the 16 rows of a fragment, and the 16 k of one read differ in f).
-template <int ROWS, int THREADS, bool K_MAJOR, bool ASYNC>
+template <int ROWS, int KT, int THREADS, bool K_MAJOR, bool ASYNC>
 struct Stage {
-    static constexpr int kBytes = ROWS * kTileK * 2;
+    static constexpr int kBytes = ROWS * KT * 2;
     static constexpr int kLoads = kBytes / 16 / THREADS;   // chunks per thread
-    static constexpr int kLine = K_MAJOR ? 8 : ROWS / 8;   // chunks per line (row, or k)
+    static constexpr int kLine = K_MAJOR ? KT / 8 : ROWS / 8;   // chunks per line (row, or k)
     static_assert(kLoads * THREADS * 16 == kBytes, "every thread loads the same number of chunks");
 
     static __device__ __forceinline__ int swizzle(int line)
     {
-        return K_MAJOR ? line & 7 : (((line & 3) | ((line >> 3 & 3) << 2)) << 1) & (kLine - 1);
+        if (K_MAJOR) return KT == 64 ? line & 7 : line >> 1 & 3;
+        return (((line & 3) | ((line >> 3 & 3) << 2)) << 1) & (kLine - 1);
     }
 
     u4v reg[ASYNC ? 1 : kLoads];
@@ -86,15 +88,15 @@ struct Stage {
     // Load of step t into LDS at `to` (ASYNC) or into registers.
     __device__ __forceinline__ void load(const Operand& o, int t, char* to)
     {
-        const int left = o.k - t * kTileK;   // k that there are from this step on
-        const uint16_t* base = o.p + (K_MAJOR ? static_cast<int64_t>(t) * kTileK : static_cast<int64_t>(t) * kTileK * o.ld);
+        const int left = o.k - t * KT;   // k that there are from this step on
+        const uint16_t* base = o.p + (K_MAJOR ? static_cast<int64_t>(t) * KT : static_cast<int64_t>(t) * KT * o.ld);
         if constexpr (ASYNC) {
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, kInside, 0x00027000);
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, left > 0 ? kInside : 0, 0x00027000);
             const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 uint32_t v = off[j];
-                if (left < kTileK) {
+                if (left < KT) {
                     int line, chunk;
                     place(j, line, chunk);
                     if ((K_MAJOR ? chunk * 8 : line) >= left) v = kOutside;
@@ -139,7 +141,7 @@ struct Stage {
     {
         const int lane = static_cast<int>(threadIdx.x) & 63, r = lane & 15, g = lane >> 4;
         if constexpr (K_MAJOR) {
-            return *reinterpret_cast<const s8v*>(at + (row0 + r) * 128 + ((kk * 4 + g) ^ (r & 7)) * 16);
+            return *reinterpret_cast<const s8v*>(at + (row0 + r) * (kLine * 16) + ((kk * 4 + g) ^ swizzle(r)) * 16);
         } else {
             // 16 lanes read four k of 16 rows, four rows each, and get four k of one row
             const int k = kk * 32 + g * 8 + (r >> 2);
@@ -160,11 +162,13 @@ private:
 template <int TM, int TN, int WM, int WN, bool BF16, bool L_KMAJOR, bool R_KMAJOR, bool ASYNC>
 struct TileProduct {
     static constexpr int kWavesN = TN / WN, kThreads = 64 * (TM / WM) * kWavesN;
-    static constexpr int kFm = WM / 16, kFn = WN / 16;
-    using SL = Stage<TM, kThreads, L_KMAJOR, ASYNC>;
-    using SR = Stage<TN, kThreads, R_KMAJOR, ASYNC>;
+    static constexpr int kFm = WM / kMfma, kFn = WN / kMfma;
+    static constexpr bool kTurns = kThreads == 512;   // see run_in_turns
+    static constexpr int kStages = kTurns ? 4 : 2, kTileK = kTurns ? 32 : 64;
+    using SL = Stage<TM, kTileK, kThreads, L_KMAJOR, ASYNC>;
+    using SR = Stage<TN, kTileK, kThreads, R_KMAJOR, ASYNC>;
     static constexpr int kStage = SL::kBytes + SR::kBytes;
-    static constexpr int kLds = 2 * kStage;
+    static constexpr int kLds = kStages * kStage;
 
     f4v acc[kFm][kFn];
 
@@ -178,14 +182,16 @@ struct TileProduct {
         return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) % kWavesN * WN;
     }
 
-    __device__ __forceinline__ void fragments(const char* at, int kk, s8v (&l)[kFm], s8v (&r)[kFn])
+    // The fragments of 32 k from 32 * half on, and their products.
+    s8v l[kFm], r[kFn];
+    __device__ __forceinline__ void fragments(const char* at, int half)
     {
 #pragma unroll
-        for (int j = 0; j < kFn; ++j) r[j] = SR::fragment(at + SL::kBytes, wave_n() + 16 * j, kk);
+        for (int j = 0; j < kFn; ++j) r[j] = SR::fragment(at + SL::kBytes, wave_n() + kMfma * j, half);
 #pragma unroll
-        for (int i = 0; i < kFm; ++i) l[i] = SL::fragment(at, wave_m() + 16 * i, kk);
+        for (int i = 0; i < kFm; ++i) l[i] = SL::fragment(at, wave_m() + kMfma * i, half);
     }
-    __device__ __forceinline__ void multiply(const s8v (&l)[kFm], const s8v (&r)[kFn])
+    __device__ __forceinline__ void multiply()
     {
 #pragma unroll
         for (int i = 0; i < kFm; ++i)
@@ -196,12 +202,75 @@ struct TileProduct {
     // The sums over all of K; every thread of the group, lds: kLds bytes.
     __device__ __forceinline__ void run(const Operand& lo, const Operand& ro, char* lds)
     {
-        SL sl;
-        SR sr;
 #pragma unroll
         for (int i = 0; i < kFm; ++i)
 #pragma unroll
             for (int j = 0; j < kFn; ++j) acc[i][j] = f4v{};
+        if constexpr (kTurns)
+            run_in_turns(lo, ro, lds);
+        else
+            run_in_step(lo, ro, lds);
+    }
+
+    // Two waves share a SIMD, one of each half of the group.  While one multiplies, the other takes its next fragments from LDS and
+    // starts loads, and a barrier changes their roles, so that the matrix cores have one wave's work at any time.  With the halves'
+    // phases counted through, the first half takes step s in phase 2s and multiplies it in 2s + 1, the second takes it in 2s + 1:
+    // step s's buffer is free from phase 2s + 2 on, where loads for step s + 4 go into it, and a step's loads have five phases.
+    __device__ __forceinline__ void run_in_turns(const Operand& lo, const Operand& ro, char* lds)
+    {
+        SL sl;
+        SR sr;
+        const int steps = (lo.k + kTileK - 1) / kTileK;
+        if (steps == 0) return;
+        auto load = [&](int t) {   // beyond the last step: zeros that nobody reads
+            char* to = lds + t % kStages * kStage;
+            sl.load(lo, t, to);
+            sr.load(ro, t, to + SL::kBytes);
+        };
+        constexpr int kEach = SL::kLoads + SR::kLoads;   // loads of a step
+        static_assert(2 * kEach == 8, "the waits below count them");
+        sl.begin(lo);
+        sr.begin(ro);
+        load(0);
+        load(1);
+        load(2);
+        wait_loads_8();
+        barrier();
+        const bool second = threadIdx.x >= kThreads / 2;
+        if (second) barrier();
+        for (int t = 0; t < steps; ++t) {
+            fragments(lds + t % kStages * kStage, 0);
+            load(t + 3);
+            wait_reads_and_loads_8();   // step t + 1 has arrived
+            barrier();
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            barrier();
+        }
+        if (!second) barrier();
+        wait_loads_0();
+    }
+
+    static __device__ __forceinline__ void barrier()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // all but the last 8 loads into LDS have arrived; also all reads of LDS
+    static __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+    static __device__ __forceinline__ void wait_loads_8() { asm volatile("s_waitcnt vmcnt(8)" ::: "memory"); }
+    static __device__ __forceinline__ void wait_loads_0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+    static __device__ __forceinline__ void wait_reads_and_loads_8() { asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory"); }
+
+    // Every wave reads a step's fragments and multiplies them, while the next step's operands are on their way.
+    __device__ __forceinline__ void run_in_step(const Operand& lo, const Operand& ro, char* lds)
+    {
+        SL sl;
+        SR sr;
         const int steps = (lo.k + kTileK - 1) / kTileK;
         if (steps == 0) return;
         sl.begin(lo);
@@ -219,28 +288,53 @@ struct TileProduct {
                 sr.load(ro, t + 1, to + SL::kBytes);
             }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                s8v l[kFm], r[kFn];
-                fragments(at, kk, l, r);
-                multiply(l, r);
+            for (int half = 0; half < 2; ++half) {
+                fragments(at, half);
+                multiply();
             }
             if (t + 1 < steps) {
                 sl.store(to);
                 sr.store(to + SL::kBytes);
             }
+            wait_reads();   // they have left the buffer that the next step's loads go into
             __syncthreads();
         }
     }
 
-    // f(row, column, four sums of the row from the column on) for all of the lane's places in the tile.
-    template <class F>
-    __device__ __forceinline__ void each(F&& f) const
+    // The tile's sums by way of LDS (the buffers that run() has left), so that a wave meets whole lines of the result:
+    // direct: f(row, column, four sums of the row from the column on); turned: g(row, column, four sums of the column from the
+    // row on).  Every thread of the group.
+    template <class F, class G>
+    __device__ __forceinline__ void finish(char* lds, bool direct, F&& f, bool turned, G&& g) const
     {
+        constexpr int kRows = 2 * kMfma, kLd = WN + 4;   // a turn's rows; 4 floats more keep the rows of a write in different banks
+        static_assert(kRows * kLd * 4 * (kThreads / 64) <= kLds, "every wave has its part of the buffers");
         const int lane = static_cast<int>(threadIdx.x) & 63;
+        float* mine = reinterpret_cast<float*>(lds) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * (kRows * kLd);
+        __syncthreads();   // the last fragments have left the buffers
 #pragma unroll
-        for (int i = 0; i < kFm; ++i)
+        for (int h = 0; h < WM / kRows; ++h) {
 #pragma unroll
-            for (int j = 0; j < kFn; ++j) f(wave_m() + 16 * i + (lane & 15), wave_n() + 16 * j + 4 * (lane >> 4), acc[i][j]);
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < kFn; ++j)
+                    *reinterpret_cast<f4v*>(mine + (16 * i + (lane & 15)) * kLd + 16 * j + 4 * (lane >> 4)) = acc[2 * h + i][j];
+            if (direct) {
+#pragma unroll 4
+                for (int q = lane; q < kRows * WN / 4; q += 64) {
+                    const int row = q / (WN / 4), col = q % (WN / 4) * 4;
+                    f(wave_m() + kRows * h + row, wave_n() + col, *reinterpret_cast<const f4v*>(mine + row * kLd + col));
+                }
+            }
+            if (turned) {
+#pragma unroll 4
+                for (int q = lane; q < kRows / 4 * WN; q += 64) {
+                    const int col = q / (kRows / 4), row = q % (kRows / 4) * 4;
+                    const float* at = mine + row * kLd + col;
+                    g(wave_m() + kRows * h + row, wave_n() + col, f4v{at[0], at[kLd], at[2 * kLd], at[3 * kLd]});
+                }
+            }
+        }
     }
 };
 

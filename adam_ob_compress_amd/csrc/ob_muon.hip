@@ -162,27 +162,27 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_product(Muo
     _Float16* to = reinterpret_cast<_Float16*>(c.half + (PRODUCT == MUON_GRAM ? mt.a : PRODUCT == MUON_POLY ? mt.b : mt.x[~turn & 1]));
     const int64_t ld = PRODUCT == MUON_STEP ? mt.k : mt.r;
     const int cols = PRODUCT == MUON_STEP ? mt.k : mt.r;
-    tile.each([&](int r, int col, f4v s) {
-        const int i = m0 + r, j = n0 + col;
-        if (i >= mt.r || j >= cols) return;   // both sides are multiples of 8
+    // four elements of the result, with what is added to the sums
+    auto value = [&](int64_t at, f4v s) {
         h4v h;
         if constexpr (PRODUCT == MUON_GRAM) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(s[e] * kGram);
         } else {
-            const h4v old = *reinterpret_cast<const h4v*>(from + i * ld + j);
+            const h4v old = *reinterpret_cast<const h4v*>(from + at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float o = static_cast<float>(old[e]);
                 h[e] = static_cast<_Float16>(PRODUCT == MUON_POLY ? fmaf(kC * kUp, s[e], kB * o) : fmaf(kUp, s[e], kA * o));
             }
         }
-        *reinterpret_cast<h4v*>(to + i * ld + j) = h;
-        if (PRODUCT != MUON_STEP && tl.i != tl.j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[(j + e) * ld + i] = h[e];
-        }
-    });
+        *reinterpret_cast<h4v*>(to + at) = h;
+    };
+    // both sides are multiples of 8; A is symmetric, and so is what is added to the turned sums
+    tile.finish(
+        lds, true, [&](int r, int col, f4v s) { if (m0 + r < mt.r && n0 + col < cols) value((m0 + r) * ld + n0 + col, s); },
+        PRODUCT != MUON_STEP && tl.i != tl.j,
+        [&](int r, int col, f4v s) { if (m0 + r < mt.r && n0 + col < cols) value((n0 + col) * ld + m0 + r, s); });
 }
 
 // The last X and the update.
@@ -211,33 +211,47 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_last(MuonCa
     const _Float16* from = reinterpret_cast<const _Float16*>(c.half + mt.x[turn & 1]);
     float* master = kMaster ? c.master + mt.state : nullptr;
     const u4 none{};
-    auto update = [&](float old, float x) { return fmaf(-l, fmaf(d, old, sx * x), old); };
-    auto one = [&](int64_t at, float x) {
-        const float now = update(kMaster ? master[at] : load_any1<D>(p, mt.elem + at), x);
-        if (kMaster) master[at] = now;
-        store_any1<D, false>(p, mt.elem + at, now, 0);
-    };
-    tile.each([&](int r, int col, f4v s) {
-        const int i = m0 + r, j = n0 + col;
-        if (i >= rows || j >= cols) return;
-        const h4v old = *reinterpret_cast<const h4v*>(from + static_cast<int64_t>(i) * mt.k + j);
-        f4 x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmaf(kUp, s[e], kA * static_cast<float>(old[e]));
-        if (!tall && j + 4 <= cols) {
-            const int64_t at = static_cast<int64_t>(i) * mt.cols + j;
+    auto update = [&](float was, float x) { return fmaf(-l, fmaf(d, was, sx * x), was); };
+    // four parameters behind each other, `left` of them there
+    auto four = [&](int64_t at, f4 x, int left) {
+        if (left >= 4) {
             const f4 was = kMaster ? load4u(master, at) : load_any4<D>(p, mt.elem + at);
             f4 now;
 #pragma unroll
             for (int e = 0; e < 4; ++e) now[e] = update(was[e], x[e]);
             if (kMaster) *reinterpret_cast<f4e*>(master + at) = now;
             store_any4<D, false>(p, mt.elem + at, now, none);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (j + e < cols) one(tall ? static_cast<int64_t>(j + e) * mt.cols + i : static_cast<int64_t>(i) * mt.cols + j + e, x[e]);
+            return;
         }
-    });
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+            if (e >= left) continue;
+            const float now = update(kMaster ? master[at + e] : load_any1<D>(p, mt.elem + at + e), x[e]);
+            if (kMaster) master[at + e] = now;
+            store_any1<D, false>(p, mt.elem + at + e, now, 0);
+        }
+    };
+    tile.finish(
+        lds, !tall,
+        [&](int r, int col, f4v s) {
+            const int i = m0 + r, j = n0 + col;
+            if (i >= rows || j >= cols) return;
+            const h4v old = *reinterpret_cast<const h4v*>(from + static_cast<int64_t>(i) * mt.k + j);
+            f4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = fmaf(kUp, s[e], kA * static_cast<float>(old[e]));
+            four(static_cast<int64_t>(i) * mt.cols + j, x, cols - j);
+        },
+        tall,
+        [&](int r, int col, f4v s) {
+            const int i = m0 + r, j = n0 + col, left = rows - i;
+            if (left <= 0 || j >= cols) return;
+            f4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)   // rows up to a multiple of 8 are there
+                x[e] = fmaf(kUp, s[e], kA * static_cast<float>(from[static_cast<int64_t>(i + e) * mt.k + j]));
+            four(static_cast<int64_t>(j) * mt.cols + i, x, left);
+        });
 }
 
 template <int TM, int WM, int WN>
