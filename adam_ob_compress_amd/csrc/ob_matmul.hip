@@ -68,8 +68,24 @@ __device__ __forceinline__ void store_row4(void* p, int64_t i, f4 x, int left)
         if (e < left) store_any1<D, false>(p, i + e, x[e], 0);
 }
 
-template <int D, class P>
-__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
+// Four elements of D from their sums.  WHOLE: all four are there.
+template <int D, bool WHOLE>
+__device__ __forceinline__ void put4(const ProductArgs& p, const char* c, char* d, int64_t ci, int64_t di, f4v sum, int left)
+{
+    f4 x;
+    if (p.beta != 0.0f) {
+        const f4 y = load_row4<D>(c, ci, WHOLE ? 4 : left);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
+    }
+    store_row4<D>(d, di, x, WHOLE ? 4 : left);
+}
+
+template <int D, bool WHOLE, class P>
+__device__ __forceinline__ void finish_part(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
 {
     constexpr int64_t kBytes = D == 0 ? 4 : 2;
     const char* c = static_cast<const char*>(p.c) + batch * p.batch_c * kBytes;
@@ -77,33 +93,23 @@ __device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char
     tile.finish(
         lds, true,
         [&](int r, int col, f4v sum) {
-            const int i = m0 + r, j = n0 + col, left = p.n - j;
-            if (i >= p.m || left <= 0) return;
-            f4 x;
-            if (p.beta != 0.0f) {
-                const f4 y = load_row4<D>(c, i * p.ldc + j, left);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
-            }
-            store_row4<D>(d, i * p.ldd + j, x, left);
+            const int64_t i = m0 + r, j = n0 + col;
+            if (WHOLE || (i < p.m && j < p.n)) put4<D, WHOLE>(p, c, d, i * p.ldc + j, i * p.ldd + j, sum, p.n - static_cast<int>(j));
         },
         mirror,
-        [&](int r, int col, f4v sum) {   // above the diagonal, with C's rows below it
-            const int i = m0 + r, j = n0 + col, left = p.m - i;
-            if (j >= p.n || left <= 0) return;
-            f4 x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
-            if (p.beta != 0.0f) {
-                const f4 y = load_row4<D>(c, j * p.ldc + i, left);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
-            }
-            store_row4<D>(d, j * p.ldd + i, x, left);
+        [&](int r, int col, f4v sum) {   // above the diagonal, with C's rows there
+            const int64_t i = m0 + r, j = n0 + col;
+            if (WHOLE || (i < p.m && j < p.n)) put4<D, WHOLE>(p, c, d, j * p.ldc + i, j * p.ldd + i, sum, p.m - static_cast<int>(i));
         });
+}
+
+template <int D, int TM, class P>
+__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
+{
+    if (p.m - m0 >= TM && p.n - n0 >= TM)
+        finish_part<D, true>(p, tile, lds, batch, m0, n0, mirror);
+    else
+        finish_part<D, false>(p, tile, lds, batch, m0, n0, mirror);
 }
 
 template <int TM, int WM, int WN, bool AK, bool BK, bool CHUNKS>
@@ -111,20 +117,22 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_product(ProductA
 {
     using P = TileProduct<TM, TM, WM, WN, OB_MM_BF16 != 0, AK, BK, CHUNKS>;
     __shared__ __attribute__((aligned(16))) char lds[P::kLds];
-    const int64_t t = p.first + by_xcd(blockIdx.x, gridDim.x), batch = t / p.tiles;
+    const int64_t t = p.first + by_xcd(blockIdx.x, gridDim.x), q = t / p.tiles;
     int ti, tj;
-    tile_at(p, t - batch * p.tiles, ti, tj);
-    const int m0 = ti * TM, n0 = tj * TM;
+    tile_at(p, t - q * p.tiles, ti, tj);
+    // the same in all lanes, which the divisions and roots hide: addresses stay in scalar registers
+    const int64_t batch = __builtin_amdgcn_readfirstlane(static_cast<int>(q));
+    const int m0 = __builtin_amdgcn_readfirstlane(ti) * TM, n0 = __builtin_amdgcn_readfirstlane(tj) * TM;
     P tile;
     tile.run(Operand{p.a + batch * p.batch_a + (AK ? m0 * p.lda : m0), p.lda, p.m - m0, p.k},
              Operand{p.b + batch * p.batch_b + (BK ? n0 * p.ldb : n0), p.ldb, p.n - n0, p.k}, lds);
-    const bool mirror = p.symmetric && ti != tj;
+    const bool mirror = p.symmetric && m0 != n0;
     if (p.out_type == OB_F32)
-        finish<0>(p, tile, lds, batch, m0, n0, mirror);
+        finish<0, TM>(p, tile, lds, batch, m0, n0, mirror);
     else if (p.out_type == OB_BF16)
-        finish<1>(p, tile, lds, batch, m0, n0, mirror);
+        finish<1, TM>(p, tile, lds, batch, m0, n0, mirror);
     else
-        finish<2>(p, tile, lds, batch, m0, n0, mirror);
+        finish<2, TM>(p, tile, lds, batch, m0, n0, mirror);
 }
 
 template <int TM, int WM, int WN, bool CHUNKS>

@@ -320,16 +320,16 @@ struct TileProduct {
                 for (int j = 0; j < kFn; ++j)
                     *reinterpret_cast<f4v*>(mine + (16 * i + (lane & 15)) * kLd + 16 * j + 4 * (lane >> 4)) = acc[2 * h + i][j];
             if (direct) {
-#pragma unroll 4
-                for (int q = lane; q < kRows * WN / 4; q += 64) {
-                    const int row = q / (WN / 4), col = q % (WN / 4) * 4;
+#pragma unroll
+                for (int k = 0; k < kRows * WN / 256; ++k) {
+                    const int q = lane + 64 * k, row = q / (WN / 4), col = q % (WN / 4) * 4;
                     f(wave_m() + kRows * h + row, wave_n() + col, *reinterpret_cast<const f4v*>(mine + row * kLd + col));
                 }
             }
             if (turned) {
-#pragma unroll 4
-                for (int q = lane; q < kRows / 4 * WN; q += 64) {
-                    const int col = q / (kRows / 4), row = q % (kRows / 4) * 4;
+#pragma unroll
+                for (int k = 0; k < kRows * WN / 256; ++k) {
+                    const int q = lane + 64 * k, col = q / (kRows / 4), row = q % (kRows / 4) * 4;
                     const float* at = mine + row * kLd + col;
                     g(wave_m() + kRows * h + row, wave_n() + col, f4v{at[0], at[kLd], at[2 * kLd], at[3 * kLd]});
                 }

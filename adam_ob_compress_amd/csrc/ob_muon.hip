@@ -128,11 +128,14 @@ __global__ __launch_bounds__(kListBlock) void k_muon_write(MuonCall c, ListPtrs 
 
 typedef _Float16 h4v __attribute__((ext_vector_type(4)));
 
+// The place of X in an iteration (both are loaded: an index would move the whole description out of the scalar registers).
+__device__ __forceinline__ int64_t x_of(const MuonMatrix& mt, int turn) { return turn & 1 ? mt.x[1] : mt.x[0]; }
+
 // The tile's sums for a product: rows from m0, columns from n0 on.
 template <int PRODUCT, class P>
 __device__ __forceinline__ void muon_sums(P& tile, const MuonCall& c, const MuonMatrix& mt, int turn, int m0, int n0, char* lds)
 {
-    const uint16_t* x = c.half + mt.x[turn & 1];
+    const uint16_t* x = c.half + x_of(mt, turn);
     if constexpr (PRODUCT == MUON_GRAM)
         tile.run(Operand{x + static_cast<int64_t>(m0) * mt.k, mt.k, mt.r - m0, mt.k},
                  Operand{x + static_cast<int64_t>(n0) * mt.k, mt.k, mt.r - n0, mt.k}, lds);
@@ -158,8 +161,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_product(Muo
     const int m0 = tl.i * TM, n0 = tl.j * TM;
     P tile;
     muon_sums<PRODUCT>(tile, c, mt, turn, m0, n0, lds);
-    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + (PRODUCT == MUON_STEP ? mt.x[turn & 1] : mt.a));
-    _Float16* to = reinterpret_cast<_Float16*>(c.half + (PRODUCT == MUON_GRAM ? mt.a : PRODUCT == MUON_POLY ? mt.b : mt.x[~turn & 1]));
+    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + (PRODUCT == MUON_STEP ? x_of(mt, turn) : mt.a));
+    _Float16* to = reinterpret_cast<_Float16*>(c.half + (PRODUCT == MUON_GRAM ? mt.a : PRODUCT == MUON_POLY ? mt.b : x_of(mt, turn + 1)));
     const int64_t ld = PRODUCT == MUON_STEP ? mt.k : mt.r;
     const int cols = PRODUCT == MUON_STEP ? mt.k : mt.r;
     // four elements of the result, with what is added to the sums
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_last(MuonCa
     const float d = static_cast<float>(c.wd * static_cast<double>(mt.wd_mult)), sx = static_cast<float>(scale / kScaleX);
     const bool tall = mt.rows > mt.cols;
     const int rows = tall ? mt.cols : mt.rows, cols = tall ? mt.rows : mt.cols;   // of X, without what was rounded up
-    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + mt.x[turn & 1]);
+    const _Float16* from = reinterpret_cast<const _Float16*>(c.half + x_of(mt, turn));
     float* master = kMaster ? c.master + mt.state : nullptr;
     const u4 none{};
     auto update = [&](float was, float x) { return fmaf(-l, fmaf(d, was, sx * x), was); };
