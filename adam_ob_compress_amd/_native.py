@@ -89,7 +89,8 @@ class ob_product(ctypes.Structure):
                 ("c", ctypes.c_void_p), ("c_row", ctypes.c_int64), ("c_batch", ctypes.c_int64),
                 ("d", ctypes.c_void_p), ("d_row", ctypes.c_int64), ("d_batch", ctypes.c_int64),
                 ("in_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("alpha", ctypes.c_float),
-                ("beta", ctypes.c_float), ("symmetric", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("beta", ctypes.c_float), ("symmetric", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p)]
 
 
 _lib = None
@@ -151,6 +152,7 @@ def lib() -> ctypes.CDLL:
         "ob_muon_step": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_muon_hparams), P, P]),
         "ob_muon_check": (I32, [P, P, P, P, P, P, ctypes.POINTER(ob_muon_hparams), P]),
         "ob_matmul": (I32, [ctypes.POINTER(ob_product), P]),
+        "ob_matmul_workspace": (I64, [ctypes.POINTER(ob_product)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -835,17 +837,23 @@ def _refuse_product(a, b, out, c):
     raise ValueError("the tensors are refused")
 
 
-def ob_matmul(a, b, out, alpha=1.0, beta=0.0, c=None, symmetric=False, stream=None):
+def ob_matmul(a, b, out, alpha=1.0, beta=0.0, c=None, symmetric=False, stream=None, workspace=None):
     """out = alpha * a @ b + beta * c for matrices or batches of them: a, b bfloat16 or float16, either by rows or transposed
     views; out and c (which may be out) float32, bfloat16 or float16, by rows.  symmetric: the caller knows that a @ b and
-    c are; what is below the diagonal is computed and written above it too."""
+    c are; what is below the diagonal is computed and written above it too.  workspace: a byte tensor, or None to take what
+    a product with few tiles and a long sum has use for (at most some 100 MB) from torch's allocator."""
     if stream is None:
         index = out.get_device() if isinstance(out, torch.Tensor) else -1
-        s = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
+        code = _obtorch().matmul(a, b, out, c, alpha, beta, symmetric, torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0,
+                                 workspace)
     else:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    code = _obtorch().matmul(a, b, out, c, alpha, beta, symmetric, s)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), out.device if isinstance(out, torch.Tensor) else None)
+        with torch.cuda.stream(stream):   # so that the workspace is the stream's
+            code = _obtorch().matmul(a, b, out, c, alpha, beta, symmetric, stream.cuda_stream, workspace)
     if code > 0:
         raise ObError(code, "ob_matmul")
     if code < 0:
+        if (-code - 1) >> 32 == 4:
+            raise ValueError("workspace must be a contiguous byte tensor on the tensors' device, as large as the product has use for")
         _refuse_product(a, b, out, c)

@@ -22,13 +22,15 @@ struct ProductArgs {
     int32_t tiles_m, tiles_n;
     int64_t tiles;        // per matrix
     int64_t first;        // of the launch: its first tile, counted over the whole batch
+    int64_t full;         // tiles of the launch that one work group takes each; then `split` work groups for each of the rest
+    int32_t split;
+    float* parts;         // the rest's partial sums: a tile's squared side of floats for each work group
 };
 
-enum { TILE_256 = 0, TILE_128 = 1, TILE_64 = 2 };
-constexpr int kTileSize[] = {256, 128, 64};
-
-// Tiles [first, first + count) with the kernel for these layouts; chunks: both operands in 16-byte chunks.
+// `count` work groups of the kernel for these layouts; size: place in kTileSize; chunks: both operands in 16-byte chunks.
 template <bool BF16>
-hipError_t launch_product(const ProductArgs& p, int tile, bool a_kmajor, bool b_kmajor, bool chunks, int64_t count, hipStream_t s);
+hipError_t launch_product(const ProductArgs& p, int size, bool a_kmajor, bool b_kmajor, bool chunks, int64_t count, hipStream_t s);
+// The `rest` tiles behind the full ones from their partial sums.
+hipError_t launch_product_join(const ProductArgs& p, int size, int64_t rest, hipStream_t s);
 
 }  // namespace ob

@@ -85,7 +85,7 @@ __device__ __forceinline__ void put4(const ProductArgs& p, const char* c, char* 
 }
 
 template <int D, bool WHOLE, class P>
-__device__ __forceinline__ void finish_part(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
+__device__ __forceinline__ void finish_part(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror, int only)
 {
     constexpr int64_t kBytes = D == 0 ? 4 : 2;
     const char* c = static_cast<const char*>(p.c) + batch * p.batch_c * kBytes;
@@ -100,16 +100,41 @@ __device__ __forceinline__ void finish_part(const ProductArgs& p, const P& tile,
         [&](int r, int col, f4v sum) {   // above the diagonal, with C's rows there
             const int64_t i = m0 + r, j = n0 + col;
             if (WHOLE || (i < p.m && j < p.n)) put4<D, WHOLE>(p, c, d, j * p.ldc + i, j * p.ldd + i, sum, p.m - static_cast<int>(i));
-        });
+        },
+        only);
 }
 
 template <int D, int TM, class P>
-__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror)
+__device__ __forceinline__ void finish_as(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, int only)
 {
+    const bool mirror = p.symmetric && m0 != n0;
     if (p.m - m0 >= TM && p.n - n0 >= TM)
-        finish_part<D, true>(p, tile, lds, batch, m0, n0, mirror);
+        finish_part<D, true>(p, tile, lds, batch, m0, n0, mirror, only);
     else
-        finish_part<D, false>(p, tile, lds, batch, m0, n0, mirror);
+        finish_part<D, false>(p, tile, lds, batch, m0, n0, mirror, only);
+}
+
+template <int TM, class P>
+__device__ __forceinline__ void finish(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, int only)
+{
+    if (p.out_type == OB_F32)
+        finish_as<0, TM>(p, tile, lds, batch, m0, n0, only);
+    else if (p.out_type == OB_BF16)
+        finish_as<1, TM>(p, tile, lds, batch, m0, n0, only);
+    else
+        finish_as<2, TM>(p, tile, lds, batch, m0, n0, only);
+}
+
+// Matrix, first row and first column of the launch's tile t.  The same in all lanes, which divisions and roots hide: so told,
+// addresses stay in scalar registers.
+__device__ __forceinline__ void tile_place(const ProductArgs& p, int64_t t, int size, int64_t& batch, int& m0, int& n0)
+{
+    const int64_t q = (p.first + t) / p.tiles;
+    int ti, tj;
+    tile_at(p, p.first + t - q * p.tiles, ti, tj);
+    batch = __builtin_amdgcn_readfirstlane(static_cast<int>(q));
+    m0 = __builtin_amdgcn_readfirstlane(ti) * size;
+    n0 = __builtin_amdgcn_readfirstlane(tj) * size;
 }
 
 template <int TM, int WM, int WN, bool AK, bool BK, bool CHUNKS>
@@ -117,23 +142,53 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_product(ProductA
 {
     using P = TileProduct<TM, TM, WM, WN, OB_MM_BF16 != 0, AK, BK, CHUNKS>;
     __shared__ __attribute__((aligned(16))) char lds[P::kLds];
-    const int64_t t = p.first + by_xcd(blockIdx.x, gridDim.x), q = t / p.tiles;
-    int ti, tj;
-    tile_at(p, t - q * p.tiles, ti, tj);
-    // the same in all lanes, which the divisions and roots hide: addresses stay in scalar registers
-    const int64_t batch = __builtin_amdgcn_readfirstlane(static_cast<int>(q));
-    const int m0 = __builtin_amdgcn_readfirstlane(ti) * TM, n0 = __builtin_amdgcn_readfirstlane(tj) * TM;
+    const int64_t b = blockIdx.x;
+    const bool whole = b < p.full;
+    const int64_t q = whole ? 0 : by_xcd(b - p.full, gridDim.x - p.full);   // part of a tile
+    int64_t batch;
+    int m0, n0, k0 = 0, k = p.k;
+    tile_place(p, whole ? by_xcd(b, p.full) : p.full + q / p.split, TM, batch, m0, n0);
+    if (!whole) {
+        const int64_t steps = (k + P::kTileK - 1) / P::kTileK, part = q % p.split;
+        k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(steps * part / p.split) * P::kTileK);
+        const int64_t end = steps * (part + 1) / p.split * P::kTileK;
+        k = __builtin_amdgcn_readfirstlane(static_cast<int>(end < p.k ? end : p.k)) - k0;
+    }
     P tile;
-    tile.run(Operand{p.a + batch * p.batch_a + (AK ? m0 * p.lda : m0), p.lda, p.m - m0, p.k},
-             Operand{p.b + batch * p.batch_b + (BK ? n0 * p.ldb : n0), p.ldb, p.n - n0, p.k}, lds);
-    const bool mirror = p.symmetric && m0 != n0;
-    if (p.out_type == OB_F32)
-        finish<0, TM>(p, tile, lds, batch, m0, n0, mirror);
-    else if (p.out_type == OB_BF16)
-        finish<1, TM>(p, tile, lds, batch, m0, n0, mirror);
+    tile.run(Operand{p.a + batch * p.batch_a + (AK ? m0 * p.lda + k0 : k0 * p.lda + m0), p.lda, p.m - m0, k},
+             Operand{p.b + batch * p.batch_b + (BK ? n0 * p.ldb + k0 : k0 * p.ldb + n0), p.ldb, p.n - n0, k}, lds);
+    if (whole)
+        finish<TM>(p, tile, lds, batch, m0, n0, -1);
     else
-        finish<2, TM>(p, tile, lds, batch, m0, n0, mirror);
+        tile.put(p.parts + q * P::kFloats);
 }
+
+#if OB_MM_BF16 == 0
+// A turn (32 rows of each wave) of one of the tiles that several work groups shared: their sums in order.
+template <int TM, int WM, int WN>
+__global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_product_join(ProductArgs p)
+{
+    using P = TileProduct<TM, TM, WM, WN, false, true, true, true>;
+    __shared__ __attribute__((aligned(16))) char lds[P::kLdsOut];
+    const int only = static_cast<int>(blockIdx.x % P::kTurnsOut);
+    const int64_t t = blockIdx.x / P::kTurnsOut;
+    int64_t batch;
+    int m0, n0;
+    tile_place(p, p.full + t, TM, batch, m0, n0);
+    P tile;
+    tile.clear();
+    for (int s = 0; s < p.split; ++s) tile.add(p.parts + (t * p.split + s) * P::kFloats, only);
+    finish<TM>(p, tile, lds, batch, m0, n0, only);
+}
+
+template <int TM, int WM, int WN>
+hipError_t join(const ProductArgs& p, int64_t rest, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_product_join<TM, WM, WN>), dim3(static_cast<unsigned>(rest * (WM / 32))), dim3(64 * (TM / WM) * (TM / WN)), 0,
+                       s, p);
+    return hipGetLastError();
+}
+#endif
 
 template <int TM, int WM, int WN, bool CHUNKS>
 hipError_t launch(const ProductArgs& p, bool ak, bool bk, int64_t count, hipStream_t s)
@@ -153,13 +208,20 @@ hipError_t launch(const ProductArgs& p, bool ak, bool bk, int64_t count, hipStre
 }  // namespace
 
 template <bool BF16>
-hipError_t launch_product(const ProductArgs& p, int tile, bool ak, bool bk, bool chunks, int64_t count, hipStream_t s)
+hipError_t launch_product(const ProductArgs& p, int size, bool ak, bool bk, bool chunks, int64_t count, hipStream_t s)
 {
-    if (tile == TILE_256) return chunks ? launch<256, 128, 64, true>(p, ak, bk, count, s) : hipErrorInvalidValue;
-    if (tile == TILE_128) return chunks ? launch<128, 64, 64, true>(p, ak, bk, count, s) : launch<128, 64, 64, false>(p, ak, bk, count, s);
+    if (size == 0) return chunks ? launch<256, 128, 64, true>(p, ak, bk, count, s) : hipErrorInvalidValue;
+    if (size == 1) return chunks ? launch<128, 64, 64, true>(p, ak, bk, count, s) : launch<128, 64, 64, false>(p, ak, bk, count, s);
     return chunks ? launch<64, 32, 32, true>(p, ak, bk, count, s) : launch<64, 32, 32, false>(p, ak, bk, count, s);
 }
 
 template hipError_t launch_product<OB_MM_BF16 != 0>(const ProductArgs&, int, bool, bool, bool, int64_t, hipStream_t);
+
+#if OB_MM_BF16 == 0
+hipError_t launch_product_join(const ProductArgs& p, int size, int64_t rest, hipStream_t s)
+{
+    return size == 0 ? join<256, 128, 64>(p, rest, s) : size == 1 ? join<128, 64, 64>(p, rest, s) : join<64, 32, 32>(p, rest, s);
+}
+#endif
 
 }  // namespace ob

@@ -169,6 +169,7 @@ struct TileProduct {
     using SR = Stage<TN, kTileK, kThreads, R_KMAJOR, ASYNC>;
     static constexpr int kStage = SL::kBytes + SR::kBytes;
     static constexpr int kLds = kStages * kStage;
+    static constexpr int kEach = SL::kLoads + SR::kLoads;   // loads of a step
 
     f4v acc[kFm][kFn];
 
@@ -199,13 +200,18 @@ struct TileProduct {
             for (int j = 0; j < kFn; ++j) acc[i][j] = mfma<BF16>(r[j], l[i], acc[i][j]);
     }
 
-    // The sums over all of K; every thread of the group, lds: kLds bytes.
-    __device__ __forceinline__ void run(const Operand& lo, const Operand& ro, char* lds)
+    __device__ __forceinline__ void clear()
     {
 #pragma unroll
         for (int i = 0; i < kFm; ++i)
 #pragma unroll
             for (int j = 0; j < kFn; ++j) acc[i][j] = f4v{};
+    }
+
+    // The sums over all of K; every thread of the group, lds: kLds bytes.
+    __device__ __forceinline__ void run(const Operand& lo, const Operand& ro, char* lds)
+    {
+        clear();
         if constexpr (kTurns)
             run_in_turns(lo, ro, lds);
         else
@@ -227,21 +233,20 @@ struct TileProduct {
             sl.load(lo, t, to);
             sr.load(ro, t, to + SL::kBytes);
         };
-        constexpr int kEach = SL::kLoads + SR::kLoads;   // loads of a step
-        static_assert(2 * kEach == 8, "the waits below count them");
         sl.begin(lo);
         sr.begin(ro);
         load(0);
         load(1);
         load(2);
-        wait_loads_8();
+        wait_loads<2 * kEach>();
         barrier();
         const bool second = threadIdx.x >= kThreads / 2;
         if (second) barrier();
         for (int t = 0; t < steps; ++t) {
             fragments(lds + t % kStages * kStage, 0);
             load(t + 3);
-            wait_reads_and_loads_8();   // step t + 1 has arrived
+            wait_loads<2 * kEach>();   // step t + 1 has arrived
+            wait_reads();
             barrier();
             __builtin_amdgcn_s_setprio(1);
             multiply();
@@ -249,7 +254,7 @@ struct TileProduct {
             barrier();
         }
         if (!second) barrier();
-        wait_loads_0();
+        wait_loads<0>();
     }
 
     static __device__ __forceinline__ void barrier()
@@ -260,11 +265,13 @@ struct TileProduct {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     }
-    // all but the last 8 loads into LDS have arrived; also all reads of LDS
+    // all reads of LDS have arrived; all loads into LDS but the last N have
     static __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-    static __device__ __forceinline__ void wait_loads_8() { asm volatile("s_waitcnt vmcnt(8)" ::: "memory"); }
-    static __device__ __forceinline__ void wait_loads_0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-    static __device__ __forceinline__ void wait_reads_and_loads_8() { asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory"); }
+    template <int N>
+    static __device__ __forceinline__ void wait_loads()
+    {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    }
 
     // Every wave reads a step's fragments and multiplies them, while the next step's operands are on their way.
     __device__ __forceinline__ void run_in_step(const Operand& lo, const Operand& ro, char* lds)
@@ -301,19 +308,43 @@ struct TileProduct {
         }
     }
 
+    // The sums as they lie in registers, to memory and added from there (of one turn of finish()).
+    static constexpr int kFloats = TM * TN;
+    __device__ __forceinline__ void put(float* to) const
+    {
+#pragma unroll
+        for (int i = 0; i < kFm; ++i)
+#pragma unroll
+            for (int j = 0; j < kFn; ++j)
+                *reinterpret_cast<f4v*>(to + ((i * kFn + j) * kThreads + static_cast<int>(threadIdx.x)) * 4) = acc[i][j];
+    }
+    __device__ __forceinline__ void add(const float* from, int only)
+    {
+#pragma unroll
+        for (int i = 0; i < kFm; ++i) {
+            if (i / 2 != only) continue;
+#pragma unroll
+            for (int j = 0; j < kFn; ++j)
+                acc[i][j] += *reinterpret_cast<const f4v*>(from + ((i * kFn + j) * kThreads + static_cast<int>(threadIdx.x)) * 4);
+        }
+    }
+
     // The tile's sums by way of LDS (the buffers that run() has left), so that a wave meets whole lines of the result:
     // direct: f(row, column, four sums of the row from the column on); turned: g(row, column, four sums of the column from the
-    // row on).  Every thread of the group.
+    // row on).  Every thread of the group.  only: the turn of kRows rows of each wave that is wanted (-1: all).
+    static constexpr int kRows = 2 * kMfma, kTurnsOut = WM / kRows;   // rows of a turn, turns
+    static constexpr int kLdsOut = kRows * (WN + 4) * 4 * (kThreads / 64);
     template <class F, class G>
-    __device__ __forceinline__ void finish(char* lds, bool direct, F&& f, bool turned, G&& g) const
+    __device__ __forceinline__ void finish(char* lds, bool direct, F&& f, bool turned, G&& g, int only = -1) const
     {
-        constexpr int kRows = 2 * kMfma, kLd = WN + 4;   // a turn's rows; 4 floats more keep the rows of a write in different banks
-        static_assert(kRows * kLd * 4 * (kThreads / 64) <= kLds, "every wave has its part of the buffers");
+        constexpr int kLd = WN + 4;   // 4 floats more keep the rows of a write in different banks
+        static_assert(kLdsOut <= kLds, "every wave has its part of the buffers");
         const int lane = static_cast<int>(threadIdx.x) & 63;
         float* mine = reinterpret_cast<float*>(lds) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * (kRows * kLd);
         __syncthreads();   // the last fragments have left the buffers
 #pragma unroll
-        for (int h = 0; h < WM / kRows; ++h) {
+        for (int h = 0; h < kTurnsOut; ++h) {
+            if (only >= 0 && h != only) continue;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll

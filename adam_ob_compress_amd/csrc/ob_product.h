@@ -49,7 +49,7 @@ inline ob_status check_product(const ob_product* p)
     // D's elements must not overlap
     if (p->m > 1 && p->d_row < p->n) return OB_ERR_ARG;
     if (p->batch > 1 && p->d_batch < (p->m - 1) * p->d_row + p->n) return OB_ERR_ARG;
-    if (!product_aligned(p->d, out)) return OB_ERR_ALIGN;
+    if (!product_aligned(p->d, out) || !product_aligned(p->workspace, 16)) return OB_ERR_ALIGN;
     if (p->beta != 0.0f) {
         if (!product_stride(p->m, p->c_row) || !product_stride(p->batch, p->c_batch)) return OB_ERR_ARG;
         if (!product_aligned(p->c, out)) return OB_ERR_ALIGN;
@@ -85,6 +85,81 @@ inline int64_t product_tiles(int64_t m, int64_t n, int64_t tile, bool symmetric)
 {
     const int64_t a = (m + tile - 1) / tile, b = (n + tile - 1) / tile;
     return symmetric ? a * (a + 1) / 2 : a * b;
+}
+
+// How a launch's tiles are given to work groups: `full` of them to one each, and the `rest`, which would leave compute units
+// idle, to `split` each, whose parts of K are added by another launch.
+struct TileShares {
+    int64_t full, rest;
+    int32_t split;      // 1: rest is 0
+};
+
+// What the choice goes by: sides of the tiles; how many work groups of each a compute unit holds (by LDS); the card's rate, in
+// operations a microsecond, with one, two, ... of them on each unit; microseconds that a tile takes besides its sums.  (8192^3,
+// 4096^3 and fractions of a round, fp16.)
+constexpr int kTileSizes = 3;
+constexpr int64_t kTileSize[kTileSizes] = {256, 128, 64};
+constexpr int kTileHeld[kTileSizes] = {1, 2, 4};
+constexpr double kTileRate[kTileSizes][4] = {{1200e6}, {650e6, 950e6}, {250e6, 450e6, 580e6, 680e6}};
+constexpr double kTileExtra[kTileSizes] = {7.0, 5.0, 4.0};
+constexpr int64_t kUnits = 256;
+constexpr double kJoin = 5.0, kJoinBytes = 4e6;   // microseconds of the second launch, bytes a microsecond there
+constexpr int32_t kMostSplit = 16;
+constexpr int64_t kLeastSteps = 8;                // of 32 k that a part has
+
+// Microseconds for `tiles` tiles with sums over k.
+inline double tile_round(int size, int64_t tiles, double k)
+{
+    const int64_t slots = kUnits * kTileHeld[size];
+    const double work = 2.0 * static_cast<double>(kTileSize[size] * kTileSize[size]) * k;
+    const int64_t rounds = tiles / slots, left = tiles % slots;
+    double t = static_cast<double>(rounds) * (work * static_cast<double>(slots) / kTileRate[size][kTileHeld[size] - 1] + kTileExtra[size]);
+    if (left > 0) {
+        const int64_t n = (left + kUnits - 1) / kUnits;
+        t += work * static_cast<double>(n * kUnits) / kTileRate[size][n - 1] + kTileExtra[size];
+    }
+    return t;
+}
+
+// The best shares of `tiles` tiles, sums over k (the shortest, of those in a launch's last round) and their time.
+inline TileShares tile_shares(int size, int64_t tiles, int64_t k, bool may_split, double& us)
+{
+    TileShares best{tiles, 0, 1};
+    us = tile_round(size, tiles, static_cast<double>(k));
+    const int64_t rest = tiles % (kUnits * kTileHeld[size]);
+    if (!may_split || rest == 0) return best;
+    const double before = tile_round(size, tiles - rest, static_cast<double>(k));
+    for (int32_t s = 2; s <= kMostSplit && k / s >= 32 * kLeastSteps; ++s) {
+        const double bytes = 8.0 * static_cast<double>(rest * s * kTileSize[size] * kTileSize[size]);
+        const double t = before + tile_round(size, rest * s, static_cast<double>(k) / s) + kJoin + bytes / kJoinBytes;
+        if (t < us) {
+            us = t;
+            best = {tiles - rest, rest, s};
+        }
+    }
+    return best;
+}
+
+// The tile size and the shares that take the least time.  slow: operands by way of registers, for which there is no largest tile.
+struct ProductPlan {
+    int size;
+    TileShares shares;
+};
+inline ProductPlan plan_product(const ob_product& p, bool chunks, bool may_split)
+{
+    ProductPlan best{};
+    double least = -1.0;
+    for (int size = chunks ? 0 : 1; size < kTileSizes; ++size) {
+        const int64_t each = product_tiles(p.m, p.n, kTileSize[size], p.symmetric != 0);
+        if (each > INT64_MAX / p.batch) continue;
+        double us;
+        const TileShares s = tile_shares(size, each * p.batch, std::max<int64_t>(p.k, 1), may_split, us);
+        if (least < 0.0 || us < least) {
+            least = us;
+            best = {size, s};
+        }
+    }
+    return best;
 }
 
 }  // namespace ob

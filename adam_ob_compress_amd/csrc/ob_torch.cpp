@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Functions.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -356,10 +357,11 @@ int32_t type_of(const at::Tensor& t, int64_t where)
     }
 }
 
-// matmul(a, b, out, c or None, alpha, beta, symmetric, stream): a product on the tensors' device
+// matmul(a, b, out, c or None, alpha, beta, symmetric, stream, workspace or None): a product on the tensors' device; None: what
+// the product has use for is taken from torch's allocator, on the device's current stream
 PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
-    return guarded(n, 8, [&] {
+    return guarded(n, 9, [&] {
         const at::Tensor &a = matrix(args[0], 0), &b = matrix(args[1], 1), &d = matrix(args[2], 2);
         const at::Tensor* c = args[3] == Py_None ? nullptr : &matrix(args[3], 3);
         const int64_t dim = d.dim(), x = dim - 2, y = dim - 1;
@@ -408,6 +410,15 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n)
         hipStream_t s = stream_of(args[7]);
         if (PyErr_Occurred()) throw Bad{0, 0};
         const c10::DeviceGuard guard(d.device());
+        at::Tensor own;   // freed for what is enqueued after this call
+        if (const int64_t bytes = ob_matmul_workspace(&p)) {
+            if (args[8] != Py_None) {
+                p.workspace = room(args[8], bytes, d.get_device(), 4);
+            } else {
+                own = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(d.device()));
+                p.workspace = own.data_ptr();
+            }
+        }
         return status_of([&] { return ob_matmul(&p, s); });
     });
 }

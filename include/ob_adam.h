@@ -476,8 +476,10 @@ ob_status ob_clip_grads(ob_tensors list, const void* const* g, void* const* out,
  *             C is: what is below the diagonal is computed, and written above it too.
  * D may be C itself (same pointer and strides) and overlaps nothing else.  Zero extents give no work.
  * Extents are at most 2^31 - 1 - 256, offsets within a matrix and a batch below 2^60 elements; OB_ERR_ARG beyond.
- * Sums run in an order that depends on the extents, layouts and alignment alone.  Runs on the current device; allocates
- * nothing, synchronises nothing and records kernels only. */
+ * workspace: ob_matmul_workspace(product) bytes of device memory, 16-byte aligned, of any content, or NULL: with it, tiles that
+ * would not fill the card are shared by several work groups, which add their parts of K; calls that may overlap need their own.
+ * Sums run in an order that depends on the extents, layouts and alignment, and on whether there is a workspace, alone.  Runs on
+ * the current device; allocates nothing, synchronises nothing and records kernels only. */
 typedef struct {
     int64_t batch, m, n, k;
     const void* a;
@@ -492,8 +494,11 @@ typedef struct {
     float alpha, beta;       /* finite */
     int32_t symmetric;       /* 0 or 1 */
     int32_t reserved;        /* 0 */
+    void* workspace;         /* or NULL */
 } ob_product;
 
+/* Bytes of the workspace that this product (its workspace aside) has use for; 0: none, or ob_matmul would refuse it. */
+int64_t ob_matmul_workspace(const ob_product* product);
 ob_status ob_matmul(const ob_product* product, hipStream_t stream);
 
 /* ---- Muon over lists of matrices ----

@@ -101,6 +101,49 @@ def test_symmetric(m, k, layout, out):
     assert torch.equal(got, c)
 
 
+@pytest.mark.parametrize("layout", ["nn", "nt", "tn", "tt"])
+@pytest.mark.parametrize("m,n,k,batch", [(64, 64, 65536, 0), (40, 24, 40_000, 0), (300, 520, 20_008, 0), (257, 129, 9999, 0),
+                                         (512, 512, 8192, 3), (1100, 1030, 4096, 0), (4096, 4224, 1024, 0)])
+def test_long_sums_and_rests(m, n, k, batch, layout):
+    """Tiles that several work groups share: few tiles, or a rest behind full rounds; with and without a workspace, in place."""
+    gen = torch.Generator("cuda").manual_seed(k)
+    a = operand(gen, batch, m, k, torch.bfloat16, layout[0] == "t")
+    b = operand(gen, batch, k, n, torch.bfloat16, layout[1] == "t")
+    c = torch.randn(*a.shape[:-1], n, generator=gen, device="cuda")
+    out = torch.empty_like(c)
+    check(a, b, out, 0.5, 0.25, c)
+    room = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")   # of any content: NaN
+    again = c.clone()
+    ob.ob_matmul(a, b, again, alpha=0.5, beta=0.25, c=again, workspace=room)
+    assert torch.equal(out, again)
+    half = torch.empty_like(c, dtype=torch.float16)
+    check(a, b, half, 1.0, 0.0, None)
+    if m == 512:
+        check(a, a.transpose(1, 2), c[:, :, :m].contiguous(), 1.0, 0.0, None, symmetric=True)
+
+
+def test_shared_tiles_in_a_graph_and_on_a_stream():
+    gen = torch.Generator("cuda").manual_seed(6)
+    a, b = operand(gen, 0, 100, 30_000, torch.float16), operand(gen, 0, 30_000, 72, torch.float16)
+    want, out = torch.empty(100, 72, device="cuda"), torch.empty(100, 72, device="cuda")
+    side = torch.cuda.Stream()
+    ob.ob_matmul(a, b, want)
+    side.wait_stream(torch.cuda.current_stream())
+    ob.ob_matmul(a, b, out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(want, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ob.ob_matmul(a, b, out)
+    for k in range(3):
+        a.mul_(0.5)
+        g.replay()
+        ob.ob_matmul(a, b, want)
+        junk = torch.full((1 << 24,), 2.0 ** 100, device="cuda")   # what the allocator hands out between replays
+        torch.cuda.synchronize()
+        assert torch.equal(want, out) and bool((junk == 2.0 ** 100).all()), k
+
+
 def test_in_place_and_zero_extents():
     gen = torch.Generator("cuda").manual_seed(1)
     a, b = operand(gen, 0, 130, 70, torch.float16), operand(gen, 0, 70, 300, torch.float16)
@@ -209,4 +252,8 @@ def test_refusals():
         ob.ob_matmul(a, b[:, :4], out[:, :4], symmetric=True)
     with pytest.raises(ValueError, match="GPU"):
         ob.ob_matmul(a.cpu(), b, out)
+    long = torch.zeros(8, 1 << 16, device="cuda", dtype=torch.bfloat16)
+    for bad in (torch.zeros(16, device="cuda", dtype=torch.uint8), torch.zeros(1 << 26, device="cuda"), torch.zeros(1 << 26, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            ob.ob_matmul(long, long.t(), out, workspace=bad)
     assert not out.any()

@@ -21,8 +21,8 @@ def test_host_side_of_products(tmp_path):
 
 
 def test_layout_matches_the_header():
-    # 4 extents, A and B with three strides each, C and D with two, two types, two factors, two flags
-    assert ctypes.sizeof(ob.ob_product) == 8 * (4 + 4 + 4 + 3 + 3) + 6 * 4
+    # 4 extents, A and B with three strides each, C and D with two, two types, two factors, two flags, the workspace
+    assert ctypes.sizeof(ob.ob_product) == 8 * (4 + 4 + 4 + 3 + 3) + 6 * 4 + 8
     assert ob.ob_product.d.offset == 8 * 15 and ob.ob_product.alpha.offset == 8 * 18 + 8
 
 
