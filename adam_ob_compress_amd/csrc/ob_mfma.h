@@ -62,7 +62,8 @@ struct Stage {
     }
 
     u4v reg[ASYNC ? 1 : kLoads];
-    uint32_t off[ASYNC ? kLoads : 1];   // byte offsets of the thread's chunks from the step's first byte
+    uint32_t off[ASYNC ? kLoads : 1];         // ASYNC: byte offsets of the thread's chunks from the step's first byte
+    const uint16_t* at[ASYNC ? 1 : kLoads];   // else their addresses
 
     // place of the thread's chunk j: line and chunk in it
     static __device__ __forceinline__ void place(int j, int& line, int& chunk)
@@ -74,14 +75,15 @@ struct Stage {
 
     __device__ __forceinline__ void begin(const Operand& o)
     {
-        if constexpr (ASYNC) {
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                int line, chunk;
-                place(j, line, chunk);
-                const bool in = (K_MAJOR ? line : chunk * 8) < o.rows;
+        for (int j = 0; j < kLoads; ++j) {
+            int line, chunk;
+            place(j, line, chunk);
+            const bool in = (K_MAJOR ? line : chunk * 8) < o.rows;
+            if constexpr (ASYNC)
                 off[j] = in ? static_cast<uint32_t>(line * o.ld + chunk * 8) * 2u : kOutside;
-            }
+            else   // a row that is not there: another one, whose sums nobody stores
+                at[j] = o.p + (K_MAJOR ? (in ? line : 0) * o.ld + chunk * 8 : line * o.ld + (in ? chunk * 8 : 0));
         }
     }
 
@@ -89,9 +91,9 @@ struct Stage {
     __device__ __forceinline__ void load(const Operand& o, int t, char* to)
     {
         const int left = o.k - t * KT;   // k that there are from this step on
-        const uint16_t* base = o.p + (K_MAJOR ? static_cast<int64_t>(t) * KT : static_cast<int64_t>(t) * KT * o.ld);
+        const int64_t step = K_MAJOR ? static_cast<int64_t>(t) * KT : static_cast<int64_t>(t) * KT * o.ld;
         if constexpr (ASYNC) {
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, left > 0 ? kInside : 0, 0x00027000);
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(o.p + step), 0, left > 0 ? kInside : 0, 0x00027000);
             const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
@@ -104,21 +106,28 @@ struct Stage {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, OB_LDS(void, to + (j * THREADS + wave * 64) * 16), 16,
                                                          static_cast<int>(v), 0, 0, 0);
             }
-        } else {
+        } else if (K_MAJOR ? left >= KT : left > KT && o.ld >= 8) {
+            // Whole chunks.  By rows, one that reaches past the last row ends before the next k's does, which there is: it meets memory
+            // of the operand's, and gives sums that nobody stores.
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) reg[j] = *reinterpret_cast<const u4u*>(at[j] + step);
+        } else {   // the last step (all, of short lines): nothing behind the operand's end, zeros behind its last k
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 int line, chunk;
                 place(j, line, chunk);
-                const int along = (K_MAJOR ? left : o.rows) - chunk * 8;             // elements that there are from the chunk on
-                const bool there = line < (K_MAJOR ? o.rows : left);
-                const uint16_t* p = base + line * o.ld + chunk * 8;
+                const bool in = (K_MAJOR ? line : chunk * 8) < o.rows;
+                const int along = K_MAJOR ? left - chunk * 8 : o.rows - (in ? chunk * 8 : 0);   // elements that there are from the chunk on
+                const uint16_t* p = at[j] + step;
                 u4v v{};
-                if (there && along >= 8) {
-                    v = *reinterpret_cast<const u4u*>(p);
-                } else if (there) {
+                if (K_MAJOR || line < left) {
+                    if (along >= 8) {
+                        v = *reinterpret_cast<const u4u*>(p);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < along) v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+                        for (int e = 0; e < 8; ++e)
+                            if (e < along) v[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+                    }
                 }
                 reg[j] = v;
             }
@@ -273,7 +282,8 @@ struct TileProduct {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
     }
 
-    // Every wave reads a step's fragments and multiplies them, while the next step's operands are on their way.
+    // Every wave reads a step's fragments and multiplies them, while the operands of the next step are on their way.  (Three steps
+    // ahead: 1024^3 on tiles of 64 8.1 us, 7.8 so; 2048^3 31.6 and 26.9, as fewer groups fit.)
     __device__ __forceinline__ void run_in_step(const Operand& lo, const Operand& ro, char* lds)
     {
         SL sl;

@@ -94,31 +94,33 @@ struct TileShares {
     int32_t split;      // 1: rest is 0
 };
 
-// What the choice goes by: sides of the tiles; how many work groups of each a compute unit holds (by LDS); the card's rate, in
-// operations a microsecond, with one, two, ... of them on each unit; microseconds that a tile takes besides its sums.  (8192^3,
-// 4096^3 and fractions of a round, fp16.)
+// What the choice goes by.  kTileRate: operations a microsecond with one, two, ... work groups of a size on each of the 256
+// compute units, of which a unit holds kTileHeld (by LDS).  kTilePower: what the whole card sustains, where its clock falls with the
+// power that is drawn (a card half filled with tiles of 256 runs each a third faster).  kTileExtra: microseconds that a round takes
+// besides its sums.  Measured on fp16 products of 256^3 to 4096^3, 64 x 64 x 65536, and symmetric ones of 528 to 2112 tiles; the estimates
+// are within a fifth of the times.
 constexpr int kTileSizes = 3;
 constexpr int64_t kTileSize[kTileSizes] = {256, 128, 64};
 constexpr int kTileHeld[kTileSizes] = {1, 2, 4};
-constexpr double kTileRate[kTileSizes][4] = {{1200e6}, {650e6, 950e6}, {250e6, 450e6, 580e6, 680e6}};
-constexpr double kTileExtra[kTileSizes] = {7.0, 5.0, 4.0};
+constexpr double kTileRate[kTileSizes][4] = {{1784e6}, {640e6, 1000e6}, {290e6, 540e6, 640e6, 720e6}};
+constexpr double kTilePower[kTileSizes] = {1200e6, 950e6, 700e6};
+constexpr double kTileExtra[kTileSizes] = {8.0, 4.0, 3.0};
 constexpr int64_t kUnits = 256;
-constexpr double kJoin = 5.0, kJoinBytes = 4e6;   // microseconds of the second launch, bytes a microsecond there
+// The launch that adds partial sums: microseconds, and bytes a microsecond (written, then read).
+constexpr double kJoin = 5.0, kJoinBytes = 1.6e6;
 constexpr int32_t kMostSplit = 16;
 constexpr int64_t kLeastSteps = 8;                // of 32 k that a part has
 
 // Microseconds for `tiles` tiles with sums over k.
 inline double tile_round(int size, int64_t tiles, double k)
 {
-    const int64_t slots = kUnits * kTileHeld[size];
+    const int held = kTileHeld[size];
+    const int64_t slots = kUnits * held, rounds = tiles / slots, left = tiles % slots, n = (left + kUnits - 1) / kUnits;
     const double work = 2.0 * static_cast<double>(kTileSize[size] * kTileSize[size]) * k;
-    const int64_t rounds = tiles / slots, left = tiles % slots;
-    double t = static_cast<double>(rounds) * (work * static_cast<double>(slots) / kTileRate[size][kTileHeld[size] - 1] + kTileExtra[size]);
-    if (left > 0) {
-        const int64_t n = (left + kUnits - 1) / kUnits;
-        t += work * static_cast<double>(n * kUnits) / kTileRate[size][n - 1] + kTileExtra[size];
-    }
-    return t;
+    double units = static_cast<double>(rounds * slots) / kTileRate[size][held - 1];
+    if (left > 0) units += static_cast<double>(n * kUnits) / kTileRate[size][n - 1];
+    const double power = static_cast<double>(tiles) / kTilePower[size];
+    return work * std::max(units, power) + kTileExtra[size] * static_cast<double>(rounds + (left > 0));
 }
 
 // The best shares of `tiles` tiles, sums over k (the shortest, of those in a launch's last round) and their time.

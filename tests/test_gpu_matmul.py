@@ -37,7 +37,7 @@ def check(a, b, out, alpha, beta, c, symmetric=False):
     assert float(far.max()) <= 0, (float(far.max()), tuple(a.shape), tuple(b.shape))
 
 
-SHAPES = [(1, 1, 1), (1, 5, 3), (16, 16, 32), (33, 17, 65), (64, 64, 64), (65, 127, 129), (96, 200, 136), (128, 256, 320),
+SHAPES = [(3, 2, 1000), (5, 6, 333), (1, 1, 1), (1, 5, 3), (16, 16, 32), (33, 17, 65), (64, 64, 64), (65, 127, 129), (96, 200, 136), (128, 256, 320),
           (129, 300, 77), (1, 512, 4096), (520, 8, 1000), (264, 520, 72)]
 
 
@@ -166,6 +166,8 @@ def test_repeated_operands_and_infinities():
     gen = torch.Generator("cuda").manual_seed(2)
     a, b = operand(gen, 3, 40, 24, torch.bfloat16), operand(gen, 0, 24, 48, torch.bfloat16).expand(3, 24, 48)
     check(a, b, torch.empty(3, 40, 48, device="cuda"), 1.0, 0.0, None)
+    column = operand(gen, 0, 40, 1, torch.bfloat16).expand(40, 200)   # one column for every k
+    check(column, operand(gen, 0, 200, 48, torch.bfloat16), torch.empty(40, 48, device="cuda"), 1.0, 0.0, None)
     row = operand(gen, 0, 1, 24, torch.bfloat16).expand(40, 24)
     check(row, b[0], torch.empty(40, 48, device="cuda"), 1.0, 0.0, None)
     # an infinity and a NaN stay in their rows and columns; what lies beyond an operand never enters
