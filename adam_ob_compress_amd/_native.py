@@ -776,7 +776,7 @@ def ob_muon_create(tensors: Tensors, shapes) -> MuonPlan:
 def ob_muon_step(plan: MuonPlan, grads, params, m, hp: ob_muon_hparams, workspace, master=None, control=None, stream=None,
                  norm=None):
     """Muon step: m and the optional master copy flat, of the list's state_elems; workspace: a byte tensor of
-    plan.workspace_bytes.  norm=(g_mult, max_norm): ob_grad_norm with these first, once the arguments of both are checked; it
+    plan.workspace_bytes (None where that is 0).  norm=(g_mult, max_norm): ob_grad_norm with these first, once the arguments of both are checked; it
     counts the step in control."""
     if norm is not None and control is None:
         raise TypeError("control must be a torch.Tensor")

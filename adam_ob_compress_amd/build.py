@@ -29,6 +29,7 @@ UNITS = [
     ("ob_clip.hip", []),
     ("ob_clip_api.cpp", []),
     ("ob_muon.hip", []),
+    ("ob_muon_small.hip", []),
     ("ob_muon_api.cpp", []),
 ]
 BUILD_DIR = os.path.join(PKG, "_build")

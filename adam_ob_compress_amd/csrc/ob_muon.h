@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "ob_lists.h"
+#include "ob_product.h"
 
 namespace ob {
 
@@ -40,7 +41,6 @@ struct MuonTile {
 
 constexpr int kMuonItem = 8192;       // elements of an item
 constexpr int kMuonWriteTile = 64;    // side of the tiles that X is written by
-constexpr int kMuonTiles[] = {256, 128, 64};
 
 // The three products of an iteration: A = X X^T (symmetric), b A + c A^2 (symmetric), X = a X + B X.
 enum { MUON_GRAM = 0, MUON_POLY = 1, MUON_STEP = 2 };
@@ -54,14 +54,58 @@ struct MuonGroup {
     int64_t place0, places;       // tensors in the list's order
     MuonRange matrices, items, write;
     MuonRange tiles[3];           // by product
-    int32_t tile[3];              // place in kMuonTiles
+    int32_t tile[3];              // place in kTileSize
 };
+
+// Matrices of one pair of types that fit a compute unit's LDS each: one launch does their whole step.
+struct MuonSmall {
+    int64_t place0, places;
+    MuonRange matrices;
+    int32_t lds;                  // place in kMuonSmallLds
+};
+
+// LDS that such a launch's work groups have: four, two or one of them on a compute unit.
+constexpr int kMuonSmallSizes = 3;
+constexpr int64_t kMuonSmallLds[kMuonSmallSizes] = {40 << 10, 80 << 10, 160 << 10};
+constexpr int kMuonSmallBlocks = 10;   // blocks of 16 rows of the smaller side at most
+
+// Layout of such a matrix in LDS, in elements of 16 bits: X with its rows up to a multiple of 32 (they are the sum's index in B X), its
+// columns too, and 8 more elements to a line, so that lines start in different banks; A and B likewise.
+struct MuonSmallLayout {
+    int32_t rows, sums, cols;     // r up to 16 and to 32, k up to 32
+    int32_t ldx, lda, a, b, scratch;
+    int64_t bytes;
+};
+// One block of A alone, or three: the waves share their sums, by way of 8 KB.
+constexpr int kMuonSmallScratch = 4096;
+inline MuonSmallLayout muon_small_layout(int64_t r, int64_t k)
+{
+    MuonSmallLayout l{};
+    const int64_t rows = (r + 15) / 16 * 16, sums = (r + 31) / 32 * 32, cols = (k + 31) / 32 * 32;
+    const int64_t x = sums * (cols + 8), a = rows * (sums + 8), scratch = rows <= 32 ? kMuonSmallScratch : 0;
+    l.bytes = 2 * (x + 2 * a + scratch) + 128;
+    if (l.bytes > kMuonSmallLds[kMuonSmallSizes - 1]) return l;
+    l.rows = static_cast<int32_t>(rows);
+    l.sums = static_cast<int32_t>(sums);
+    l.cols = static_cast<int32_t>(cols);
+    l.ldx = l.cols + 8;
+    l.lda = l.sums + 8;
+    l.a = static_cast<int32_t>(x);
+    l.b = static_cast<int32_t>(x + a);
+    l.scratch = static_cast<int32_t>(x + 2 * a);
+    return l;
+}
+inline bool muon_is_small(int64_t r, int64_t k)
+{
+    return r <= 16 * kMuonSmallBlocks && muon_small_layout(r, k).bytes <= kMuonSmallLds[kMuonSmallSizes - 1];
+}
 
 struct MuonShape {
     std::vector<MuonMatrix> matrices;
     std::vector<MuonItem> items;
     std::vector<MuonTile> write, tiles;
     std::vector<MuonGroup> groups;
+    std::vector<MuonSmall> small;
     int64_t half_elems = 0;       // the largest group's 16-bit elements
     int64_t parts = 0, most = 0;  // its partial sums, its matrices
     int64_t workspace() const { return 2 * half_elems + 8 * parts + 4 * (most + most % 2); }
@@ -70,10 +114,12 @@ struct MuonShape {
 constexpr int64_t kMuonSide = int64_t(1) << 30;
 // Workspace that a group of several matrices may take: room for enough tiles to fill the card many times over.
 constexpr int64_t kMuonGroupBytes = int64_t(2) << 30;
-// Work groups that are enough for a tile size: the next smaller tile only where fewer would leave compute units idle.
-constexpr int64_t kMuonEnough = 192;
-
 inline int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+inline int64_t muon_tile_count(const MuonMatrix& m, int product, int64_t size)
+{
+    return product == MUON_STEP ? product_tiles(m.r, m.k, size, false) : product_tiles(m.r, m.r, size, true);
+}
 
 // Tiles of all matrices [m0, m1) for `product`, ordered for a launch: work groups go around the eight XCDs, each of which
 // gets one part of every matrix, in panels of eight rows of tiles (those below the diagonal row by row).
@@ -155,20 +201,26 @@ inline bool muon_close(MuonShape& s, int64_t m0, int64_t place0, int64_t places)
     g.items.count = static_cast<int64_t>(s.items.size()) - g.items.first;
     g.write.count = static_cast<int64_t>(s.write.size()) - g.write.first;
     for (int product = 0; product < 3; ++product) {
-        for (int t = 0; t < 3; ++t) {
+        double least = -1.0;
+        int64_t count = 0;
+        for (int t = 0; t < kTileSizes; ++t) {
             int64_t n = 0;
+            double k_sum = 0.0;   // over the tiles
             for (int64_t q = m0; q < m1; ++q) {
-                const int64_t ti = (s.matrices[q].r + kMuonTiles[t] - 1) / kMuonTiles[t], tj = (s.matrices[q].k + kMuonTiles[t] - 1) / kMuonTiles[t];
-                n += product == MUON_STEP ? ti * tj : ti * (ti + 1) / 2;
+                const MuonMatrix& m = s.matrices[q];
+                const int64_t tiles = muon_tile_count(m, product, kTileSize[t]);
+                n += tiles;
+                k_sum += static_cast<double>(tiles) * (product == MUON_GRAM ? m.k : m.r);
             }
-            if (n >= kMuonEnough || t == 2) {
-                if (n > INT32_MAX / 512) return false;
-                g.tile[product] = t;
-                g.tiles[product] = {static_cast<int64_t>(s.tiles.size()), n};
-                muon_tiles(s.matrices, m0, m1, product, kMuonTiles[t], s.tiles);
-                break;
-            }
+            const double us = tile_round(t, n, k_sum / static_cast<double>(n));
+            if (n > INT32_MAX / 512 || (least >= 0.0 && us >= least)) continue;
+            least = us;
+            count = n;
+            g.tile[product] = t;
         }
+        if (least < 0.0) return false;
+        g.tiles[product] = {static_cast<int64_t>(s.tiles.size()), count};
+        muon_tiles(s.matrices, m0, m1, product, kTileSize[g.tile[product]], s.tiles);
     }
     s.half_elems = std::max(s.half_elems, at);
     s.parts = std::max(s.parts, parts);
@@ -188,33 +240,55 @@ inline ob_status build_muon(const ListShape& l, const float* lr_mults, const flo
     }
     bool fits = true;
     const ob_status st = for_runs(l, most_places, true, [&](int64_t k, int64_t e) {
-        int64_t m0 = static_cast<int64_t>(s.matrices.size()), place0 = k, bytes = 0;
-        for (int64_t j = k; j < e; ++j) {
-            const int32_t t = l.order[j];
-            const int64_t n = rows[t] * cols[t];
-            for (int64_t x = 0; x < l.size[t]; x += n) {
-                MuonMatrix m{};
-                m.elem = x;
-                m.state = l.state_off[t] + x;
-                m.place = static_cast<int32_t>(j);
-                m.rows = static_cast<int32_t>(rows[t]);
-                m.cols = static_cast<int32_t>(cols[t]);
+        // f(matrix, its place) for the run's matrices that are small, or are not
+        auto each = [&](bool small, auto&& f) {
+            for (int64_t j = k; j < e; ++j) {
+                const int32_t t = l.order[j];
+                const int64_t n = rows[t] * cols[t];
                 const int64_t r = up8(std::min(rows[t], cols[t])), c = up8(std::max(rows[t], cols[t]));
-                m.r = static_cast<int32_t>(r);
-                m.k = static_cast<int32_t>(c);
-                m.lr_mult = lr_mults ? lr_mults[j] : 1.0f;
-                m.wd_mult = wd_mults ? wd_mults[j] : 1.0f;
-                const int64_t takes = 4 * r * c + 4 * r * r;
-                if (bytes > 0 && bytes + takes > kMuonGroupBytes) {
-                    fits = fits && muon_close(s, m0, place0, j - place0 + 1);
-                    m0 = static_cast<int64_t>(s.matrices.size());
-                    place0 = j;
-                    bytes = 0;
+                if (muon_is_small(r, c) != small) continue;
+                for (int64_t x = 0; x < l.size[t]; x += n) {
+                    MuonMatrix m{};
+                    m.elem = x;
+                    m.state = l.state_off[t] + x;
+                    m.place = static_cast<int32_t>(j);
+                    m.rows = static_cast<int32_t>(rows[t]);
+                    m.cols = static_cast<int32_t>(cols[t]);
+                    m.r = static_cast<int32_t>(r);
+                    m.k = static_cast<int32_t>(c);
+                    m.lr_mult = lr_mults ? lr_mults[j] : 1.0f;
+                    m.wd_mult = wd_mults ? wd_mults[j] : 1.0f;
+                    f(m, j);
                 }
-                bytes += takes;
-                s.matrices.push_back(m);
             }
+        };
+        const int64_t first = static_cast<int64_t>(s.matrices.size());
+        int64_t most = 0;
+        each(true, [&](const MuonMatrix& m, int64_t) {
+            most = std::max(most, muon_small_layout(m.r, m.k).bytes);
+            s.matrices.push_back(m);
+        });
+        int64_t m0 = static_cast<int64_t>(s.matrices.size());
+        if (m0 > first) {
+            // the longest first, so that the last work groups are short ones
+            std::stable_sort(s.matrices.begin() + first, s.matrices.end(), [](const MuonMatrix& a, const MuonMatrix& b) {
+                return static_cast<int64_t>(a.r) * a.k > static_cast<int64_t>(b.r) * b.k;
+            });
+            fits = fits && m0 - first <= INT32_MAX / 512;
+            s.small.push_back({k, e - k, {first, m0 - first}, most <= kMuonSmallLds[0] ? 0 : most <= kMuonSmallLds[1] ? 1 : 2});
         }
+        int64_t place0 = k, bytes = 0;
+        each(false, [&](const MuonMatrix& m, int64_t j) {
+            const int64_t takes = 4 * static_cast<int64_t>(m.r) * m.k + 4 * static_cast<int64_t>(m.r) * m.r;
+            if (bytes > 0 && bytes + takes > kMuonGroupBytes) {
+                fits = fits && muon_close(s, m0, place0, j - place0 + 1);
+                m0 = static_cast<int64_t>(s.matrices.size());
+                bytes = 0;
+            }
+            if (bytes == 0) place0 = j;
+            bytes += takes;
+            s.matrices.push_back(m);
+        });
         if (static_cast<int64_t>(s.matrices.size()) > m0) fits = fits && muon_close(s, m0, place0, e - place0);
         return OB_OK;
     });
@@ -223,7 +297,7 @@ inline ob_status build_muon(const ListShape& l, const float* lr_mults, const flo
 }
 
 inline ob_status check_muon(const ListShape& l, const void* const* g, void* const* p, const float* master, const float* m,
-                            const void* workspace, const ob_muon_hparams* hp, const ob_control* control)
+                            const void* workspace, int64_t workspace_bytes, const ob_muon_hparams* hp, const ob_control* control)
 {
     if (!hp) return OB_ERR_ARG;
     if (!std::isfinite(hp->lr) || !std::isfinite(hp->weight_decay)) return OB_ERR_ARG;
@@ -233,7 +307,7 @@ inline ob_status check_muon(const ListShape& l, const void* const* g, void* cons
     if (hp->scale != OB_MUON_PLAIN && hp->scale != OB_MUON_SHAPE && hp->scale != OB_MUON_MATCH_RMS) return OB_ERR_ARG;
     if (control && !is_aligned(control, 8)) return OB_ERR_ALIGN;
     if (l.n == 0) return OB_OK;
-    if (!p || !m || !workspace) return OB_ERR_ARG;
+    if (!p || !m || (workspace_bytes > 0 && !workspace)) return OB_ERR_ARG;
     if (!is_aligned(m, 16) || !is_aligned(master, 16) || !is_aligned(workspace, 16)) return OB_ERR_ALIGN;
     return check_pointers(l, g, p);
 }

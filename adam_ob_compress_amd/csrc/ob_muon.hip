@@ -1,31 +1,9 @@
 // ob_muon.hip -- the Muon step over lists of matrices: momentum with the sums of squares, the normalised matrices in fp16, the
 // products of the iterations, and the update in the last product's epilogue.
-#include "ob_any.h"
-#include "ob_mfma.h"
-#include "ob_muon_kernels.h"
+#include "ob_muon_device.h"
 
 namespace ob {
 namespace {
-
-// The iteration's polynomial, and the powers of two that its matrices are held times: X in fp16 times 2^9, A and
-// B = b A + c A^2 times 2^10.  |X| <= 1.3, |A| <= 1.5 and |B| < 12 throughout, so nothing overflows, and values down to 2^-14 / 2^9 of X keep all
-// their bits.  fp16 rounds eight times finer than bf16 at the same rate: X after five iterations is off by 1.2e-3 to 4e-3 (2-norm), in
-// bf16 by 1e-2 to 3e-2.
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kScaleX = 512.0f;
-constexpr float kGram = 1.0f / 256.0f;      // sums of X X^T (2^18) to A (2^10)
-constexpr float kUp = 1.0f / 1024.0f;       // sums of A A (2^20) to 2^10, of B X (2^19) to 2^9
-
-__device__ __forceinline__ bool skips(const MuonCall& c) { return c.control && c.control->skip != 0; }
-__device__ __forceinline__ float grad_scale(const MuonCall& c) { return c.control ? c.control->grad_scale : 1.0f; }
-
-// u from the scaled gradient and the new momentum
-__device__ __forceinline__ float direction(const MuonCall& c, float g, float m)
-{
-    return c.nesterov ? static_cast<float>((1.0 - c.momentum) * static_cast<double>(g) + c.momentum * static_cast<double>(m)) : m;
-}
-
-__device__ __forceinline__ f4 load4u(const float* p, int64_t i) { return *reinterpret_cast<const f4e*>(p + i); }
 
 // m = mu m + (1-mu) g', and the sum of u^2 of an item.  One pass: g and m in, m out.
 template <int G>
@@ -126,8 +104,6 @@ __global__ __launch_bounds__(kListBlock) void k_muon_write(MuonCall c, ListPtrs 
     }
 }
 
-typedef _Float16 h4v __attribute__((ext_vector_type(4)));
-
 // The place of X in an iteration (both are loaded: an index would move the whole description out of the scalar registers).
 __device__ __forceinline__ int64_t x_of(const MuonMatrix& mt, int turn) { return turn & 1 ? mt.x[1] : mt.x[0]; }
 
@@ -205,16 +181,13 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_last(MuonCa
     P tile;
     muon_sums<MUON_STEP>(tile, c, mt, turn, m0, n0, lds);
 
-    const double R = mt.rows, C = mt.cols, big = R > C ? R : C;
-    const double scale = c.scale == OB_MUON_MATCH_RMS ? 0.2 * sqrt(big) : c.scale == OB_MUON_SHAPE && R > C ? sqrt(R / C) : 1.0;
-    const float l = static_cast<float>(c.lr * static_cast<double>(mt.lr_mult) * (c.control ? static_cast<double>(c.control->lr_scale) : 1.0));
-    const float d = static_cast<float>(c.wd * static_cast<double>(mt.wd_mult)), sx = static_cast<float>(scale / kScaleX);
+    const Rates q = rates_of(c, mt);
     const bool tall = mt.rows > mt.cols;
     const int rows = tall ? mt.cols : mt.rows, cols = tall ? mt.rows : mt.cols;   // of X, without what was rounded up
     const _Float16* from = reinterpret_cast<const _Float16*>(c.half + x_of(mt, turn));
     float* master = kMaster ? c.master + mt.state : nullptr;
     const u4 none{};
-    auto update = [&](float was, float x) { return fmaf(-l, fmaf(d, was, sx * x), was); };
+    auto update = [&](float was, float x) { return q.update(was, x); };
     // four parameters behind each other, `left` of them there
     auto four = [&](int64_t at, f4 x, int left) {
         if (left >= 4) {

@@ -101,7 +101,7 @@ ob_status ob_muon_check(ob_muon plan, const void* const* g, void* const* p, cons
                         const void* workspace, const ob_muon_hparams* hp, const ob_control* control)
 try {
     if (!plan) return OB_ERR_ARG;
-    return ob::check_muon(plan->list, g, p, master, m, workspace, hp, control);
+    return ob::check_muon(plan->list, g, p, master, m, workspace, plan->shape.workspace(), hp, control);
 } catch (...) {
     return OB_ERR_OOM;
 }
@@ -130,22 +130,32 @@ try {
     c.control = control;
     ob::ListPtrs ptrs;
     (void)hipGetLastError();  // clear a stale error so the checks see these launches only
-    for (const ob::MuonGroup& q : s.groups) {
+    int gd = 0, pk = 0;
+    // the addresses of a group's tensors; whether any has a gradient
+    auto take = [&](int64_t place0, int64_t places) {
         bool any = false;
-        for (int64_t j = 0; j < q.places; ++j) {
-            const int32_t t = l.order[q.place0 + j];
+        for (int64_t j = 0; j < places; ++j) {
+            const int32_t t = l.order[place0 + j];
             ptrs.g[j] = l.size[t] > 0 ? g[t] : nullptr;
             ptrs.p[j] = l.size[t] > 0 ? p[t] : nullptr;
             any = any || ptrs.g[j];
         }
-        if (!any) continue;
-        const int32_t t0 = l.order[q.place0];
-        const int gd = l.g_dtype[t0], pd = l.p_dtype[t0];
-        const int pk = pd == OB_F32 ? ob::PK_F32 : pd + (master ? 2 : 0);
+        const int32_t t0 = l.order[place0];
+        gd = l.g_dtype[t0];
+        pk = l.p_dtype[t0] == OB_F32 ? ob::PK_F32 : l.p_dtype[t0] + (master ? 2 : 0);
+        c.place0 = static_cast<int32_t>(place0);
+        return any;
+    };
+    for (const ob::MuonSmall& q : s.small) {
+        if (!take(q.place0, q.places)) continue;
+        c.matrices = plan->d_matrices + q.matrices.first;
+        if (ob::launch_muon_small(c, ptrs, q.matrices.count, gd, pk, hp->iterations, q.lds, stream) != hipSuccess) return OB_ERR_HIP;
+    }
+    for (const ob::MuonGroup& q : s.groups) {
+        if (!take(q.place0, q.places)) continue;
         c.matrices = plan->d_matrices + q.matrices.first;
         c.items = plan->d_items + q.items.first;
         c.write = plan->d_write + q.write.first;
-        c.place0 = static_cast<int32_t>(q.place0);
         if (ob::launch_muon_momentum(c, ptrs, gd, q.items.count, stream) != hipSuccess) return OB_ERR_HIP;
         if (ob::launch_muon_factor(c, q.matrices.count, stream) != hipSuccess) return OB_ERR_HIP;
         if (ob::launch_muon_write(c, ptrs, gd, q.write.count, stream) != hipSuccess) return OB_ERR_HIP;

@@ -31,4 +31,8 @@ hipError_t launch_muon_product(const MuonCall& c, int product, const MuonTile* t
 hipError_t launch_muon_last(const MuonCall& c, const ListPtrs& ptrs, const MuonTile* tiles, int64_t count, int tile, int turn, int pk,
                             hipStream_t s);
 
+// The whole step for matrices that fit a compute unit's LDS: one work group for each; lds: place in kMuonSmallLds.
+hipError_t launch_muon_small(const MuonCall& c, const ListPtrs& ptrs, int64_t matrices, int g_dtype, int pk, int iterations, int lds,
+                             hipStream_t s);
+
 }  // namespace ob

@@ -259,9 +259,10 @@ PyObject* state8(PyObject*, PyObject* const* args, Py_ssize_t n)
     });
 }
 
-// A workspace: a byte tensor of at least this size.
+// A workspace: a byte tensor of at least this size, or None where that is 0.
 void* room(PyObject* item, int64_t bytes, long device, int64_t where)
 {
+    if (item == Py_None && bytes == 0) return nullptr;
     if (!THPVariable_Check(item)) throw Bad{where, 0};
     const int64_t n = THPVariable_Unpack(item).numel();
     if (n < bytes) throw Bad{where, 0};

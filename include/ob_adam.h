@@ -523,8 +523,8 @@ ob_status ob_matmul(const ob_product* product, hipStream_t stream);
  * each other, each by rows.  rows, cols: T host int64, 1 to 2^30.  It belongs to the list's device, copies what it needs of
  * the list, and owns its device tables.
  * m, master: flat, ob_tensors_state_elems(list) fp32 in the list's layout; g, p, master otherwise as in ob_adamw_step.
- * workspace: ob_muon_workspace(plan) bytes of device memory, 16-byte aligned, of any content; calls that may overlap (other
- * streams, captured graphs replayed at once) need their own.
+ * workspace: ob_muon_workspace(plan) bytes of device memory, 16-byte aligned, of any content (NULL where that is 0: small matrices
+ * need none); calls that may overlap (other streams, captured graphs replayed at once) need their own.
  * ob_muon_check: the status with which ob_muon_step would refuse these arguments; no GPU work. */
 typedef struct ob_muon_s* ob_muon;
 

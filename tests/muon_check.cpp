@@ -51,6 +51,32 @@ static void check_plan(const std::vector<Mat>& mats, const std::vector<int32_t>&
     int64_t want = 0;
     for (const Mat& m : mats) want += m.e;
     CHECK(static_cast<int64_t>(s.matrices.size()) == want);
+    // one matrix of a group or launch: in a tensor of it, with its description
+    auto described = [&](const ob::MuonMatrix& m, int64_t place0, int64_t count) {
+        CHECK(m.place >= place0 && m.place < place0 + count);
+        const int32_t t = l.order[m.place], t0 = l.order[place0];
+        CHECK(l.g_dtype[t] == l.g_dtype[t0] && l.p_dtype[t] == l.p_dtype[t0]);
+        CHECK(m.rows == rows[t] && m.cols == cols[t] && m.state == l.state_off[t] + m.elem);
+        CHECK(m.elem % (rows[t] * cols[t]) == 0 && m.elem < l.size[t]);
+        CHECK(seen.insert({m.place, m.elem}).second);
+        CHECK(m.r % 8 == 0 && m.k % 8 == 0 && m.r >= std::min(m.rows, m.cols) && m.k >= std::max(m.rows, m.cols) &&
+              m.r < std::min(m.rows, m.cols) + 8 && m.k < std::max(m.rows, m.cols) + 8);
+        CHECK(m.lr_mult == lr[m.place] && m.wd_mult == wd[m.place]);
+    };
+    for (const ob::MuonSmall& q : s.small) {
+        CHECK(q.places >= 1 && q.places <= places && q.matrices.count >= 1 && q.lds >= 0 && q.lds < ob::kMuonSmallSizes);
+        for (int64_t k = 0; k < q.matrices.count; ++k) {
+            const ob::MuonMatrix& m = s.matrices[q.matrices.first + k];
+            described(m, q.place0, q.places);
+            CHECK(ob::muon_is_small(m.r, m.k));
+            const ob::MuonSmallLayout y = ob::muon_small_layout(m.r, m.k);
+            // as the kernel lays it out: X, A, B, the waves' shares of a sum, a number for each wave
+            CHECK(y.rows % 16 == 0 && y.sums % 32 == 0 && y.cols % 32 == 0 && y.rows <= 16 * ob::kMuonSmallBlocks);
+            CHECK(y.rows >= m.r && y.sums >= y.rows && y.cols >= m.k && y.ldx >= y.cols + 8 && y.lda >= y.sums + 8);
+            CHECK(y.a == y.sums * y.ldx && y.b == y.a + y.rows * y.lda && y.scratch == y.b + y.rows * y.lda);
+            CHECK(y.bytes >= 2 * (y.scratch + (y.rows <= 32 ? 8 * 64 * 8 : 0)) + 8 * 8 && y.bytes <= ob::kMuonSmallLds[q.lds]);
+        }
+    }
     for (const ob::MuonGroup& g : s.groups) {
         CHECK(g.places >= 1 && g.places <= places && g.matrices.count >= 1);
         int64_t bytes = 0;
@@ -58,15 +84,8 @@ static void check_plan(const std::vector<Mat>& mats, const std::vector<int32_t>&
         std::vector<bool> part;
         for (int64_t q = 0; q < g.matrices.count; ++q) {
             const ob::MuonMatrix& m = s.matrices[g.matrices.first + q];
-            CHECK(m.place >= g.place0 && m.place < g.place0 + g.places);
-            const int32_t t = l.order[m.place], t0 = l.order[g.place0];
-            CHECK(l.g_dtype[t] == l.g_dtype[t0] && l.p_dtype[t] == l.p_dtype[t0]);
-            CHECK(m.rows == rows[t] && m.cols == cols[t] && m.state == l.state_off[t] + m.elem);
-            CHECK(m.elem % (rows[t] * cols[t]) == 0 && m.elem < l.size[t]);
-            CHECK(seen.insert({m.place, m.elem}).second);
-            CHECK(m.r % 8 == 0 && m.k % 8 == 0 && m.r >= std::min(m.rows, m.cols) && m.k >= std::max(m.rows, m.cols) &&
-                  m.r < std::min(m.rows, m.cols) + 8 && m.k < std::max(m.rows, m.cols) + 8);
-            CHECK(m.lr_mult == lr[m.place] && m.wd_mult == wd[m.place]);
+            described(m, g.place0, g.places);
+            CHECK(!ob::muon_is_small(m.r, m.k));
             for (int64_t x : {m.x[0], m.x[1], m.a, m.b}) CHECK(x % 128 == 0);
             const int64_t rk = static_cast<int64_t>(m.r) * m.k, rr = static_cast<int64_t>(m.r) * m.r;
             room.push_back({m.x[0], rk});
@@ -113,7 +132,7 @@ static void check_plan(const std::vector<Mat>& mats, const std::vector<int32_t>&
             CHECK(n == range.count);
         };
         cover(s.write, g.write, ob::kMuonWriteTile, false);
-        for (int p = 0; p < 3; ++p) cover(s.tiles, g.tiles[p], ob::kMuonTiles[g.tile[p]], p != ob::MUON_STEP);
+        for (int p = 0; p < 3; ++p) cover(s.tiles, g.tiles[p], ob::kTileSize[g.tile[p]], p != ob::MUON_STEP);
     }
     CHECK(static_cast<int64_t>(seen.size()) == want);
     CHECK(s.workspace() % 8 == 0);
@@ -142,6 +161,11 @@ int main()
     check_plan({{40, 4096, 4096}, {2, 300, 20}}, {0, 0}, {0, 0}, 200);
     check_plan({{1, 32000, 4096}, {1, 65536, 8192}, {1, 16, 16}}, {0, 0, 0}, {0, 0, 0}, 200);
     check_plan({}, {}, {}, 200);
+    // around the limits of a compute unit's LDS, long thin ones, small ones between large ones
+    check_plan({{1, 160, 160}, {1, 161, 160}, {1, 168, 168}, {3, 128, 256}, {1, 64, 1100}, {1, 16, 2300}, {1, 2400, 9}, {1, 700, 64}, {5, 33, 17}, {1, 4000, 4000}},
+               {0, 0, 0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0, 0, 0, 0, 0, 0, 0}, 200);
+    CHECK(ob::muon_is_small(160, 160) && !ob::muon_is_small(168, 168) && ob::muon_is_small(128, 256) && !ob::muon_is_small(128, 512));
+    CHECK(ob::muon_is_small(16, 2048) && !ob::muon_is_small(8, 4096) && !ob::muon_is_small(INT64_C(1) << 30, INT64_C(1) << 30));
 
     // refusals of a plan
     const std::vector<Mat> one{{2, 8, 4}};
@@ -162,25 +186,26 @@ int main()
     const float* m = reinterpret_cast<float*>(0x3000);
     const void* w = reinterpret_cast<void*>(0x4000);
     const ob_muon_hparams hp = good();
-    CHECK(ob::check_muon(l, g, p, nullptr, m, w, &hp, nullptr) == OB_OK);
-    CHECK(ob::check_muon(l, g, p, nullptr, m, w, nullptr, nullptr) == OB_ERR_ARG);
-    CHECK(ob::check_muon(l, nullptr, p, nullptr, m, w, &hp, nullptr) == OB_ERR_ARG);
-    CHECK(ob::check_muon(l, g, nullptr, nullptr, m, w, &hp, nullptr) == OB_ERR_ARG);
-    CHECK(ob::check_muon(l, g, p, nullptr, nullptr, w, &hp, nullptr) == OB_ERR_ARG);
-    CHECK(ob::check_muon(l, g, p, nullptr, m, nullptr, &hp, nullptr) == OB_ERR_ARG);
-    CHECK(ob::check_muon(l, g, p, nullptr, m + 1, w, &hp, nullptr) == OB_ERR_ALIGN);
-    CHECK(ob::check_muon(l, g, p, m + 1, m, w, &hp, nullptr) == OB_ERR_ALIGN);
-    CHECK(ob::check_muon(l, g, p, nullptr, m, reinterpret_cast<void*>(0x4008), &hp, nullptr) == OB_ERR_ALIGN);
-    CHECK(ob::check_muon(l, g, p, nullptr, m, w, &hp, reinterpret_cast<ob_control*>(0x5004)) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, w, 64, &hp, nullptr) == OB_OK);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, w, 64, nullptr, nullptr) == OB_ERR_ARG);
+    CHECK(ob::check_muon(l, nullptr, p, nullptr, m, w, 64, &hp, nullptr) == OB_ERR_ARG);
+    CHECK(ob::check_muon(l, g, nullptr, nullptr, m, w, 64, &hp, nullptr) == OB_ERR_ARG);
+    CHECK(ob::check_muon(l, g, p, nullptr, nullptr, w, 64, &hp, nullptr) == OB_ERR_ARG);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, nullptr, 64, &hp, nullptr) == OB_ERR_ARG);
+    CHECK(ob::check_muon(l, g, p, nullptr, m + 1, w, 64, &hp, nullptr) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, p, m + 1, m, w, 64, &hp, nullptr) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, reinterpret_cast<void*>(0x4008), 64, &hp, nullptr) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, w, 64, &hp, reinterpret_cast<ob_control*>(0x5004)) == OB_ERR_ALIGN);
     void* odd[1] = {reinterpret_cast<void*>(0x2002)};
-    CHECK(ob::check_muon(l, g, odd, nullptr, m, w, &hp, nullptr) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, odd, nullptr, m, w, 64, &hp, nullptr) == OB_ERR_ALIGN);
+    CHECK(ob::check_muon(l, g, p, nullptr, m, nullptr, 0, &hp, nullptr) == OB_OK);   // a plan that needs none
     const void* no[1] = {nullptr};
     void* nop[1] = {nullptr};
-    CHECK(ob::check_muon(l, no, nop, nullptr, m, w, &hp, nullptr) == OB_OK);   // no gradient: nothing to do
+    CHECK(ob::check_muon(l, no, nop, nullptr, m, w, 64, &hp, nullptr) == OB_OK);   // no gradient: nothing to do
     auto with = [&](auto&& change) {
         ob_muon_hparams h = good();
         change(h);
-        return ob::check_muon(l, g, p, nullptr, m, w, &h, nullptr);
+        return ob::check_muon(l, g, p, nullptr, m, w, 64, &h, nullptr);
     };
     using H = ob_muon_hparams;
     const float nan = std::nanf("");

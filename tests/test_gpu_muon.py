@@ -122,7 +122,8 @@ def directions(l, shapes, grads, m, mu, nesterov, mult=1.0):
 
 
 SHAPES = [[(1, 1)], [(1, 7)], [(8, 8)], [(33, 17)], [(64, 64), (64, 64)], [(100, 37), (5, 129), (129, 5)], [(3, 40, 24), (2, 24, 40)],
-          [(130, 300), (300, 130)], [(256, 256), (264, 520)], [(16, 2000)], [(2000, 3)], [(520, 700), (64, 1), (1, 64)]]
+          [(130, 300), (300, 130)], [(256, 256), (264, 520)], [(16, 2000)], [(2000, 3)], [(520, 700), (64, 1), (1, 64)],
+          [(160, 160), (168, 168)], [(128, 256), (300, 96), (17, 1000)], [(2400, 9), (20, 1500), (32, 32)]]
 
 
 @pytest.mark.parametrize("iterations", [1, 2])
@@ -401,10 +402,13 @@ def test_refusals():
         ob.ob_muon_create(l, [(8, 5)])
     with pytest.raises(ValueError, match="entries"):
         ob.ob_muon_create(l, [(8, 4), (8, 4)])
+    _, large, g2, p2, m2, work2 = make([(200, 300)])
     with pytest.raises(ValueError, match="bytes"):
-        ob.ob_muon_step(plan, grads, params, m, hp, work[:16])
+        ob.ob_muon_step(large, g2, p2, m2, hp, work2[:-1])
     with pytest.raises(TypeError, match="workspace"):
-        ob.ob_muon_step(plan, grads, params, m, hp, None)
+        ob.ob_muon_step(large, g2, p2, m2, hp, None)
+    with pytest.raises(TypeError, match="workspace"):
+        ob.ob_muon_step(large, g2, p2, m2, hp, work2.view(torch.int8))
     with pytest.raises(TypeError, match="muon_hparams"):
         ob.ob_muon_step(plan, grads, params, m, ob.adamw_hparams(), work)
     with pytest.raises(ValueError, match="m must have"):
