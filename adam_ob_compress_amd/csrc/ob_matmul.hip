@@ -34,32 +34,59 @@ __device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n)
     return x * each + (x < more ? x : more) + b / 8;
 }
 
+// Four elements of type D as they are loaded, and widened.
 template <int D>
-__device__ __forceinline__ f4 load_row4(const void* p, int64_t i, int left)
-{
-    if (left >= 4) {
-        if constexpr (D == 0) return *reinterpret_cast<const f4e*>(static_cast<const float*>(p) + i);
-        const u2e u = *reinterpret_cast<const u2e*>(static_cast<const uint16_t*>(p) + i);
-        return f4{widen16<D>(u.x & 0xffffu), widen16<D>(u.x >> 16), widen16<D>(u.y & 0xffffu), widen16<D>(u.y >> 16)};
+struct Four {
+    f4e v;
+    __device__ __forceinline__ f4 wide() const { return v; }
+};
+template <>
+struct Four<1> {
+    u2e v;
+    __device__ __forceinline__ f4 wide() const
+    {
+        return f4{widen16<1>(v.x & 0xffffu), widen16<1>(v.x >> 16), widen16<1>(v.y & 0xffffu), widen16<1>(v.y >> 16)};
     }
-    f4 r{};
+};
+template <>
+struct Four<2> {
+    u2e v;
+    __device__ __forceinline__ f4 wide() const
+    {
+        return f4{widen16<2>(v.x & 0xffffu), widen16<2>(v.x >> 16), widen16<2>(v.y & 0xffffu), widen16<2>(v.y >> 16)};
+    }
+};
+
+// From element i on, `left` of them there.
+template <int D>
+__device__ __forceinline__ Four<D> load_four(const char* p, int64_t i, int left)
+{
+    Four<D> r{};
+    if (left >= 4) {
+        r.v = *reinterpret_cast<const decltype(r.v)*>(p + i * (D == 0 ? 4 : 2));
+    } else if constexpr (D == 0) {
 #pragma unroll
-    for (int e = 0; e < 3; ++e)
-        if (e < left) r[e] = load_any1<D>(p, i + e);
+        for (int e = 0; e < 3; ++e)
+            if (e < left) r.v[e] = reinterpret_cast<const float*>(p)[i + e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) r.v[e >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i + e]) << (16 * (e & 1));
+    }
     return r;
 }
 
 template <int D>
-__device__ __forceinline__ void store_row4(void* p, int64_t i, f4 x, int left)
+__device__ __forceinline__ void store_four(char* p, int64_t i, f4 x, int left)
 {
     if (left >= 4) {
         if constexpr (D == 0) {
-            *reinterpret_cast<f4e*>(static_cast<float*>(p) + i) = x;
+            *reinterpret_cast<f4e*>(p + i * 4) = x;
         } else {
             u2e u;
             u.x = round16x2<D, false>(x.x, x.y, 0, 0);
             u.y = round16x2<D, false>(x.z, x.w, 0, 0);
-            *reinterpret_cast<u2e*>(static_cast<uint16_t*>(p) + i) = u;
+            *reinterpret_cast<u2e*>(p + i * 2) = u;
         }
         return;
     }
@@ -68,38 +95,38 @@ __device__ __forceinline__ void store_row4(void* p, int64_t i, f4 x, int left)
         if (e < left) store_any1<D, false>(p, i + e, x[e], 0);
 }
 
-// Four elements of D from their sums.  WHOLE: all four are there.
-template <int D, bool WHOLE>
-__device__ __forceinline__ void put4(const ProductArgs& p, const char* c, char* d, int64_t ci, int64_t di, f4v sum, int left)
-{
-    f4 x;
-    if (p.beta != 0.0f) {
-        const f4 y = load_row4<D>(c, ci, WHOLE ? 4 : left);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
-    }
-    store_row4<D>(d, di, x, WHOLE ? 4 : left);
-}
-
+// The result of a tile, WHOLE (all of it is there) or not.  mirror: what is below the diagonal goes above it too.
 template <int D, bool WHOLE, class P>
 __device__ __forceinline__ void finish_part(const ProductArgs& p, const P& tile, char* lds, int64_t batch, int m0, int n0, bool mirror, int only)
 {
     constexpr int64_t kBytes = D == 0 ? 4 : 2;
     const char* c = static_cast<const char*>(p.c) + batch * p.batch_c * kBytes;
     char* d = static_cast<char*>(p.d) + batch * p.batch_d * kBytes;
+    auto load = [&](int r, int col) {
+        const int i = m0 + r, j = n0 + col;
+        if (p.beta == 0.0f || (!WHOLE && (i >= p.m || j >= p.n))) return Four<D>{};
+        return load_four<D>(c, i * p.ldc + j, WHOLE ? 4 : p.n - j);
+    };
     tile.finish(
-        lds, true,
-        [&](int r, int col, f4v sum) {
-            const int64_t i = m0 + r, j = n0 + col;
-            if (WHOLE || (i < p.m && j < p.n)) put4<D, WHOLE>(p, c, d, i * p.ldc + j, i * p.ldd + j, sum, p.n - static_cast<int>(j));
+        lds, load,
+        [&](int r, int col, f4v sum, const Four<D>& old) {
+            const int i = m0 + r, j = n0 + col;
+            f4v x;
+            if (p.beta != 0.0f) {
+                const f4 y = old.wide();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(p.alpha, sum[e], p.beta * y[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = p.alpha * sum[e];
+            }
+            if (WHOLE || (i < p.m && j < p.n)) store_four<D>(d, i * p.ldd + j, x, WHOLE ? 4 : p.n - j);
+            return x;
         },
-        mirror,
-        [&](int r, int col, f4v sum) {   // above the diagonal, with C's rows there
-            const int64_t i = m0 + r, j = n0 + col;
-            if (WHOLE || (i < p.m && j < p.n)) put4<D, WHOLE>(p, c, d, j * p.ldc + i, j * p.ldd + i, sum, p.m - static_cast<int>(i));
+        mirror, [](int, int) { return 0; },
+        [&](int r, int col, f4v x, int) {
+            const int i = m0 + r, j = n0 + col;
+            if (WHOLE || (i < p.m && j < p.n)) store_four<D>(d, j * p.ldd + i, x, WHOLE ? 4 : p.m - i);
         },
         only);
 }

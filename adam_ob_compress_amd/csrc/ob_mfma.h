@@ -339,40 +339,61 @@ struct TileProduct {
         }
     }
 
-    // The tile's sums by way of LDS (the buffers that run() has left), so that a wave meets whole lines of the result:
-    // direct: f(row, column, four sums of the row from the column on); turned: g(row, column, four sums of the column from the
-    // row on).  Every thread of the group.  only: the turn of kRows rows of each wave that is wanted (-1: all).
-    static constexpr int kRows = 2 * kMfma, kTurnsOut = WM / kRows;   // rows of a turn, turns
+    // The tile's sums by way of LDS (the buffers that run() has left), so that a wave meets whole lines of the result, in turns of
+    // kRows of its rows.  Every thread of the group; only: the turn that is wanted (-1: all).
+    //   x = f(row, column, four sums of the row from the column on, load(row, column))
+    //   turned: g(row, column, four x of the column from the row on, load_turned(row, column))
+    // A turn's loads are started before the turn before is finished: the results may lie where the loads read, so that the compiler
+    // would keep each load behind the store before it, 32 waits in a row (4096 x 11008 x 4096 with a residual 385 us, now see below).
+    static constexpr int kRows = 2 * kMfma, kTurnsOut = WM / kRows;
     static constexpr int kLdsOut = kRows * (WN + 4) * 4 * (kThreads / 64);
-    template <class F, class G>
-    __device__ __forceinline__ void finish(char* lds, bool direct, F&& f, bool turned, G&& g, int only = -1) const
+    template <class L, class F, class LT, class G>
+    __device__ __forceinline__ void finish(char* lds, L&& load, F&& f, bool turned, LT&& load_turned, G&& g, int only = -1) const
     {
         constexpr int kLd = WN + 4;   // 4 floats more keep the rows of a write in different banks
+        constexpr int kEachOut = kRows * WN / 256;   // times four elements of a lane in a turn
         static_assert(kLdsOut <= kLds, "every wave has its part of the buffers");
-        const int lane = static_cast<int>(threadIdx.x) & 63;
+        const int lane = static_cast<int>(threadIdx.x) & 63, m = wave_m(), n = wave_n();
         float* mine = reinterpret_cast<float*>(lds) + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * (kRows * kLd);
+        auto row = [&](int k) { return (lane + 64 * k) / (WN / 4); };
+        auto col = [&](int k) { return (lane + 64 * k) % (WN / 4) * 4; };
+        auto row_turned = [&](int k) { return (lane + 64 * k) % (kRows / 4) * 4; };
+        auto col_turned = [&](int k) { return (lane + 64 * k) / (kRows / 4); };
+        // two turns' loads if they take no more than 64 registers, else one's
+        constexpr int kHeld = sizeof(load(0, 0)) * kEachOut * 2 <= 256 ? 2 : 1;
+        decltype(load(0, 0)) held[kHeld][kEachOut];
+        decltype(load_turned(0, 0)) held_turned[kEachOut];
+        auto start = [&](int h) {
+#pragma unroll
+            for (int k = 0; k < kEachOut; ++k) held[h % kHeld][k] = load(m + kRows * h + row(k), n + col(k));
+        };
         __syncthreads();   // the last fragments have left the buffers
+        if (only < 0 && kHeld == 2) start(0);
 #pragma unroll
         for (int h = 0; h < kTurnsOut; ++h) {
             if (only >= 0 && h != only) continue;
+            if (only >= 0 || kHeld == 1) start(h);
+            if (turned) {
+#pragma unroll
+                for (int k = 0; k < kEachOut; ++k) held_turned[k] = load_turned(m + kRows * h + row_turned(k), n + col_turned(k));
+            }
+            if (only < 0 && kHeld == 2 && h + 1 < kTurnsOut) start(h + 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int j = 0; j < kFn; ++j)
-                    *reinterpret_cast<f4v*>(mine + (16 * i + (lane & 15)) * kLd + 16 * j + 4 * (lane >> 4)) = acc[2 * h + i][j];
-            if (direct) {
+                    *reinterpret_cast<f4v*>(mine + (kMfma * i + (lane & 15)) * kLd + kMfma * j + 4 * (lane >> 4)) = acc[2 * h + i][j];
 #pragma unroll
-                for (int k = 0; k < kRows * WN / 256; ++k) {
-                    const int q = lane + 64 * k, row = q / (WN / 4), col = q % (WN / 4) * 4;
-                    f(wave_m() + kRows * h + row, wave_n() + col, *reinterpret_cast<const f4v*>(mine + row * kLd + col));
-                }
+            for (int k = 0; k < kEachOut; ++k) {
+                f4v* at = reinterpret_cast<f4v*>(mine + row(k) * kLd + col(k));
+                const f4v x = f(m + kRows * h + row(k), n + col(k), *at, held[h % kHeld][k]);
+                if (turned) *at = x;
             }
             if (turned) {
 #pragma unroll
-                for (int k = 0; k < kRows * WN / 256; ++k) {
-                    const int q = lane + 64 * k, col = q / (kRows / 4), row = q % (kRows / 4) * 4;
-                    const float* at = mine + row * kLd + col;
-                    g(wave_m() + kRows * h + row, wave_n() + col, f4v{at[0], at[kLd], at[2 * kLd], at[3 * kLd]});
+                for (int k = 0; k < kEachOut; ++k) {
+                    const float* at = mine + row_turned(k) * kLd + col_turned(k);
+                    g(m + kRows * h + row_turned(k), n + col_turned(k), f4v{at[0], at[kLd], at[2 * kLd], at[3 * kLd]}, held_turned[k]);
                 }
             }
         }

@@ -141,27 +141,33 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_product(Muo
     _Float16* to = reinterpret_cast<_Float16*>(c.half + (PRODUCT == MUON_GRAM ? mt.a : PRODUCT == MUON_POLY ? mt.b : x_of(mt, turn + 1)));
     const int64_t ld = PRODUCT == MUON_STEP ? mt.k : mt.r;
     const int cols = PRODUCT == MUON_STEP ? mt.k : mt.r;
-    // four elements of the result, with what is added to the sums
-    auto value = [&](int64_t at, f4v s) {
-        h4v h;
-        if constexpr (PRODUCT == MUON_GRAM) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(s[e] * kGram);
-        } else {
-            const h4v old = *reinterpret_cast<const h4v*>(from + at);
+    // both sides are multiples of 8; A is symmetric, and so is what is added to its sums
+    tile.finish(
+        lds,
+        [&](int r, int col) {
+            h4v old{};
+            if (PRODUCT != MUON_GRAM && m0 + r < mt.r && n0 + col < cols) old = *reinterpret_cast<const h4v*>(from + (m0 + r) * ld + n0 + col);
+            return old;
+        },
+        [&](int r, int col, f4v s, h4v old) {
+            f4v x;
+            h4v h;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float o = static_cast<float>(old[e]);
-                h[e] = static_cast<_Float16>(PRODUCT == MUON_POLY ? fmaf(kC * kUp, s[e], kB * o) : fmaf(kUp, s[e], kA * o));
+                x[e] = PRODUCT == MUON_GRAM ? s[e] * kGram : PRODUCT == MUON_POLY ? fmaf(kC * kUp, s[e], kB * o) : fmaf(kUp, s[e], kA * o);
+                h[e] = static_cast<_Float16>(x[e]);
             }
-        }
-        *reinterpret_cast<h4v*>(to + at) = h;
-    };
-    // both sides are multiples of 8; A is symmetric, and so is what is added to the turned sums
-    tile.finish(
-        lds, true, [&](int r, int col, f4v s) { if (m0 + r < mt.r && n0 + col < cols) value((m0 + r) * ld + n0 + col, s); },
-        PRODUCT != MUON_STEP && tl.i != tl.j,
-        [&](int r, int col, f4v s) { if (m0 + r < mt.r && n0 + col < cols) value((n0 + col) * ld + m0 + r, s); });
+            if (m0 + r < mt.r && n0 + col < cols) *reinterpret_cast<h4v*>(to + (m0 + r) * ld + n0 + col) = h;
+            return x;
+        },
+        PRODUCT != MUON_STEP && tl.i != tl.j, [](int, int) { return 0; },
+        [&](int r, int col, f4v x, int) {
+            h4v h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(x[e]);
+            if (m0 + r < mt.r && n0 + col < cols) *reinterpret_cast<h4v*>(to + (n0 + col) * ld + m0 + r) = h;
+        });
 }
 
 // The last X and the update.
@@ -186,47 +192,64 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_last(MuonCa
     const int rows = tall ? mt.cols : mt.rows, cols = tall ? mt.rows : mt.cols;   // of X, without what was rounded up
     const _Float16* from = reinterpret_cast<const _Float16*>(c.half + x_of(mt, turn));
     float* master = kMaster ? c.master + mt.state : nullptr;
-    const u4 none{};
-    auto update = [&](float was, float x) { return q.update(was, x); };
-    // four parameters behind each other, `left` of them there
-    auto four = [&](int64_t at, f4 x, int left) {
-        if (left >= 4) {
-            const f4 was = kMaster ? load4u(master, at) : load_any4<D>(p, mt.elem + at);
-            f4 now;
+    // Four parameters behind each other from `at` on, `left` of them there: as they are, and updated.
+    auto load = [&](int64_t at, int left) {
+        f4 was{};
+        if (left >= 4)
+            was = kMaster ? load4u(master, at) : load_any4<D>(p, mt.elem + at);
+        else
 #pragma unroll
-            for (int e = 0; e < 4; ++e) now[e] = update(was[e], x[e]);
+            for (int e = 0; e < 3; ++e)
+                if (e < left) was[e] = kMaster ? master[at + e] : load_any1<D>(p, mt.elem + at + e);
+        return was;
+    };
+    auto store = [&](int64_t at, f4 was, f4v x, int left) {
+        f4 now;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) now[e] = q.update(was[e], x[e]);
+        if (left >= 4) {
             if (kMaster) *reinterpret_cast<f4e*>(master + at) = now;
-            store_any4<D, false>(p, mt.elem + at, now, none);
+            store_any4<D, false>(p, mt.elem + at, now, u4{});
             return;
         }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
             if (e >= left) continue;
-            const float now = update(kMaster ? master[at + e] : load_any1<D>(p, mt.elem + at + e), x[e]);
-            if (kMaster) master[at + e] = now;
-            store_any1<D, false>(p, mt.elem + at + e, now, 0);
+            if (kMaster) master[at + e] = now[e];
+            store_any1<D, false>(p, mt.elem + at + e, now[e], 0);
         }
     };
+    struct Held {
+        h4v x;
+        f4 was;
+    };
+    // a matrix with more rows than columns is turned over: its parameters lie along X's columns
     tile.finish(
-        lds, !tall,
-        [&](int r, int col, f4v s) {
+        lds,
+        [&](int r, int col) {
             const int i = m0 + r, j = n0 + col;
-            if (i >= rows || j >= cols) return;
-            const h4v old = *reinterpret_cast<const h4v*>(from + static_cast<int64_t>(i) * mt.k + j);
-            f4 x;
+            Held h{};
+            if (i >= rows || j >= cols) return h;
+            h.x = *reinterpret_cast<const h4v*>(from + static_cast<int64_t>(i) * mt.k + j);
+            if (!tall) h.was = load(static_cast<int64_t>(i) * mt.cols + j, cols - j);
+            return h;
+        },
+        [&](int r, int col, f4v s, const Held& h) {
+            const int i = m0 + r, j = n0 + col;
+            f4v x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = fmaf(kUp, s[e], kA * static_cast<float>(old[e]));
-            four(static_cast<int64_t>(i) * mt.cols + j, x, cols - j);
+            for (int e = 0; e < 4; ++e) x[e] = fmaf(kUp, s[e], kA * static_cast<float>(h.x[e]));
+            if (!tall && i < rows && j < cols) store(static_cast<int64_t>(i) * mt.cols + j, h.was, x, cols - j);
+            return x;
         },
         tall,
-        [&](int r, int col, f4v s) {
-            const int i = m0 + r, j = n0 + col, left = rows - i;
-            if (left <= 0 || j >= cols) return;
-            f4 x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)   // rows up to a multiple of 8 are there
-                x[e] = fmaf(kUp, s[e], kA * static_cast<float>(from[static_cast<int64_t>(i + e) * mt.k + j]));
-            four(static_cast<int64_t>(j) * mt.cols + i, x, left);
+        [&](int r, int col) {
+            const int i = m0 + r, j = n0 + col;
+            return i < rows && j < cols ? load(static_cast<int64_t>(j) * mt.cols + i, rows - i) : f4{};
+        },
+        [&](int r, int col, f4v x, f4 was) {
+            const int i = m0 + r, j = n0 + col;
+            if (i < rows && j < cols) store(static_cast<int64_t>(j) * mt.cols + i, was, x, rows - i);
         });
 }
 
