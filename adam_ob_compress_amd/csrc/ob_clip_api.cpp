@@ -76,7 +76,7 @@ try {
             ptrs.p[j - k] = out ? out[sh.order[j]] : const_cast<void*>(g[sh.order[j]]);
         }
         const int gd = sh.g_dtype[sh.order[k]], od = out ? sh.p_dtype[sh.order[k]] : gd;
-        const ob_status st = ob::for_parts(l.step.first[e] - l.step.first[k], ob::kMostGroups / ob::kStepTiles, [&](int64_t i, int64_t n) {
+        const ob_status st = ob::for_parts(l.step.first[e] - l.step.first[k], ob::kMostGroups, [&](int64_t i, int64_t n) {
             const ob::ListLaunch L{l.step.d_items + l.step.first[k] + i, l.d_tensors, n, static_cast<int32_t>(k)};
             (void)hipGetLastError();
             return ob::launch_clip(L, ptrs, gd, od, cp, stream) == hipSuccess ? OB_OK : OB_ERR_HIP;
