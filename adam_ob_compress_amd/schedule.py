@@ -89,6 +89,7 @@ class OneBitAdam:
         return kind
 
     def _clip(self, g, stream):
+        nat._gdtype(g)   # what the step would refuse is not clipped
         if g.dtype not in self._clips:   # a list of one tensor for each type that gradients come in
             self._clips[g.dtype] = GradClip([self.p], max_norm=self.max_norm, grad_dtype=g.dtype)
         self.norm = self._clips[g.dtype]([g], stream=stream)
