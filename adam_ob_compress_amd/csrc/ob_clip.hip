@@ -146,6 +146,53 @@ __global__ __launch_bounds__(kNormBlock) void k_total_norm(NormTables t, double 
     if (tid == 0) norms[t.tensors] = norm_of<MAX>(all, g_mult);
 }
 
+// The norms of a short list in one launch: a wave for each tensor in turn.
+template <int G, bool MAX>
+__global__ __launch_bounds__(kNormBlock) void k_short_norms(ListLaunch L, NormPtrs ptrs, NormTables t, double g_mult, float* norms)
+{
+    constexpr int V = G == 0 ? 4 : 8, U = 4;   // elements of a load, loads in flight
+    __shared__ double lds[kNormBlock / 64];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+    double all = 0.0;
+    for (int64_t k = tid >> 6; k < t.tensors; k += kNormBlock / 64) {
+        const char* g = static_cast<const char*>(ptrs.g[k]);
+        double s[2] = {0.0, 0.0};
+        uint32_t m = 0;
+        if (g != nullptr && t.first[k] < t.first[k + 1]) {
+            const int n = L.items[t.first[k]].len;   // a short tensor is one item
+            for (int at = V * lane; at < n; at += 64 * V * U) {
+                u4e x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = at + 64 * V * u;
+                    x[u] = u4e{};
+                    if (i + V <= n) x[u] = *reinterpret_cast<const u4e*>(g + int64_t(i) * (16 / V));
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (MAX)
+                        m = max_bits<G>(x[u], m);
+                    else
+                        add_squares<G>(x[u], s);
+                }
+            }
+            const int rest = n / V * V + lane;   // less than a load's elements at the end
+            if (rest < n) {
+                const float e = load_grad1<G>(g, rest);
+                m = max_u(m, __float_as_uint(e) & 0x7fffffffu);
+                add_square(e, s[0]);
+            }
+        }
+        const double v = join_wave<MAX>(MAX ? static_cast<double>(__uint_as_float(m)) : s[0] + s[1]);
+        if (lane == 0) {
+            norms[t.order[k]] = norm_of<MAX>(v, g_mult);
+            all = join<MAX>(all, v);
+        }
+    }
+    all = join_block<MAX, kNormBlock / 64>(all, lds);
+    if (tid == 0) norms[t.tensors] = norm_of<MAX>(all, g_mult);
+}
+
 // Eight elements from element i on, widened, and back.
 template <int G>
 __device__ __forceinline__ void load8(const void* g, int64_t i, float x[8])
@@ -256,6 +303,17 @@ hipError_t launch_item_norms(const ListLaunch& L, const NormPtrs& ptrs, int g_dt
                    : g_dtype == OB_F16 ? (max ? k_item_norms<2, true> : k_item_norms<2, false>)
                                        : (max ? k_item_norms<0, true> : k_item_norms<0, false>);
     hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(L.n_items)), dim3(kListBlock), 0, s, L, ptrs, nt_items, partials);
+    return hipGetLastError();
+}
+
+hipError_t launch_short_norms(const ListLaunch& L, const NormPtrs& ptrs, int g_dtype, int kind, const NormTables& t, double g_mult,
+                              float* norms, hipStream_t s)
+{
+    const bool max = kind == OB_NORM_MAX;
+    const auto k = g_dtype == OB_BF16  ? (max ? k_short_norms<1, true> : k_short_norms<1, false>)
+                   : g_dtype == OB_F16 ? (max ? k_short_norms<2, true> : k_short_norms<2, false>)
+                                       : (max ? k_short_norms<0, true> : k_short_norms<0, false>);
+    hipLaunchKernelGGL(k, dim3(1), dim3(kNormBlock), 0, s, L, ptrs, t, g_mult, norms);
     return hipGetLastError();
 }
 

@@ -4,6 +4,7 @@
 #include "ob_list_handle.h"
 
 static_assert(OB_F32 == 0 && OB_BF16 == 1 && OB_F16 == 2, "kernels are chosen by these numbers");
+static_assert(ob::kShortElems <= ob::kNormElems, "a tensor of a short list is one item");
 
 extern "C" {
 
@@ -26,6 +27,21 @@ try {
     const ob::NormTables tables{l.d_norm_first, l.d_order, static_cast<int64_t>(l.shape.size.size()), l.norm.first.back(),
                                 static_cast<double*>(workspace)};
     ob::NormPtrs ptrs;
+    bool brief = tables.tensors > 0 && tables.tensors <= ob::kShortTensors;
+    int64_t total = 0;
+    for (size_t t = 0; brief && t < l.shape.size.size(); ++t) {
+        total += l.shape.size[t];
+        brief = l.shape.size[t] <= ob::kShortElems && total <= ob::kShortTotal && l.shape.g_dtype[t] == l.shape.g_dtype[0];
+    }
+    if (brief) {
+        for (int64_t k = 0; k < tables.tensors; ++k) {
+            const int32_t t = l.shape.order[k];
+            ptrs.g[k] = l.shape.size[t] > 0 ? g[t] : nullptr;
+        }
+        const ob::ListLaunch L{l.norm.d_items, l.d_tensors, tables.items, 0};
+        (void)hipGetLastError();
+        return ob::launch_short_norms(L, ptrs, l.shape.g_dtype[0], kind, tables, g_mult, norms, stream) == hipSuccess ? OB_OK : OB_ERR_HIP;
+    }
     const ob_status st = ob::for_runs(l.shape, ob::kNormPtrs, false, [&](int64_t k, int64_t e) {
         const int gd = l.shape.g_dtype[l.shape.order[k]];
         const int64_t items = l.norm.first[e] - l.norm.first[k], bytes = ob::kNormElems * ob::dtype_bytes(gd);

@@ -38,7 +38,7 @@ def factor(norm, max_norm, mult):
     return mult * (min(1.0, max_norm / (norm + 1e-6)) if 0 < max_norm < math.inf else 1.0)
 
 
-SIZES = [[1], [5, 1, 7], [20_011, 3, 4096, 1025], [300_007, 16384, 16385, 2], [70_000] * 70, [3] * 500]
+SIZES = [[1], [5, 1, 7], [4096, 1, 4095, 1023] * 5, [4097, 5], [1030] * 32, [9] * 33, [20_011, 3, 4096, 1025], [300_007, 16384, 16385, 2], [70_000] * 70, [3] * 500]
 
 
 @pytest.mark.parametrize("kind", ["2", "max"])
