@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ob_product.h"
+
 namespace ob {
 namespace {
 
@@ -62,7 +64,7 @@ struct Stage {
     }
 
     u4v reg[ASYNC ? 1 : kLoads];
-    uint32_t off[ASYNC ? kLoads : 1];         // ASYNC: byte offsets of the thread's chunks from the step's first byte
+    uint32_t off[ASYNC ? kLoads : 1];         // ASYNC: byte offsets of the thread's chunks from the step's first byte (product_reach())
     const uint16_t* at[ASYNC ? 1 : kLoads];   // else their addresses
 
     // place of the thread's chunk j: line and chunk in it
@@ -174,6 +176,7 @@ struct TileProduct {
     static constexpr int kFm = WM / kMfma, kFn = WN / kMfma;
     static constexpr bool kTurns = kThreads == 512;   // see run_in_turns
     static constexpr int kStages = kTurns ? 4 : 2, kTileK = kTurns ? 32 : 64;
+    static_assert(kTileK <= kTileStep && TM <= 256 && TN <= 256, "product_reach() is about such steps");
     using SL = Stage<TM, kTileK, kThreads, L_KMAJOR, ASYNC>;
     using SR = Stage<TN, kTileK, kThreads, R_KMAJOR, ASYNC>;
     static constexpr int kStage = SL::kBytes + SR::kBytes;

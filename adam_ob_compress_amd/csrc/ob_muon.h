@@ -121,6 +121,14 @@ inline int64_t muon_tile_count(const MuonMatrix& m, int product, int64_t size)
     return product == MUON_STEP ? product_tiles(m.r, m.k, size, false) : product_tiles(m.r, m.r, size, true);
 }
 
+// Whether a tile of this side can load what the product has of the matrix (with a side of many millions it may not).
+inline bool muon_reach(const MuonMatrix& m, int product, int64_t size)
+{
+    const int64_t lines = std::min<int64_t>(size, m.r);
+    if (product == MUON_GRAM) return product_reach(lines, m.k);
+    return product_reach(lines, m.r) && (product != MUON_STEP || product_reach(std::min<int64_t>(kTileStep, m.r), m.k));
+}
+
 // Tiles of all matrices [m0, m1) for `product`, ordered for a launch: work groups go around the eight XCDs, each of which
 // gets one part of every matrix, in panels of eight rows of tiles (those below the diagonal row by row).
 inline void muon_tiles(const std::vector<MuonMatrix>& mats, int64_t m0, int64_t m1, int product, int64_t size, std::vector<MuonTile>& out)
@@ -206,14 +214,16 @@ inline bool muon_close(MuonShape& s, int64_t m0, int64_t place0, int64_t places)
         for (int t = 0; t < kTileSizes; ++t) {
             int64_t n = 0;
             double k_sum = 0.0;   // over the tiles
+            bool reach = true;
             for (int64_t q = m0; q < m1; ++q) {
                 const MuonMatrix& m = s.matrices[q];
+                reach = reach && muon_reach(m, product, kTileSize[t]);
                 const int64_t tiles = muon_tile_count(m, product, kTileSize[t]);
                 n += tiles;
                 k_sum += static_cast<double>(tiles) * (product == MUON_GRAM ? m.k : m.r);
             }
             const double us = tile_round(t, n, k_sum / static_cast<double>(n));
-            if (n > INT32_MAX / 512 || (least >= 0.0 && us >= least)) continue;
+            if (!reach || n > INT32_MAX / 512 || (least >= 0.0 && us >= least)) continue;
             least = us;
             count = n;
             g.tile[product] = t;

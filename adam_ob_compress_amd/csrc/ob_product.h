@@ -80,6 +80,13 @@ inline bool product_chunks(const ProductOperand& o, const void* p, int64_t batch
            (batch <= 1 || batch_stride % 8 == 0);
 }
 
+// k that a tile takes in a step at most; its loads have byte offsets of 32 bits from the step's first element, and one that ends
+// behind 2^31 - 1 gives zeros.
+constexpr int64_t kTileStep = 64;
+// Whether the loads of `lines` lines (rows of an operand by K, k of one by rows), ld elements apart, stay within that; up to 256 elements
+// of a line are taken.
+inline bool product_reach(int64_t lines, int64_t ld) { return lines <= 1 || ld <= ((int64_t(1) << 30) - 1 - 256) / (lines - 1); }
+
 // The tiles of a product: rows and columns of tiles, all of them or those with a part below the diagonal.
 inline int64_t product_tiles(int64_t m, int64_t n, int64_t tile, bool symmetric)
 {

@@ -520,8 +520,9 @@ ob_status ob_matmul(const ob_product* product, hipStream_t stream);
  * master.  control with skip set: nothing changes.
  *
  * The plan holds the matrices' shapes for a list: tensor t has sizes[t] = E * rows[t] * cols[t] elements, E >= 0 matrices behind
- * each other, each by rows.  rows, cols: T host int64, 1 to 2^30.  It belongs to the list's device, copies what it needs of
- * the list, and owns its device tables.
+ * each other, each by rows.  rows, cols: T host int64, 1 to 2^30, and of a matrix that is not small, with its sides s <= l rounded up
+ * to 8, (min(s, 64) - 1) l + 256 below 2^30 (64 rows of 17 million, 8 of 153 million: OB_ERR_ARG beyond).  It belongs to the list's
+ * device, copies what it needs of the list, and owns its device tables.
  * m, master: flat, ob_tensors_state_elems(list) fp32 in the list's layout; g, p, master otherwise as in ob_adamw_step.
  * workspace: ob_muon_workspace(plan) bytes of device memory, 16-byte aligned, of any content (NULL where that is 0: small matrices
  * need none); calls that may overlap (other streams, captured graphs replayed at once) need their own.
