@@ -691,13 +691,15 @@ def ob_state8_decode(m_codes, m_scales, v_codes, v_scales, m, v, stream=None):
 # ---- norms of many tensors, and clipped gradients ----
 
 def _workspace(workspace, nbytes, device, stream):
-    """The caller's workspace, or a new one that is kept until the call's work is done."""
+    """The caller's workspace, or a new one: of the stream that the call is enqueued on, behind what its memory was used for."""
     if workspace is not None:
         return workspace
-    w = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device))
-    return w
+    if stream is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
 def _fail_workspace(tensors, workspace, nbytes, code, place):
