@@ -64,6 +64,8 @@ class OneBitAdam:
         self.step_index = 0
         self.dense_steps = 0
         self.max_norm, self._clips, self.norm = max_norm, {}, None
+        if max_norm is not None:   # a list of one tensor for each type that gradients come in
+            self._clips = {d: GradClip([p], max_norm=max_norm, grad_dtype=d) for d in (torch.float32, torch.bfloat16)}
         self.err_sumsq = self.plus_count = None
         if diagnostics:
             self.err_sumsq = torch.zeros(plan.num_chunks, dtype=torch.float64, device=dev)
@@ -90,8 +92,7 @@ class OneBitAdam:
 
     def _clip(self, g, stream):
         nat._gdtype(g)   # what the step would refuse is not clipped
-        if g.dtype not in self._clips:   # a list of one tensor for each type that gradients come in
-            self._clips[g.dtype] = GradClip([self.p], max_norm=self.max_norm, grad_dtype=g.dtype)
+        nat._want(g, "g", g.dtype, self.plan.n)
         self.norm = self._clips[g.dtype]([g], stream=stream)
 
     def small_error_chunks(self, threshold: float = 1e-6) -> list[int]:
