@@ -15,6 +15,7 @@ from ._native import (  # noqa: F401
     ob_adam_worker_update,
     ob_hparams, ob_lamb_compress_step, ob_lamb_worker_update,
     ob_lamb_warmup_step, ob_pack, ob_plan_create, ob_plan_read_timing, ob_plan_set_diagnostics,
+    ob_plan_set_guard,
     ob_plan_set_timing,
     ob_server_reduce, ob_status_str, ob_unpack,
     OB_CONTROL_BYTES, OB_STATE_BLOCK, Tensors, adamw_hparams, control_create, control_fields, ob_adamw8_step,

@@ -129,6 +129,7 @@ def lib() -> ctypes.CDLL:
         "ob_status_str": (ctypes.c_char_p, [I32]),
         "ob_plan_set_timing": (I32, [P, I32]),
         "ob_plan_set_diagnostics": (I32, [P, P, P]),
+        "ob_plan_set_guard": (I32, [P, P]),
         "ob_plan_read_timing": (I32, [P, I32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(I64)]),
         "ob_tensors_create": (I32, [I64, P, P, P, P, P, ctypes.POINTER(P)]),
         "ob_tensors_destroy": (I32, [P]),
@@ -436,6 +437,12 @@ def ob_plan_set_diagnostics(plan: Plan, err_sumsq=None, plus_count=None):
     _want(plus_count, "plus_count", torch.int64, plan.num_chunks)
     _check(lib().ob_plan_set_diagnostics(plan.handle, _dev(err_sumsq, "err_sumsq"),
                                          _dev(plus_count, "plus_count")), "ob_plan_set_diagnostics")
+
+
+def ob_plan_set_guard(plan: Plan, norm=None):
+    """Leave out later steps that find norm (one fp32 element) not finite when they run on the GPU; None: leave out none."""
+    _want(norm, "norm", torch.float32, 1)
+    _check(lib().ob_plan_set_guard(plan.handle, _dev(norm, "norm")), "ob_plan_set_guard")
 
 
 def ob_plan_set_timing(plan: Plan, enable: bool):

@@ -39,6 +39,8 @@ struct ob_plan_s {
     double* diag_err_sumsq = nullptr;
     unsigned long long* diag_plus = nullptr;
 
+    const float* guard = nullptr;      // ob_plan_set_guard
+
     // Chunk groups of the compressed step's two passes.  Pass 2 re-reads g and err, which pass 1 has
     // just read; run over consecutive chunks whose pass-1 bytes about fit in the GPU's last-level cache
     // (the Infinity Cache, 256 MB on MI355X), pass 1 then pass 2 per group serves most of that re-read
@@ -88,6 +90,14 @@ struct ob_plan_s {
         pd.n_items = t[table].n_items;
         pd.K = K;
         pd.item0 = 0;
+        pd.guard = nullptr;
+        return pd;
+    }
+    // The same for a launch of a step that the guard may leave out.
+    ob::PlanDev guarded(int table) const
+    {
+        ob::PlanDev pd = dev(table);
+        pd.guard = guard;
         return pd;
     }
 };
@@ -508,7 +518,7 @@ try {
     const ob::DenseParams dp = dense_params(hp);
     DeviceGuard guard(plan->device);
     if (!guard.ok) return OB_ERR_HIP;
-    const ob::PlanDev pd = plan->dev(T_DENSE);
+    const ob::PlanDev pd = plan->guarded(T_DENSE);
     const int bf = g_dtype == OB_BF16;
     return timed(plan, OB_KERNEL_DENSE, stream,
                  [&] { return ob::launch_dense(pd, g, bf, m, v, p, 0, dp, stream); });
@@ -636,6 +646,7 @@ ob_status compress_passes(ob_plan plan, const void* g, ob_dtype g_dtype, void* e
             &chain);
         if (st != OB_OK) return st;
         if ((st = pass2_view(plan, T_COMPRESS, stream, &pd, &chain)) != OB_OK) return st;
+        pd.guard = plan->guard;
         st = timed(
             plan, OB_KERNEL_COMPRESS, stream,
             [&] {
@@ -646,7 +657,7 @@ ob_status compress_passes(ob_plan plan, const void* g, ob_dtype g_dtype, void* e
         if (st != OB_OK) return st;
     }
     if (!plan->diag_err_sumsq) return st;
-    const ob::PlanDev pdd = plan->dev(T_COMPRESS);   // the pass-1 table the error sums were written by
+    const ob::PlanDev pdd = plan->guarded(T_COMPRESS);   // the pass-1 table the error sums were written by
     return timed(plan, OB_KERNEL_DIAG, stream, [&] {
         return ob::launch_diag_reduce(pdd, plan->diag_err_sumsq, plan->diag_plus, stream);
     });
@@ -663,17 +674,20 @@ ob::LambParams lamb_params(const ob_hparams* hp, double bc1, double bc2)
 }
 
 // Trust ratios of every layer from the per-block sums (tables w_table / u_table), then the update on
-// the dense block table.
+// the dense block table.  guard: of the step that they belong to.
 ob_status lamb_finish(ob_plan plan, int w_table, int u_table, const float* m, const float* v, float* p,
-                      float* ratios_out, int bias_correction, const ob::LambParams& lp, hipStream_t stream)
+                      float* ratios_out, int bias_correction, const ob::LambParams& lp, const float* guard,
+                      hipStream_t stream)
 {
     ob::PlanDev pr = plan->dev(T_DENSE);
+    pr.guard = guard;
     pr.w_first = plan->t[w_table].d_first;
     pr.u_first = plan->t[u_table].d_first;
     ob_status st = timed(plan, OB_KERNEL_TRUST_RATIO, stream,
                          [&] { return ob::launch_trust_ratio(pr, ratios_out, stream); });
     if (st != OB_OK) return st;
-    const ob::PlanDev pa = plan->dev(T_DENSE);
+    ob::PlanDev pa = plan->dev(T_DENSE);
+    pa.guard = guard;
     return timed(plan, OB_KERNEL_LAMB_APPLY, stream, [&] {
         return ob::launch_lamb_apply(pa, m, v, p, ratios_out, bias_correction, lp, stream);
     });
@@ -788,7 +802,8 @@ try {
     ob_status st = timed(plan, OB_KERNEL_WORKER_UPDATE, stream,
                          [&] { return ob::launch_worker_update(pd, words, scales, m, v, p, 1, cp, stream); });
     if (st != OB_OK) return st;
-    return lamb_finish(plan, T_COMPRESS, T_COMPRESS, m, v, p, ratios_out, 0, lamb_params(hp, 1.0, 1.0), stream);
+    return lamb_finish(plan, T_COMPRESS, T_COMPRESS, m, v, p, ratios_out, 0, lamb_params(hp, 1.0, 1.0), nullptr,
+                       stream);
 } catch (...) {
     return OB_ERR_OOM;  // host allocation failures are the only exceptions here
 }
@@ -805,7 +820,8 @@ try {
     if (st != OB_OK || plan->n == 0) return st;
     DeviceGuard guard(plan->device);
     if (!guard.ok) return OB_ERR_HIP;
-    return lamb_finish(plan, T_PASS1, T_COMPRESS, m, v, p, ratios_out, 0, lamb_params(hp, 1.0, 1.0), stream);
+    return lamb_finish(plan, T_PASS1, T_COMPRESS, m, v, p, ratios_out, 0, lamb_params(hp, 1.0, 1.0), plan->guard,
+                       stream);
 } catch (...) {
     return OB_ERR_OOM;  // host allocation failures are the only exceptions here
 }
@@ -824,13 +840,13 @@ try {
     const ob::DenseParams dp = dense_params(hp);
     DeviceGuard guard(plan->device);
     if (!guard.ok) return OB_ERR_HIP;
-    const ob::PlanDev pd = plan->dev(T_DENSE);
+    const ob::PlanDev pd = plan->guarded(T_DENSE);
     const int bf = g_dtype == OB_BF16;
     ob_status st = timed(plan, OB_KERNEL_DENSE, stream,
                          [&] { return ob::launch_dense(pd, g, bf, m, v, p, 1, dp, stream); });
     if (st != OB_OK) return st;
     return lamb_finish(plan, T_DENSE, T_DENSE, m, v, p, ratios_out, dp.bias_correction,
-                       lamb_params(hp, dp.bc1, dp.bc2), stream);
+                       lamb_params(hp, dp.bc1, dp.bc2), plan->guard, stream);
 } catch (...) {
     return OB_ERR_OOM;  // host allocation failures are the only exceptions here
 }
@@ -1010,6 +1026,14 @@ try {
     return OB_OK;
 } catch (...) {
     return OB_ERR_OOM;  // host allocation failures are the only exceptions here
+}
+
+ob_status ob_plan_set_guard(ob_plan plan, const float* norm)
+{
+    if (!plan) return OB_ERR_ARG;
+    if (!aligned(norm, 4)) return OB_ERR_ALIGN;
+    plan->guard = norm;
+    return OB_OK;
 }
 
 ob_status ob_plan_set_diagnostics(ob_plan plan, double* err_sumsq_out, uint64_t* plus_count_out)

@@ -12,6 +12,8 @@ namespace {
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u2 __attribute__((ext_vector_type(2)));
 
+// Whether the launch's step is left out: the same in all its threads, so that a kernel may return before its barriers.
+__device__ __forceinline__ bool left_out(const PlanDev& pd) { return pd.guard != nullptr && !__builtin_isfinite(*pd.guard); }
 
 // Tuning knobs (compile-time; every setting computes the same results):
 //   OB_P1_UNROLL / OB_P2_UNROLL   tiles in flight per loop trip in pass 1 / pass 2

@@ -45,6 +45,7 @@ struct PlanDev {
     // partials arrays.  Non-zero only for the chunk-group launches of the compressed step's two passes
     // (k_chunk_sumsq, k_compress, k_worker_compress); every other kernel takes 0.
     int32_t item0;
+    const float* guard;         // nullptr: none; else a step that finds it not finite writes nothing
 };
 
 struct CompressParams {

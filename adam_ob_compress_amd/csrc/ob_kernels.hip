@@ -51,6 +51,7 @@ __global__ __launch_bounds__(kBlock) void k_dense(PlanDev pd, const typename G::
                                                   float* __restrict__ m, float* __restrict__ v,
                                                   float* __restrict__ p, DenseParams dp)
 {
+    if (left_out(pd)) return;
     const Item it = pd.items[blockIdx.x];
     const int tid = threadIdx.x;
     double wsq = 0.0, usq = 0.0;
@@ -145,6 +146,7 @@ __global__ __launch_bounds__(kBlock) void k_chunk_sums(PlanDev pd, double* __res
 __global__ __launch_bounds__(kBlock) void k_trust_ratio(PlanDev pd, float* __restrict__ ratios)
 {
     __shared__ double lds[kBlock / 64];
+    if (left_out(pd)) return;
     const int c = blockIdx.x;
     const int tid = threadIdx.x;
     double sw = 0.0, su = 0.0;
@@ -164,6 +166,7 @@ __global__ __launch_bounds__(kBlock) void k_diag_reduce(PlanDev pd, double* __re
                                                         unsigned long long* __restrict__ plus_count)
 {
     __shared__ double lds[kBlock / 64];
+    if (left_out(pd)) return;
     const int c = blockIdx.x;
     const int tid = threadIdx.x;
     double se = 0.0;
@@ -197,6 +200,7 @@ __global__ __launch_bounds__(kBlock) void k_lamb_apply(PlanDev pd, const float* 
                                                        const float* __restrict__ v, float* __restrict__ p,
                                                        const float* __restrict__ ratios, LambParams lp)
 {
+    if (left_out(pd)) return;
     const Item it = pd.items[blockIdx.x];
     const int tid = threadIdx.x;
     const double r = static_cast<double>(ratios[it.chunk]);

@@ -39,8 +39,10 @@ class OneBitAdam:
     error buffer it read (``err_sumsq``) and its number of +1 signs (``plus_count``) ([P1] sec. 6.2
     and 8); ``small_error_chunks`` applies the tutorial's warning threshold to them.
 
-    ``max_norm=...`` clips every step's gradient by its global norm first, in place in ``g`` (a norm that is not finite
-    makes it NaN); the norm of the last step is in ``self.norm`` (one element on the GPU).
+    ``max_norm=...`` clips every step's gradient by its norm first, in place in ``g``; the norm of the last step is in
+    ``self.norm`` (one element on the GPU).  A norm that is not finite makes ``g`` NaN, and the step is left out on the GPU: the
+    states, parameters and outputs (``self.words`` among them) stay those of the step before.  What the host counts (the
+    schedule, the step of the bias correction) goes on.
     """
 
     def __init__(self, plan: nat.Plan, err, m, v, p, *, lr, beta1=0.9, beta2=0.999, eps=1e-8,
@@ -76,9 +78,17 @@ class OneBitAdam:
         return step_kind(self.step_index, self.freeze_step, self.refresh_period)
 
     def step(self, g, stream=None) -> str:
+        if self.max_norm is None:
+            return self._step(g, stream)
+        self._clip(g, stream)
+        nat.ob_plan_set_guard(self.plan, self.norm)
+        try:
+            return self._step(g, stream)
+        finally:
+            nat.ob_plan_set_guard(self.plan, None)   # the plan's other calls are none of this norm's
+
+    def _step(self, g, stream) -> str:
         kind = self.kind()
-        if self.max_norm is not None:
-            self._clip(g, stream)
         if kind == "dense":
             self.dense_steps += 1
             self.hp.bias_correction = 1 if self.bias_correction else 0

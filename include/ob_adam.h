@@ -294,6 +294,14 @@ ob_status ob_plan_read_timing(ob_plan plan, int32_t kernel, double* total_ms, in
  * switches them off; exactly one NULL is OB_ERR_ARG. */
 ob_status ob_plan_set_diagnostics(ob_plan plan, double* err_sumsq_out, uint64_t* plus_count_out);
 
+/* ---- steps that a norm leaves out ----
+ * For gradients clipped by their norm (ob_tensor_norms, ob_clip_grads), which are NaN if it is not finite.  With norm set (one fp32 in
+ * device memory, 4-byte aligned), a step that is made with this plan afterwards (ob_adam_warmup_step, ob_adam_compress_step,
+ * ob_lamb_warmup_step, ob_lamb_compress_step) reads it on the GPU; if it is not finite then, the step writes nothing: no state, no
+ * parameter and none of its outputs, diagnostics among them.  NULL (as after ob_plan_create): every step is made.  The worker's and
+ * the server's calls, whose outputs are exchanged, do not look at it.  A captured step keeps the address, and looks at every replay. */
+ob_status ob_plan_set_guard(ob_plan plan, const float* norm);
+
 /* ---- AdamW over many tensors at once ----
  * For models whose parameters are separate tensors (or views into buckets) rather than one flat buffer:
  * the dense Adam step of ob_adam_warmup_step with decoupled weight decay, per-tensor rates, parameters

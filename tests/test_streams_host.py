@@ -51,6 +51,8 @@ def test_one_bit_steps_make_their_clips_before_the_first_step(monkeypatch):
     monkeypatch.setattr(schedule, "GradClip", Clip)
     for name in ("ob_adam_warmup_step", "ob_adam_compress_step"):
         monkeypatch.setattr(nat, name, lambda *a: calls.append(a[-1]))
+    guards = []
+    monkeypatch.setattr(nat, "ob_plan_set_guard", lambda plan, norm: guards.append((norm is not None, len(calls))))
     opt = schedule.OneBitAdam(Plan(), *(torch.zeros(64) for _ in range(4)), lr=1.0, freeze_step=1, max_norm=2.0)
     assert sorted(made, key=str) == [(64, 2.0, torch.bfloat16), (64, 2.0, torch.float32)]
     s = Stream()
@@ -58,6 +60,8 @@ def test_one_bit_steps_make_their_clips_before_the_first_step(monkeypatch):
         opt.step(torch.zeros(64, dtype=dtype), stream=s)
     assert len(made) == 2 and [c[0] for c in calls if isinstance(c, tuple)] == [torch.float32, torch.bfloat16]
     assert all(c[1] is s for c in calls if isinstance(c, tuple))
+    # each step looks at its norm, behind its clipping, and the plan's later calls at none
+    assert guards == [(True, 1), (False, 2), (True, 3), (False, 4)]
     for bad, error in ((torch.zeros(64, dtype=torch.float16), TypeError), (torch.zeros(32), ValueError)):
         before = len(calls)
         try:
@@ -66,6 +70,17 @@ def test_one_bit_steps_make_their_clips_before_the_first_step(monkeypatch):
             assert len(calls) == before   # what the step refuses is not clipped
         else:
             raise AssertionError("not refused")
+    monkeypatch.setattr(nat, "ob_adam_compress_step", lambda *a: 1 / 0)
+    guards.clear()
+    try:
+        opt.step(torch.zeros(64))
+    except ZeroDivisionError:
+        assert [g[0] for g in guards] == [True, False]
     made.clear()
     schedule.OneBitAdam(Plan(), *(torch.zeros(64) for _ in range(4)), lr=1.0)
     assert not made
+
+
+def test_guard_refusals():
+    lib = nat.lib()
+    assert lib.ob_plan_set_guard(None, None) == 1
