@@ -70,9 +70,6 @@ class ListOptimizer:
                 raise ValueError(f"parameter {j} is no leaf and has no .grad of its own: give the gradients to step")
         return [p.grad for p in self.params]
 
-    def _changed(self, grads):
-        torch.autograd.graph.increment_version([p for p, g in zip(self.params, grads) if g is not None])
-
     def _part(self, flat, t):
         """Tensor t's part of a flat state buffer, in the parameter's shape."""
         o, p = self.list.state_offset(t), self.params[t]
@@ -169,7 +166,6 @@ class AdamW(ListOptimizer):
             if self.control is None:
                 self.hp.step -= 1   # a refused step is not counted
             raise
-        self._changed(grads)
 
     def moments(self):
         """The flat moments (m, v) in fp32; with 8-bit states what the codes stand for, in new tensors."""

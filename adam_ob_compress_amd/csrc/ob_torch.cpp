@@ -13,6 +13,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <memory>
 #include <stdexcept>
 #include <string>
@@ -109,16 +110,39 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f)
     }
 }
 
-// The library's call, without the interpreter's lock (a launch may wait for room in its queue).
-template <class F>
-PyObject* status_of(F&& call)
+// The library's call, without the interpreter's lock (a launch may wait for room in its queue); written(): behind a call that
+// was not refused, tells torch which tensors it writes.
+template <class F, class W>
+PyObject* status_of(F&& call, W&& written)
 {
     if (PyErr_Occurred()) return nullptr;   // an address that was no number
     ob_status st;
     Py_BEGIN_ALLOW_THREADS;
     st = call();
     Py_END_ALLOW_THREADS;
+    if (st == OB_OK) written();
     return PyLong_FromLong(st);
+}
+template <class F>
+PyObject* status_of(F&& call)
+{
+    return status_of(call, [] {});
+}
+
+// Raises a tensor's version, so that autograd refuses a backward pass that needs its values from before.
+void raise_version(PyObject* item)
+{
+    const at::Tensor& t = THPVariable_Unpack(item);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();   // an inference tensor has none
+}
+// The same for the tensors of a list or tuple whose gradient is there.
+void raise_versions(PyObject* tensors, PyObject* grads)
+{
+    const Py_ssize_t T = std::min(PySequence_Fast_GET_SIZE(tensors), PySequence_Fast_GET_SIZE(grads));   // they may have changed meanwhile
+    for (Py_ssize_t j = 0; j < T; ++j) {
+        PyObject* t = PySequence_Fast_GET_ITEM(tensors, j);
+        if (PySequence_Fast_GET_ITEM(grads, j) != Py_None && THPVariable_Check(t)) raise_version(t);
+    }
 }
 
 hipStream_t stream_of(PyObject* s) { return static_cast<hipStream_t>(PyLong_AsVoidPtr(s)); }
@@ -206,11 +230,13 @@ PyObject* adamw_step(PyObject*, PyObject* const* args, Py_ssize_t n)
         for (int j = 0; j < 3; ++j) f[j] = static_cast<float*>(flat(args[5 + j], at::kFloat, l.state_elems, l.device, 2 + j));
         ob_control* ctl = control_of(args[8], l, 5);
         const Norm norm(args[9]);
-        return status_of([&] {
-            return norm.with(
-                l, g, hp, ctl, s, [&] { return ob_adamw_check(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl); },
-                [&] { return ob_adamw_step(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl, s); });
-        });
+        return status_of(
+            [&] {
+                return norm.with(
+                    l, g, hp, ctl, s, [&] { return ob_adamw_check(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl); },
+                    [&] { return ob_adamw_step(l.handle, g.data(), p.data(), f[0], f[1], f[2], hp, ctl, s); });
+            },
+            [&] { raise_versions(args[2], args[1]); });
     });
 }
 
@@ -231,11 +257,13 @@ PyObject* adamw8_step(PyObject*, PyObject* const* args, Py_ssize_t n)
         auto* vq = static_cast<float*>(flat(args[9], at::kFloat, B, l.device, 6));
         ob_control* ctl = control_of(args[10], l, 7);
         const Norm norm(args[11]);
-        return status_of([&] {
-            return norm.with(
-                l, g, hp, ctl, s, [&] { return ob_adamw8_check(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl); },
-                [&] { return ob_adamw8_step(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl, s); });
-        });
+        return status_of(
+            [&] {
+                return norm.with(
+                    l, g, hp, ctl, s, [&] { return ob_adamw8_check(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl); },
+                    [&] { return ob_adamw8_step(l.handle, g.data(), p.data(), master, mc, mq, vc, vq, hp, ctl, s); });
+            },
+            [&] { raise_versions(args[2], args[1]); });
     });
 }
 
@@ -280,7 +308,8 @@ PyObject* tensor_norms(PyObject*, PyObject* const* args, Py_ssize_t n)
         const float g_mult = static_cast<float>(PyFloat_AsDouble(args[5]));
         const auto kind = static_cast<int32_t>(PyLong_AsLong(args[6]));
         hipStream_t s = stream_of(args[7]);
-        return status_of([&] { return ob_tensor_norms(l.handle, g.data(), g_mult, kind, norms, work, s); });
+        return status_of([&] { return ob_tensor_norms(l.handle, g.data(), g_mult, kind, norms, work, s); },
+                         [&] { raise_version(args[2]); });
     });
 }
 
@@ -296,7 +325,8 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n)
         const float max_norm = static_cast<float>(PyFloat_AsDouble(args[4])), g_mult = static_cast<float>(PyFloat_AsDouble(args[5]));
         const int32_t each = PyObject_IsTrue(args[6]) == 1;
         hipStream_t s = stream_of(args[7]);
-        return status_of([&] { return ob_clip_grads(l.handle, g.data(), to ? out.data() : nullptr, norms, max_norm, g_mult, each, s); });
+        return status_of([&] { return ob_clip_grads(l.handle, g.data(), to ? out.data() : nullptr, norms, max_norm, g_mult, each, s); },
+                         [&] { raise_versions(to ? args[2] : args[1], args[1]); });
     });
 }
 
@@ -316,11 +346,13 @@ PyObject* muon_step(PyObject*, PyObject* const* args, Py_ssize_t n)
         ob_control* ctl = control_of(args[10], l, 5);
         const Norm norm(args[11]);
         ob_adamw_hparams count{};   // only counts the step
-        return status_of([&] {
-            return norm.with(
-                l, g, &count, ctl, s, [&] { return ob_muon_check(plan, g.data(), p.data(), master, m, work, hp, ctl); },
-                [&] { return ob_muon_step(plan, g.data(), p.data(), master, m, work, hp, ctl, s); });
-        });
+        return status_of(
+            [&] {
+                return norm.with(
+                    l, g, &count, ctl, s, [&] { return ob_muon_check(plan, g.data(), p.data(), master, m, work, hp, ctl); },
+                    [&] { return ob_muon_step(plan, g.data(), p.data(), master, m, work, hp, ctl, s); });
+            },
+            [&] { raise_versions(args[3], args[2]); });
     });
 }
 
@@ -420,7 +452,7 @@ PyObject* matmul(PyObject*, PyObject* const* args, Py_ssize_t n)
                 p.workspace = own.data_ptr();
             }
         }
-        return status_of([&] { return ob_matmul(&p, s); });
+        return status_of([&] { return ob_matmul(&p, s); }, [&] { raise_version(args[2]); });
     });
 }
 

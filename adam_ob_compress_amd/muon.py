@@ -63,7 +63,6 @@ class Muon(ListOptimizer):
             raise ValueError("a loss scale needs max_norm (inf: no clipping)")
         nat.ob_muon_step(self.plan, grads, self.params, self.m, self.hp, self.workspace, self.master, self.control, stream, norm)
         self._calls += 1
-        self._changed(grads)
 
     def state_dict(self) -> dict:
         """Step count and flat states (references), with max_norm also the factor of set_lr_scale and the count of steps
@@ -138,5 +137,4 @@ class GradClip:
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         nat.ob_tensor_norms(self.list, grads, self.norms, 1.0 / loss_scale, self.kind, self.workspace, stream)
         nat.ob_clip_grads(self.list, grads, self.norms, self.max_norm, 1.0 / loss_scale, None, self.per_tensor, stream)
-        torch.autograd.graph.increment_version([g for g in grads if g is not None])
         return self.norms[-1:]
