@@ -3,6 +3,8 @@
 #include <cstdio>
 #include <cstdlib>
 
+#include <vector>
+
 #include "ob_muon.h"
 
 static long checks = 0;
@@ -57,8 +59,37 @@ static ob_status plan(int64_t E, int64_t rows, int64_t cols, int64_t* tile = nul
     return OB_OK;
 }
 
+struct Mat {
+    int64_t e, r, c;
+};
+
+// The tiles of a list's only group.
+static void check_tiles(const std::vector<Mat>& mats, int64_t gram, int64_t poly, int64_t step)
+{
+    std::vector<int64_t> size, rows, cols;
+    for (const Mat& m : mats) {
+        size.push_back(m.e * m.r * m.c);
+        rows.push_back(m.r);
+        cols.push_back(m.c);
+    }
+    const std::vector<int32_t> type(mats.size(), OB_F32);
+    ob::ListShape l;
+    CHECK(ob::build_shape(static_cast<int64_t>(mats.size()), size.data(), type.data(), type.data(), nullptr, nullptr, l) == OB_OK);
+    ob::MuonShape s;
+    CHECK(ob::build_muon(l, nullptr, nullptr, rows.data(), cols.data(), 200, s) == OB_OK);
+    CHECK(s.groups.size() == 1);
+    const int64_t want[3] = {gram, poly, step};
+    for (int p = 0; p < 3; ++p) CHECK(ob::kTileSize[s.groups[0].tile[p]] == want[p]);
+}
+
 int main()
 {
+    // the lists of tests/test_gpu_muon_large.py take every tile
+    check_tiles({{2, 203, 300}, {1, 300, 203}, {1, 169, 178}, {1, 171, 169}}, 64, 64, 64);
+    check_tiles({{7, 521, 777}, {6, 777, 520}}, 64, 64, 128);
+    check_tiles({{100, 201, 203}, {103, 202, 197}}, 64, 64, 256);
+    check_tiles({{4, 1100, 1301}, {4, 1303, 1101}}, 128, 128, 256);
+    check_tiles({{32, 509, 1403}, {1, 1403, 510}, {31, 1402, 507}}, 256, 256, 256);
     // inside the limit for every tile; what fits only smaller tiles takes those; on both sides of the limit for the smallest
     int64_t tile[3];
     CHECK(plan(1, 4096, 11008) == OB_OK);
