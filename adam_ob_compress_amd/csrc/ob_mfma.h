@@ -301,6 +301,7 @@ struct TileProduct {
         sr.load(ro, 0, lds + SL::kBytes);
         sl.store(lds);
         sr.store(lds + SL::kBytes);
+        if (ASYNC) wait_loads<0>();   // what other waves read behind the barrier has arrived
         __syncthreads();
         for (int t = 0; t < steps; ++t) {
             char* at = lds + (t & 1) * kStage;
@@ -318,6 +319,7 @@ struct TileProduct {
                 sl.store(to);
                 sr.store(to + SL::kBytes);
             }
+            if (ASYNC) wait_loads<0>();
             wait_reads();   // they have left the buffer that the next step's loads go into
             __syncthreads();
         }
