@@ -154,7 +154,10 @@ struct Stage {
         if constexpr (K_MAJOR) {
             return *reinterpret_cast<const s8v*>(at + (row0 + r) * (kLine * 16) + ((kk * 4 + g) ^ swizzle(r)) * 16);
         } else {
-            // 16 lanes read four k of 16 rows, four rows each, and get four k of one row
+            // 16 lanes read four k of 16 rows, four rows each, and get four k of one row.  The compiler takes the first of these reads
+            // for a possible reader of the loads into LDS that are on their way and waits for all of them (vmcnt(0)), which reads of
+            // operands by K do not make it do: on tiles of 128 and 64 a step's loads, issued just before, then overlap with nothing; on
+            // tiles of 256 the wait for the next step's alone is void.  1024^3 9.9 us by rows and 8.3 by K.
             const int k = kk * 32 + g * 8 + (r >> 2);
             const int c = ((row0 >> 3) + (r >> 1 & 1)) ^ swizzle(k);
             const char* p = at + k * (kLine * 16) + c * 16 + (r & 1) * 8;
@@ -232,6 +235,7 @@ struct TileProduct {
 
     // Bound by the power that the card may draw: 8192^3 fp16, both by K, 860 us (1278 TFLOP/s), 1.35e6 cycles at 1.58 GHz with the matrix cores
     // busy 77% of them; with all waves reading and multiplying together 1.70e6 cycles, 62%, at 1.96 GHz.  Operands of zeros: 1530 TFLOP/s.
+    // By rows also by the wait that Stage::fragment() describes: busy 65% (B by rows), 58% in the Muon step.
     // Two waves share a SIMD, one of each half of the group.  While one multiplies, the other takes its next fragments from LDS and
     // starts loads, and a barrier changes their roles, so that the matrix cores have one wave's work at any time.  With the halves'
     // phases counted through, the first half takes step s in phase 2s and multiplies it in 2s + 1, the second takes it in 2s + 1:

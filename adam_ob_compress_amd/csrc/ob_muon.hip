@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kListBlock) void k_muon_factor(MuonCall c)
 }
 
 // A tile of X from g and m, smaller side first, zeros where the sides are rounded up.  A matrix with more rows than columns is
-// turned over in LDS.  u is formed again from g and m (its norm is known only now): 2.0e8 elements 410 us, 3.9 TB/s, 3% of their step.
+// turned over in LDS.  u is formed again from g and m (its norm is known only now): 2.0e8 elements 438 us, 3.7 TB/s, 3% of their step.
 template <int G>
 __global__ __launch_bounds__(kListBlock) void k_muon_write(MuonCall c, ListPtrs ptrs)
 {
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kListBlock) void k_muon_write(MuonCall c, ListPtrs 
     const int tid = static_cast<int>(threadIdx.x), line = tid >> 4, q = (tid & 15) * 4;
     _Float16* x = reinterpret_cast<_Float16*>(c.half + mt.x[0]);
     const float* m = c.m + mt.state;
-    // Four lines of 16 for a thread, all loads before the first store (one line at a time: 4.0 TB/s).
+    // Four lines of 16 for a thread, all loads before the first store (64 experts of 512 x 1408 83 us; a line at a time 95).
     constexpr int kLines = T / 16;
     f4 gv[kLines], mv[kLines];
     const int col = col0 + q;
@@ -141,7 +141,8 @@ template <int TM, int WM, int WN, int PRODUCT>
 using MuonProduct = TileProduct<TM, TM, WM, WN, false, true, PRODUCT != MUON_STEP, true>;
 
 // One product of an iteration.  Seven matrices of 4096 x 4096 to 4096 x 11008: A 768 us, B 468, X 1506 (1100 TFLOP/s), bound by power and, in
-// the symmetric ones, by a last round that fills 72% of the card; 48 of 768 x 768: 50, 51 and 76 us, bound by the tiles' ends.
+// the symmetric ones, by a last round that fills 72% of the card, in X by a wait of the compiler's (Stage::fragment); 48 of 768 x 768: 50,
+// 51 and 76 us, bound by the tiles' ends, X by that wait too.
 template <int TM, int WM, int WN, int PRODUCT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TM / WN)) void k_muon_product(MuonCall c, const MuonTile* tiles, int turn)
 {

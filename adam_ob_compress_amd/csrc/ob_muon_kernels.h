@@ -25,7 +25,7 @@ struct MuonCall {
 hipError_t launch_muon_momentum(const MuonCall& c, const ListPtrs& ptrs, int g_dtype, int64_t items, hipStream_t s);
 hipError_t launch_muon_factor(const MuonCall& c, int64_t matrices, hipStream_t s);
 hipError_t launch_muon_write(const MuonCall& c, const ListPtrs& ptrs, int g_dtype, int64_t tiles, hipStream_t s);
-// One product of iteration `turn` (X is x[turn % 2]); tile: place in kMuonTiles.
+// One product of iteration `turn` (X is x[turn % 2]); tile: place in kTileSize.
 hipError_t launch_muon_product(const MuonCall& c, int product, const MuonTile* tiles, int64_t count, int tile, int turn, hipStream_t s);
 // The last MUON_STEP, whose result goes into the parameters of kind pk.
 hipError_t launch_muon_last(const MuonCall& c, const ListPtrs& ptrs, const MuonTile* tiles, int64_t count, int tile, int turn, int pk,

@@ -25,8 +25,9 @@ class Muon(ListOptimizer):
     captured too, and the count is of the calls of ``step()``.  Gradients that AdamW steps as well belong to one norm: give
     them all to GradClip first, and ``max_norm=inf`` to both optimizers if steps whose norm is not finite shall be left out.
 
-    The workspace (about 4 bytes per element of the matrices that go through the iterations together, at most about 2 GB for a list of
-    many) is kept with the optimizer, so its steps must not overlap each other.
+    The workspace (4 bytes per element and 4 r^2 per matrix, r the smaller side, so 8 bytes per element of a square one, for the matrices that
+    go through the iterations together: at most about 2 GB for a list of many) is kept with the optimizer, so its steps must not
+    overlap each other.
     """
 
     def __init__(self, params, *, lr=1e-3, momentum=0.95, weight_decay=0.1, max_norm=None, nesterov=True, iterations=5, eps=1e-7,
@@ -104,6 +105,9 @@ class Muon(ListOptimizer):
 class GradClip:
     """Clips the gradients of many tensors in place, by the norm of all or (``per_tensor``) each by its own; for gradients that
     more than one optimizer steps.
+
+    The norm is over the gradients given, on this GPU.  Where workers hold parts of them (sharded gradients), ob_tensor_norms and
+    ob_clip_grads are called in its place, with the norms joined over the workers between the two.
 
     ``params``: the tensors whose ``.grad`` is clipped (contiguous, on one GPU), each once.  ``norm``: "2" or "max".  Everything
     is enqueued on the current stream and nothing waits for the GPU, so a call can be captured.  A norm that is not finite makes

@@ -39,8 +39,8 @@ class OneBitAdam:
     error buffer it read (``err_sumsq``) and its number of +1 signs (``plus_count``) ([P1] sec. 6.2
     and 8); ``small_error_chunks`` applies the tutorial's warning threshold to them.
 
-    ``max_norm=...`` clips every step's gradient by its norm first, in place in ``g``; the norm of the last step is in
-    ``self.norm`` (one element on the GPU).  A norm that is not finite makes ``g`` NaN, and the step is left out on the GPU: the
+    ``max_norm=...`` clips every step's gradient by its norm (of ``g`` alone, whatever other workers have) first, in place in
+    ``g``; the norm of the last step is in ``self.norm`` (one element on the GPU).  A norm that is not finite makes ``g`` NaN, and the step is left out on the GPU: the
     states, parameters and outputs (``self.words`` among them) stay those of the step before.  What the host counts (the
     schedule, the step of the bias correction) goes on.
     """
