@@ -44,6 +44,7 @@ inline ob_status check_product(const ob_product* p)
             !product_stride(p->k, p->b_row) || !product_stride(p->n, p->b_col) || !product_stride(p->batch, p->b_batch))
             return OB_ERR_ARG;
         if (!product_aligned(p->a, 2) || !product_aligned(p->b, 2)) return OB_ERR_ALIGN;
+        if (p->d == p->a || p->d == p->b) return OB_ERR_ARG;   // work groups still read what others have written
     }
     if (!product_stride(p->m, p->d_row) || !product_stride(p->batch, p->d_batch)) return OB_ERR_ARG;
     // D's elements must not overlap

@@ -106,8 +106,9 @@ class GradClip:
     """Clips the gradients of many tensors in place, by the norm of all or (``per_tensor``) each by its own; for gradients that
     more than one optimizer steps.
 
-    The norm is over the gradients given, on this GPU.  Where workers hold parts of them (sharded gradients), ob_tensor_norms and
-    ob_clip_grads are called in its place, with the norms joined over the workers between the two.
+    The workspace and the norms are kept with it, so its calls must not overlap each other.  The norm is over the gradients
+    given, on this GPU.  Where workers hold parts of them (sharded gradients), ob_tensor_norms and ob_clip_grads are called in its
+    place, with the norms joined over the workers between the two.
 
     ``params``: the tensors whose ``.grad`` is clipped (contiguous, on one GPU), each once.  ``norm``: "2" or "max".  Everything
     is enqueued on the current stream and nothing waits for the GPU, so a call can be captured.  A norm that is not finite makes

@@ -482,7 +482,8 @@ ob_status ob_clip_grads(ob_tensors list, const void* const* g, void* const* out,
  *   k = 0     the sums are 0
  *   symmetric 1: m = n, and the caller knows that A B is symmetric (B = A^T, or powers of one symmetric matrix) and
  *             C is: what is below the diagonal is computed, and written above it too.
- * D may be C itself (same pointer and strides) and overlaps nothing else.  Zero extents give no work.
+ * D may be C itself (same pointer and strides) and overlaps nothing else (OB_ERR_ARG where it starts at A or B).  Zero extents give
+ * no work.
  * Extents are at most 2^31 - 1 - 256, offsets within a matrix and a batch below 2^60 elements; OB_ERR_ARG beyond.
  * workspace: ob_matmul_workspace(product) bytes of device memory, 16-byte aligned, of any content, or NULL: with it, tiles that
  * would not fill the card are shared by several work groups, which add their parts of K; calls that may overlap need their own.
@@ -530,7 +531,7 @@ ob_status ob_matmul(const ob_product* product, hipStream_t stream);
  * The plan holds the matrices' shapes for a list: tensor t has sizes[t] = E * rows[t] * cols[t] elements, E >= 0 matrices behind
  * each other, each by rows.  rows, cols: T host int64, 1 to 2^30, and of a matrix that is not small, with its sides s <= l rounded up
  * to 8, (min(s, 64) - 1) l + 256 below 2^30 (64 rows of 17 million, 8 of 153 million: OB_ERR_ARG beyond).  It belongs to the list's
- * device, copies what it needs of the list, and owns its device tables.
+ * device, copies what it needs of the list, and owns its device tables; it must outlive a captured step.
  * m, master: flat, ob_tensors_state_elems(list) fp32 in the list's layout; g, p, master otherwise as in ob_adamw_step.
  * workspace: ob_muon_workspace(plan) bytes of device memory, 16-byte aligned, of any content (NULL where that is 0: small matrices
  * need none); calls that may overlap (other streams, captured graphs replayed at once) need their own.
